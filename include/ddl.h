@@ -61,7 +61,9 @@ extern "C" {
 /* Largest P a plan accepts (the rank pointers travel as kernel arguments). */
 #define DDL_MAX_RANKS 128
 
-typedef enum { DDL_F32 = 0, DDL_F16 = 1 } ddl_dtype;
+/* Gradients are exchanged in DDL_F32 or DDL_F16; DDL_BF16 (bfloat16) is a type
+ * of the linear layer and of the optimizers' gradients and copies. */
+typedef enum { DDL_F32 = 0, DDL_F16 = 1, DDL_BF16 = 2 } ddl_dtype;
 typedef enum { DDL_SUM = 0, DDL_MEAN = 1 } ddl_op;
 typedef enum { DDL_RING = 0, DDL_MULTIRING = 1, DDL_TORUS2D = 2 } ddl_topo_kind;
 
@@ -446,6 +448,168 @@ typedef enum {
 } ddl_tune_knob;
 int ddl_set_tuning(int knob, int value);
 int ddl_get_tuning(int knob, int *value);
+
+/* ---- the linear layer ---------------------------------------------------- *
+ * The products whose gradients the all-reduce carries, for x m x k, weights w
+ * n x k (as most frameworks keep them), all row-major, in DDL_F16 or DDL_BF16:
+ *
+ *   ddl_linear        z = x w^T + bias,   y = act(z) + residual       (m x n)
+ *   ddl_linear_dgrad  dx = dz w + residual,                           (m x k)
+ *                     dz_prev = dx * act'(z_prev)
+ *   ddl_linear_wgrad  dw = dz^T x  (n x k),  db = column sums of dz   (n)
+ *
+ * Sums, bias, activation and residual are held in binary32 and every output
+ * is rounded once (dz_prev is computed from the unrounded dx).
+ *
+ * ld* are the elements from row to row: at least the row's length (any value
+ * for a single row).  Any alignment of a whole element is taken; rows that
+ * all start on 16-byte boundaries with lengths that are multiples of 8 are
+ * the fast case.  Columns, n, k and ld* up to 2^22, m up to 2^30.  Extents
+ * may be 0: an output without elements is left alone, an empty sum is 0.
+ * An output may be the very array given as residual or z_prev (same pointer
+ * and ld); any other overlap of an output with another argument is an error
+ * that is not detected.
+ *
+ * workspace: device memory, 16-byte aligned, of at least
+ * ddl_linear_workspace(op, m, n, k) bytes (NULL where that is 0), the call's
+ * own until the work is done.  Everything is enqueued on `stream` on the
+ * current device; no call allocates, synchronises or keeps state, so all of
+ * them can be captured into a HIP graph.
+ * Errors: DDL_E_NULL, DDL_E_ARG, DDL_E_ALIGN (an array not aligned to its
+ * element, or the workspace not to 16 bytes), DDL_E_SCRATCH (workspace too
+ * small), DDL_E_HIP. */
+typedef enum {
+    DDL_ACT_NONE = 0,
+    DDL_ACT_RELU = 1,
+    DDL_ACT_GELU = 2,      /* z Phi(z) */
+    DDL_ACT_GELU_TANH = 3, /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+    DDL_ACT_SILU = 4       /* z / (1 + exp(-z)) */
+} ddl_act;
+
+enum { DDL_LINEAR_FORWARD = 0, DDL_LINEAR_DGRAD = 1, DDL_LINEAR_WGRAD = 2 };
+
+typedef struct {
+    size_t m, n, k;
+    int dtype, act;
+    const void *x;        /* m x k */
+    size_t ldx;
+    const void *w;        /* n x k */
+    size_t ldw;
+    const void *bias;     /* NULL or n */
+    const void *residual; /* NULL or m x n, added after the activation */
+    size_t ldr;
+    void *y;              /* m x n */
+    size_t ldy;
+    void *z;              /* NULL or m x n: the activation's argument, for the
+                             backward pass */
+    size_t ldz;
+} ddl_linear_args;
+
+typedef struct {
+    size_t m, n, k;
+    int dtype, act;       /* act: of the layer before, whose z is z_prev */
+    const void *dz;       /* m x n */
+    size_t lddz;
+    const void *w;        /* n x k */
+    size_t ldw;
+    const void *residual; /* NULL or m x k: a skip connection's gradient */
+    size_t ldr;
+    void *dx;             /* m x k */
+    size_t lddx;
+    const void *z_prev;   /* m x k; both NULL only with DDL_ACT_NONE */
+    size_t ldz_prev;
+    void *dz_prev;        /* m x k */
+    size_t lddz_prev;
+} ddl_dgrad_args;
+
+typedef struct {
+    size_t m, n, k;
+    int dtype, out_dtype; /* out_dtype: DDL_F32 or dtype, of dw and db */
+    int accumulate;       /* 1: dw and db are added to */
+    const void *dz;       /* m x n */
+    size_t lddz;
+    const void *x;        /* m x k */
+    size_t ldx;
+    void *dw;             /* n x k */
+    size_t lddw;
+    void *db;             /* NULL or n */
+} ddl_wgrad_args;
+
+int ddl_linear_workspace(int op, size_t m, size_t n, size_t k, size_t *bytes);
+int ddl_linear(const ddl_linear_args *args, void *workspace, size_t workspace_bytes,
+               void *stream);
+int ddl_linear_dgrad(const ddl_dgrad_args *args, void *workspace, size_t workspace_bytes,
+                     void *stream);
+int ddl_linear_wgrad(const ddl_wgrad_args *args, void *workspace, size_t workspace_bytes,
+                     void *stream);
+
+/* ---- optimizers ---------------------------------------------------------- *
+ * The steps that follow the all-reduce where plain SGD and LARS do not: Muon
+ * for the matrices of a flat parameter buffer, AdamW for the rest of it.
+ * Both take the reduced gradient (DDL_F32, DDL_F16 or DDL_BF16), keep
+ * binary32 state, and step nweights (1 .. DDL_MAX_RANKS) binary32 replicas:
+ * replica 0 is read and every replica is written, since the replicas of a
+ * synchronous step are equal.  copy: NULL, or a DDL_F16 or DDL_BF16 buffer
+ * that receives the new weights rounded (the working copy of a 16-bit forward
+ * pass).  All buffers are indexed by the same element offsets; elements
+ * outside the handle's spans are neither read nor written.  Buffers need the
+ * alignment of an element; 16-byte aligned ones are faster.
+ *
+ * A handle is built from spans on the host alone, without a GPU.  Its first
+ * call on a device allocates its tables and workspace there, once (call it
+ * before a capture into a HIP graph, otherwise DDL_E_UNBOUND); later calls
+ * allocate nothing and run on that device (otherwise DDL_E_DEVICE).  Calls
+ * are asynchronous on `stream`; two Muon calls of one handle that may run at
+ * the same time on the device race on its workspace: order them.  Destroying
+ * a handle waits for the device's work; a handle must outlive the graphs
+ * captured from it.
+ * Errors: DDL_E_NULL, DDL_E_ARG (sizes, types, non-finite settings, or not a
+ * live handle), DDL_E_BUCKETS (spans overlap or pass 2^40 elements),
+ * DDL_E_ALIGN, DDL_E_UNBOUND, DDL_E_DEVICE, DDL_E_NOMEM, DDL_E_HIP. */
+typedef struct ddl_adamw_s *ddl_adamw;
+
+int ddl_adamw_create(ddl_adamw *out, const size_t *offsets, const size_t *counts, int nspans);
+/* m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2;
+ * w = (1 - lr weight_decay) w
+ *     - lr (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps)
+ * step counts from 1; 0 <= beta < 1, eps >= 0. */
+int ddl_adamw_step(ddl_adamw handle, const void *grad, int grad_dtype, float *m, float *v,
+                   float *const *weights, int nweights, void *copy, int copy_dtype, double lr,
+                   double beta1, double beta2, double eps, double weight_decay, long long step,
+                   void *stream);
+int ddl_adamw_destroy(ddl_adamw handle);
+
+/* A row-major rows x cols matrix at `offset` of the flat buffers, and the
+ * factor of its update. */
+typedef struct {
+    size_t offset, rows, cols;
+    double scale;
+} ddl_muon_matrix;
+
+typedef struct ddl_muon_s *ddl_muon;
+
+/* Muon (K. Jordan's description of the optimizer): the momentum's matrix is
+ * replaced by a nearly orthogonal one before it updates the weights.
+ *   orthogonal(U): X = U / (||U||_F + 1e-7), then five times
+ *     A = X X^T,  X <- 3.4445 X + (-4.7750 A + 2.0315 A A) X
+ *   (on U^T where rows > cols), which takes every singular value that is not
+ *   tiny to the neighbourhood of 1.
+ * rows, cols <= 65536; extents of 0 are allowed. */
+int ddl_muon_create(ddl_muon *out, const ddl_muon_matrix *matrices, int nmatrices);
+/* out = orthogonal(grad) for every matrix, in grad's type.  16-bit types
+ * multiply binary16 values (error of the result below 0.5%, of the order of
+ * bfloat16's rounding); binary32 multiplies pairs of binary16 values (22
+ * significant bits).  out may be grad. */
+int ddl_muon_orthogonalise(ddl_muon handle, const void *grad, void *out, int dtype,
+                           void *stream);
+/* momentum = momentum_decay momentum + g;
+ * u = g + momentum_decay momentum (nesterov 1) or momentum (0);
+ * w = (1 - lr weight_decay) w - lr scale orthogonal(u), with the precision of
+ * the binary32 form whatever the gradients' type. */
+int ddl_muon_step(ddl_muon handle, const void *grad, int grad_dtype, float *momentum,
+                  float *const *weights, int nweights, void *copy, int copy_dtype, double lr,
+                  double momentum_decay, int nesterov, double weight_decay, void *stream);
+int ddl_muon_destroy(ddl_muon handle);
 
 /* ---- measurement -------------------------------------------------------- *
  * With profiling on, kernel launches are bracketed by a pair of HIP events

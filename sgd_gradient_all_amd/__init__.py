@@ -12,3 +12,6 @@ from ._ddl import (  # noqa: F401
     LARS_COEFF, LARS_EPS, DDLError, Plan, ReadyEvent, ddl_allreduce, ddl_cache_clear, ddl_cache_count,
     ddl_plan_create, ddl_strerror, get_tuning, lib, set_tuning, topo,
 )
+from ._operators import (  # noqa: F401
+    ACTS, DDL_BF16, AdamW, Muon, linear, linear_dgrad, linear_wgrad, linear_workspace,
+)

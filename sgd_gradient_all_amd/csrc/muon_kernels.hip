@@ -1,0 +1,752 @@
+// muon_kernels.hip -- the Muon step (gfx950): momentum, the orthogonalisation
+// of every matrix by five rounds of Newton-Schulz products, and the update.
+//
+//     X = U / (||U||_F + 1e-7),  s x l with s <= l (U^T where U is tall)
+//     five times:  A = X X^T,  B = b A + c A A,  X <- a X + B X
+//
+// All matrices of a handle go through each product in one launch, whatever
+// their shapes: a table names the matrix and the tile of every workgroup.
+//
+// Numbers.  The rounds amplify a rounding of X as they amplify its small
+// singular values (3.4445 a round), so one 16-bit product is not enough for
+// binary32 weights: with binary16 operands X ends 0.2% off, which is below
+// bfloat16's own rounding and is what 16-bit outputs get; the binary32 form
+// holds X, A and B as sums of two binary16 values (22 bits) and takes three
+// products, high*high + high*low + low*high, which ends as close as binary32
+// products do.  Values are kept times 2^14: no entry of X passes 1.3 and none
+// of A or B 2.9 in magnitude (the spectral norms bound them), so nothing
+// overflows binary16, and entries as small as 2^-28 are normal numbers.
+//
+// A and B are symmetric: tiles on and below the diagonal are computed and
+// stored twice.  Workspaces are padded with zeros to whole tiles.
+#include <hip/hip_runtime.h>
+#include <math.h>
+
+#include <algorithm>
+#include <new>
+
+#include "../../include/ddl.h"
+#include "device_common.h"
+#include "gemm_core.h"
+#include "optimizer_internal.h"
+
+namespace ddl {
+namespace {
+
+using gemm::f32x4;
+using gemm::Operand;
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32v8 __attribute__((ext_vector_type(8)));
+
+constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
+constexpr int kRounds = 5;
+constexpr double kNormEps = 1e-7;
+constexpr float kScale = 16384.0f, kUnscale = 1.0f / 16384.0f;
+constexpr uint32_t kNormChunk = 8192;
+
+struct Mat {
+    uint64_t at;         // of the flat buffers
+    uint64_t x, a, b;    // of the workspace: 2 x 2 planes of X, 2 of A, 2 of B
+    uint32_t rows, cols;
+    uint32_t s, l, sp, lp;
+    uint32_t tall;
+    float scale;
+    uint32_t chunk0, chunk1;  // its parts of the sum of squares
+};
+
+// A workgroup of a product: the tile, and its part of the k tiles.
+struct Work {
+    uint32_t mat;
+    uint16_t ti, tj;
+    uint16_t part, parts;
+    uint32_t slot;   // of the first part's partial sums
+    uint32_t ticket; // of the tile's count of finished parts
+};
+
+struct Update {
+    const void *grad;
+    float *momentum;  // null: no momentum, U = grad (orthogonalise)
+    float mu;
+    int nesterov;
+    void *out;  // orthogonalise
+    float keep, lr;
+    void *copy;
+    int copy_type;
+    int vec;
+};
+
+struct StepArgs {
+    const Mat *mats;
+    const Work *work;
+    uint32_t count;
+    uint16_t *ws;
+    float *partial;
+    uint32_t *tickets;
+    int from;   // which of X's two copies is read
+    int passes; // 3: pairs of binary16; 1: the high halves alone
+    int last;
+};
+
+// The high part is rounded from the binary32 value that the low part completes:
+// without the barrier the compiler may round the product behind v to binary16
+// at once in one of its two uses, and the pair is then off by a binary16 step
+// where the two roundings differ (one element in some thousands).
+__device__ __forceinline__ void split(float v, _Float16 &h, _Float16 &l) {
+    v = dev::opaque1(v);
+    h = (_Float16)v;
+    l = (_Float16)(v - (float)h);
+}
+__device__ __forceinline__ void store_pair(uint16_t *hi, uint16_t *lo, uint64_t at,
+                                           const float (&v)[8]) {
+    f16x8 h, l;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        _Float16 a, b;
+        split(v[e], a, b);
+        h[e] = a;
+        l[e] = b;
+    }
+    *(f16x8 *)(hi + at) = h;
+    *(f16x8 *)(lo + at) = l;
+}
+__device__ __forceinline__ void load_pair(const uint16_t *hi, const uint16_t *lo, uint64_t at,
+                                          float (&v)[8]) {
+    const f16x8 h = *(const f16x8 *)(hi + at), l = *(const f16x8 *)(lo + at);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        v[e] = (float)h[e] + (float)l[e];
+}
+
+// the momentum, and the sum of squares of U over each chunk
+template <class G>
+__global__ __launch_bounds__(256) void norm_kernel(const Chunk *chunks, Update u,
+                                                   double *partial) {
+    __shared__ double lds[4];
+    const Chunk c = chunks[blockIdx.x];
+    const G *g = (const G *)u.grad + c.at;
+    float *m = u.momentum ? u.momentum + c.at : nullptr;
+    typedef float V4 __attribute__((ext_vector_type(4)));
+    typedef G G4 __attribute__((ext_vector_type(4)));
+    double sum = 0.0;
+    uint32_t done = 0;
+    auto one = [&](float gv, float &mv) {
+        mv = u.mu * mv + gv;
+        return u.nesterov ? gv + u.mu * mv : mv;
+    };
+    if (u.vec && c.at % 8 == 0) {
+        done = c.count & ~3u;
+#pragma unroll 4
+        for (uint32_t i = threadIdx.x * 4; i < done; i += 1024) {
+            const G4 gv = *(const G4 *)(g + i);
+            V4 x;
+            if (m) {
+                V4 mv = *(V4 *)(m + i);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float t = mv[e];
+                    x[e] = one((float)gv[e], t);
+                    mv[e] = t;
+                }
+                *(V4 *)(m + i) = mv;
+            } else {
+                x = __builtin_convertvector(gv, V4);
+            }
+            dev::add_squares(x, sum);
+        }
+    }
+    for (uint32_t i = done + threadIdx.x; i < c.count; i += 256) {
+        float x = (float)g[i];
+        if (m) {
+            float t = m[i];
+            x = one(x, t);
+            m[i] = t;
+        }
+        sum += (double)x * (double)x;
+    }
+    sum = dev::block_sum(sum, lds);
+    if (threadIdx.x == 0)
+        partial[blockIdx.x] = sum;
+}
+
+// X = U / norm, times kScale, as pairs, turned where tall and padded with
+// zeros: a 64 x 64 block of X a workgroup.
+template <class G>
+__global__ __launch_bounds__(256) void normalise_kernel(const Mat *mats, const Work *work,
+                                                        Update u, const double *partial,
+                                                        uint16_t *ws) {
+    __shared__ double lds[4];
+    __shared__ float inv_lds;
+    __shared__ float block[64][65];
+    const Work w = work[blockIdx.x];
+    const Mat t = mats[w.mat];
+    double sum = 0.0;
+    for (uint32_t i = t.chunk0 + threadIdx.x; i < t.chunk1; i += 256)
+        sum += partial[i];
+    sum = dev::block_sum(sum, lds);
+    if (threadIdx.x == 0)
+        inv_lds = (float)((double)kScale / (sqrt(sum) + kNormEps));
+    const uint32_t s0 = w.ti * 64u, l0 = w.tj * 64u;
+    // rows and columns of U from (r0, c0) on
+    const uint32_t r0 = t.tall ? l0 : s0, c0 = t.tall ? s0 : l0;
+    const uint32_t cc = threadIdx.x & 63u;
+#pragma unroll 4
+    for (uint32_t rr = threadIdx.x >> 6; rr < 64; rr += 4) {
+        float x = 0.0f;
+        if (r0 + rr < t.rows && c0 + cc < t.cols) {
+            const uint64_t at = t.at + (uint64_t)(r0 + rr) * t.cols + c0 + cc;
+            x = (float)((const G *)u.grad)[at];
+            if (u.momentum)  // already this step's
+                x = u.nesterov ? x + u.mu * u.momentum[at] : u.momentum[at];
+        }
+        block[rr][cc] = x;
+    }
+    __syncthreads();
+    const float inv = inv_lds;
+    uint16_t *hi = ws + t.x, *lo = hi + (uint64_t)t.sp * t.lp;
+    const uint32_t k = (threadIdx.x & 7u) * 8;
+#pragma unroll
+    for (uint32_t q = threadIdx.x >> 3; q < 64; q += 32) {
+        float v[8];
+#pragma unroll
+        for (uint32_t e = 0; e < 8; ++e)
+            v[e] = inv * (t.tall ? block[k + e][q] : block[q][k + e]);
+        store_pair(hi, lo, (uint64_t)(s0 + q) * t.lp + l0 + k, v);
+    }
+}
+
+enum { kGram, kPoly, kApply };
+
+// 8 results of the last round, from element `at` of the flat buffers on.
+template <class G>
+__device__ __forceinline__ void apply_update(const Update &u, const Replicas &r, uint64_t at,
+                                             uint32_t have, float scale, const float (&v)[8]) {
+    const bool vec = u.vec && have == 8 && at % 8 == 0;
+    if (u.out) {
+        G *o = (G *)u.out + at;
+        typedef G G8 __attribute__((ext_vector_type(8)));
+        G8 x;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            x[e] = (G)(v[e] * kUnscale);
+        if (vec) {
+            *(G8 *)o = x;
+        } else {
+#pragma unroll
+            for (uint32_t e = 0; e < 8; ++e)
+                if (e < have)
+                    o[e] = x[e];
+        }
+        return;
+    }
+    const float *w0 = r.w[0] + at;
+    f32v8 w = {};
+    if (vec) {
+        w = *(const f32v8 *)w0;
+    } else {
+#pragma unroll
+        for (uint32_t e = 0; e < 8; ++e)
+            if (e < have)
+                w[e] = w0[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        w[e] = u.keep * w[e] - scale * (v[e] * kUnscale);
+    for (int k = 0; k < r.count; ++k) {
+        float *o = r.w[k] + at;
+        if (vec) {
+            *(f32v8 *)o = w;
+        } else {
+#pragma unroll
+            for (uint32_t e = 0; e < 8; ++e)
+                if (e < have)
+                    o[e] = w[e];
+        }
+    }
+    if (u.copy) {
+        uint16_t h[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            h[e] = u.copy_type == DDL_BF16 ? __builtin_bit_cast(uint16_t, (__bf16)w[e])
+                                           : __builtin_bit_cast(uint16_t, (_Float16)w[e]);
+        uint16_t *o = (uint16_t *)u.copy + at;
+        if (vec) {
+            __builtin_memcpy(__builtin_assume_aligned(o, 16), h, 16);
+        } else {
+#pragma unroll
+            for (uint32_t e = 0; e < 8; ++e)
+                if (e < have)
+                    o[e] = h[e];
+        }
+    }
+}
+
+// One product over the tiles of every matrix.  A tile whose k is dealt to
+// several workgroups is finished by the last of them to arrive, which adds
+// the parts in their order, so the sums do not depend on who that is.
+template <class Core, int KIND, class G>
+__global__ __launch_bounds__(Core::THREADS) void product_kernel(StepArgs p, Update u,
+                                                                Replicas r) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    __shared__ uint32_t arrived;
+    // consecutive entries of the table on one die, which share operands
+    constexpr uint32_t kDies = 8;
+    const uint32_t die = blockIdx.x % kDies, per = p.count / kDies, more = p.count % kDies;
+    const Work w = p.work[die * per + (die < more ? die : more) + blockIdx.x / kDies];
+    const Mat t = p.mats[w.mat];
+    const uint64_t nx = (uint64_t)t.sp * t.lp, na = (uint64_t)t.sp * t.sp;
+    uint16_t *x = p.ws + t.x + p.from * 2 * nx, *y = p.ws + t.x + (p.from ^ 1) * 2 * nx;
+    uint16_t *a = p.ws + t.a, *b = p.ws + t.b;
+    Operand left, right;
+    left.row0 = w.ti * Core::BM;
+    right.row0 = w.tj * Core::BN;
+    left.rows = t.sp;
+    if (KIND == kGram) {
+        left.plane[0] = right.plane[0] = x;
+        left.plane[1] = right.plane[1] = x + nx;
+        left.ld = left.k = t.lp;
+        right.rows = t.sp;
+    } else {
+        left.plane[0] = KIND == kPoly ? a : b;
+        left.plane[1] = left.plane[0] + na;
+        left.ld = left.k = t.sp;
+        right.plane[0] = KIND == kPoly ? a : x;
+        right.plane[1] = KIND == kPoly ? a + na : x + nx;
+        right.rows = KIND == kPoly ? t.sp : t.lp;
+    }
+    right.ld = KIND == kPoly ? t.sp : t.lp;
+    right.k = left.k;
+    const uint32_t kt = (uint32_t)(left.k / gemm::kBK), all = kt * p.passes;
+    f32x4 acc[Core::FM][Core::FN] = {};
+    Core::run(left, right, all * w.part / w.parts, all * (w.part + 1) / w.parts,
+              p.passes == 3 ? kt : 0, lds, acc);
+    if (w.parts > 1) {
+        constexpr uint32_t N = Core::FM * Core::FN;
+        f32x4 *mine = (f32x4 *)p.partial + (uint64_t)(w.slot + w.part) * N * Core::THREADS;
+#pragma unroll
+        for (uint32_t i = 0; i < N; ++i)
+            mine[i * Core::THREADS + threadIdx.x] = acc[i / Core::FN][i % Core::FN];
+        __threadfence();
+        __syncthreads();
+        if (threadIdx.x == 0)
+            arrived = __hip_atomic_fetch_add(p.tickets + w.ticket, 1u, __ATOMIC_ACQ_REL,
+                                             __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
+        if (arrived != (uint32_t)w.parts - 1)
+            return;
+        __threadfence();
+        if (threadIdx.x == 0)  // for the next launch
+            __hip_atomic_store(p.tickets + w.ticket, 0u, __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_AGENT);
+        const f32x4 *part = (const f32x4 *)p.partial + (uint64_t)w.slot * N * Core::THREADS;
+#pragma unroll
+        for (uint32_t i = 0; i < N; ++i)
+            acc[i / Core::FN][i % Core::FN] = part[i * Core::THREADS + threadIdx.x];
+        for (uint32_t q = 1; q < w.parts; ++q) {
+            part += N * Core::THREADS;
+#pragma unroll
+            for (uint32_t i = 0; i < N; ++i)
+                acc[i / Core::FN][i % Core::FN] += part[i * Core::THREADS + threadIdx.x];
+        }
+    }
+    if constexpr (KIND == kApply) {
+        auto next = [&](uint32_t m, uint32_t n, float (&v)[8]) {
+            float old[8];
+            load_pair(x, x + nx, (uint64_t)m * t.lp + n, old);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[e] = kA * old[e] + v[e] * kUnscale;
+        };
+        if (!p.last) {
+            Core::each(acc, lds, [&](uint32_t mi, uint32_t ni, float (&v)[8]) {
+                const uint32_t m = left.row0 + mi, n = right.row0 + ni;
+                next(m, n, v);
+                store_pair(y, y + nx, (uint64_t)m * t.lp + n, v);
+            });
+        } else if (!t.tall) {
+            Core::each(acc, lds, [&](uint32_t mi, uint32_t ni, float (&v)[8]) {
+                const uint32_t m = left.row0 + mi, n = right.row0 + ni;
+                if (m >= t.s || n >= t.l)
+                    return;
+                next(m, n, v);
+                apply_update<G>(u, r, t.at + (uint64_t)m * t.cols + n,
+                                t.l - n < 8 ? t.l - n : 8, u.lr * t.scale, v);
+            });
+        } else {
+            Core::template each<true>(acc, lds, [&](uint32_t mi, uint32_t ni, float (&v)[8]) {
+                const uint32_t m = left.row0 + mi, n = right.row0 + ni;
+                if (m >= t.s || n >= t.l)
+                    return;
+                const _Float16 *h = (const _Float16 *)x + (uint64_t)m * t.lp + n;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[e] = kA * ((float)h[(uint64_t)e * t.lp] + (float)h[nx + (uint64_t)e * t.lp])
+                           + v[e] * kUnscale;
+                apply_update<G>(u, r, t.at + (uint64_t)n * t.cols + m,
+                                t.s - m < 8 ? t.s - m : 8, u.lr * t.scale, v);
+            });
+        }
+    } else {
+        uint16_t *o = KIND == kGram ? a : b;
+        auto value = [&](uint64_t at, float (&v)[8]) {
+            if (KIND == kGram) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[e] *= kUnscale;
+            } else {
+                float old[8];
+                load_pair(a, a + na, at, old);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[e] = kB * old[e] + kC * (v[e] * kUnscale);
+            }
+        };
+        Core::each(acc, lds, [&](uint32_t mi, uint32_t ni, float (&v)[8]) {
+            const uint64_t at = (uint64_t)(left.row0 + mi) * t.sp + right.row0 + ni;
+            value(at, v);
+            store_pair(o, o + na, at, v);
+        });
+        if (w.ti != w.tj)  // the mirror image
+            Core::template each<true>(acc, lds, [&](uint32_t mi, uint32_t ni, float (&v)[8]) {
+                const uint64_t at = (uint64_t)(right.row0 + ni) * t.sp + left.row0 + mi;
+                value(at, v);  // A is symmetric
+                store_pair(o, o + na, at, v);
+            });
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+
+constexpr uint32_t kMaxSide = 65536;
+
+uint32_t up(uint32_t v, uint32_t to) { return (v + to - 1) / to * to; }
+
+}  // namespace
+}  // namespace ddl
+
+using namespace ddl;
+
+struct ddl_muon_s {
+    std::vector<Mat> mats;
+    std::vector<Chunk> chunks;
+    std::vector<Work> blocks;       // normalise
+    // the products' tables, for one pass over k and for three
+    std::vector<Work> gram[2], poly[2], apply[2];
+    uint32_t tile = 64;
+    uint64_t ws = 0;     // elements of the workspace
+    uint64_t slots = 0;  // partial tiles
+    uint32_t tickets = 0;
+
+    Handle dev;
+    Mat *d_mats = nullptr;
+    Chunk *d_chunks = nullptr;
+    Work *d_blocks = nullptr, *d_gram[2] = {}, *d_poly[2] = {}, *d_apply[2] = {};
+    uint16_t *d_ws = nullptr;
+    float *d_partial = nullptr;
+    uint32_t *d_tickets = nullptr;
+    double *d_sums = nullptr;
+};
+
+namespace ddl {
+namespace {
+
+// Tiles of a product over all matrices, k cut into parts where the tiles
+// alone do not fill the card.
+void deal(ddl_muon_s &h, int kind, int passes, std::vector<Work> &out) {
+    const uint32_t T = h.tile;
+    uint64_t tiles = 0;
+    auto count = [&](const Mat &m, auto &&then) {
+        const uint32_t ni = m.sp / T, nj = kind == kApply ? m.lp / T : ni;
+        for (uint32_t j = 0; j < nj; ++j)
+            for (uint32_t i = kind == kApply ? 0 : j; i < ni; ++i)
+                then(i, j);
+    };
+    uint64_t steps = 0;  // k tiles over all tiles
+    auto depth = [&](const Mat &m) {
+        return (uint64_t)(kind == kGram ? m.lp : m.sp) / gemm::kBK * passes;
+    };
+    for (const Mat &m : h.mats)
+        count(m, [&](uint32_t, uint32_t) {
+            ++tiles;
+            steps += depth(m);
+        });
+    // parts of at most this many k tiles: the load of one of 512 equal shares
+    const uint64_t share = std::max<uint64_t>((steps + 511) / 512, 16);
+    uint64_t slots = 0;
+    uint32_t tickets = 0;
+    for (uint32_t i = 0; i < h.mats.size(); ++i) {
+        const uint64_t d = depth(h.mats[i]);
+        const uint16_t parts =
+            tiles >= 512 ? 1 : (uint16_t)std::max<uint64_t>(1, std::min<uint64_t>(d / share, 32));
+        count(h.mats[i], [&](uint32_t ti, uint32_t tj) {
+            for (uint16_t q = 0; q < parts; ++q)
+                out.push_back({i, (uint16_t)ti, (uint16_t)tj, q, parts, (uint32_t)slots,
+                               tickets});
+            if (parts > 1) {
+                slots += parts;
+                ++tickets;
+            }
+        });
+    }
+    h.slots = std::max(h.slots, slots);
+    h.tickets = std::max(h.tickets, tickets);
+}
+
+void lay_out(ddl_muon_s &h) {
+    uint64_t large = 0, middle = 0;
+    for (const Mat &m : h.mats) {
+        large += (uint64_t)up(m.s, 256) / 256 * (up(m.l, 256) / 256);
+        middle += (uint64_t)up(m.s, 128) / 128 * (up(m.l, 128) / 128);
+    }
+    h.tile = large >= 256 ? 256 : middle >= 64 ? 128 : 64;
+    for (uint32_t i = 0; i < h.mats.size(); ++i) {
+        Mat &m = h.mats[i];
+        m.sp = up(m.s, h.tile);
+        m.lp = up(m.l, h.tile);
+        m.x = h.ws;
+        h.ws += 4ull * m.sp * m.lp;
+        m.a = h.ws;
+        h.ws += 2ull * m.sp * m.sp;
+        m.b = h.ws;
+        h.ws += 2ull * m.sp * m.sp;
+        m.chunk0 = (uint32_t)h.chunks.size();
+        cut_chunks({m.at, (uint64_t)m.rows * m.cols}, kNormChunk, h.chunks, i);
+        m.chunk1 = (uint32_t)h.chunks.size();
+        for (uint32_t a = 0; a < m.sp / 64; ++a)
+            for (uint32_t b = 0; b < m.lp / 64; ++b)
+                h.blocks.push_back({i, (uint16_t)a, (uint16_t)b, 0, 1, 0, 0});
+    }
+    for (int f = 0; f < 2; ++f) {
+        const int passes = f ? 3 : 1;
+        deal(h, kGram, passes, h.gram[f]);
+        deal(h, kPoly, passes, h.poly[f]);
+        deal(h, kApply, passes, h.apply[f]);
+    }
+}
+
+int bind_muon(ddl_muon_s &h, hipStream_t s) {
+    return h.dev.bind(s, [&]() -> int {
+        int rc = upload(h.mats, &h.d_mats);
+        rc = rc ? rc : upload(h.chunks, &h.d_chunks);
+        rc = rc ? rc : upload(h.blocks, &h.d_blocks);
+        for (int f = 0; f < 2; ++f) {
+            rc = rc ? rc : upload(h.gram[f], &h.d_gram[f]);
+            rc = rc ? rc : upload(h.poly[f], &h.d_poly[f]);
+            rc = rc ? rc : upload(h.apply[f], &h.d_apply[f]);
+        }
+        rc = rc ? rc : upload(std::vector<uint32_t>(h.tickets, 0), &h.d_tickets);
+        if (!rc
+            && (hipMalloc((void **)&h.d_ws, h.ws * 2) != hipSuccess
+                || hipMalloc((void **)&h.d_partial,
+                             std::max<uint64_t>(1, h.slots) * h.tile * h.tile * 4)
+                       != hipSuccess
+                || hipMalloc((void **)&h.d_sums, h.chunks.size() * 8) != hipSuccess))
+            rc = DDL_E_NOMEM;
+        if (rc) {  // nothing half made: the next call starts anew
+            (void)hipFree(h.d_mats), (void)hipFree(h.d_chunks), (void)hipFree(h.d_blocks);
+            (void)hipFree(h.d_tickets), (void)hipFree(h.d_ws), (void)hipFree(h.d_partial);
+            (void)hipFree(h.d_sums);
+            h.d_mats = nullptr, h.d_chunks = nullptr, h.d_blocks = nullptr;
+            h.d_tickets = nullptr, h.d_ws = nullptr, h.d_partial = nullptr, h.d_sums = nullptr;
+            for (int f = 0; f < 2; ++f) {
+                (void)hipFree(h.d_gram[f]), (void)hipFree(h.d_poly[f]);
+                (void)hipFree(h.d_apply[f]);
+                h.d_gram[f] = h.d_poly[f] = h.d_apply[f] = nullptr;
+            }
+        }
+        return rc;
+    });
+}
+
+template <class Core, int KIND, class G>
+int launch_product(const StepArgs &p, const Update &u, const Replicas &r, hipStream_t s) {
+    if (Core::LDS > 65536
+        && hipFuncSetAttribute((const void *)&product_kernel<Core, KIND, G>,
+                               hipFuncAttributeMaxDynamicSharedMemorySize, Core::LDS)
+               != hipSuccess)
+        return DDL_E_HIP;
+    hipLaunchKernelGGL((product_kernel<Core, KIND, G>), dim3(p.count), dim3(Core::THREADS),
+                       Core::LDS, s, p, u, r);
+    return hipGetLastError() == hipSuccess ? DDL_OK : DDL_E_HIP;
+}
+
+template <int T, class G>
+int rounds(ddl_muon_s &h, const Update &u, const Replicas &r, int f, hipStream_t s) {
+    constexpr int WR = 2, WC = T == 256 ? 4 : 2;
+    using Rows = gemm::Core<gemm::Half, T, T, WR, WC, false, false, false>;
+    using Cols = gemm::Core<gemm::Half, T, T, WR, WC, false, true, false>;
+    StepArgs p;
+    p.mats = h.d_mats;
+    p.ws = h.d_ws;
+    p.partial = h.d_partial;
+    p.tickets = h.d_tickets;
+    p.passes = f ? 3 : 1;
+    int rc = DDL_OK;
+    for (int i = 0; i < kRounds && !rc; ++i) {
+        p.from = i & 1;
+        p.last = i == kRounds - 1;
+        p.work = h.d_gram[f];
+        p.count = (uint32_t)h.gram[f].size();
+        rc = launch_product<Rows, kGram, float>(p, u, r, s);
+        p.work = h.d_poly[f];
+        p.count = (uint32_t)h.poly[f].size();
+        rc = rc ? rc : launch_product<Rows, kPoly, float>(p, u, r, s);
+        p.work = h.d_apply[f];
+        p.count = (uint32_t)h.apply[f].size();
+        rc = rc ? rc : launch_product<Cols, kApply, G>(p, u, r, s);
+    }
+    return rc;
+}
+
+template <class G>
+int run_muon(ddl_muon_s &h, const Update &u, const Replicas &r, int f, hipStream_t s) {
+    hipLaunchKernelGGL(norm_kernel<G>, dim3((uint32_t)h.chunks.size()), dim3(256), 0, s,
+                       h.d_chunks, u, h.d_sums);
+    hipLaunchKernelGGL(normalise_kernel<G>, dim3((uint32_t)h.blocks.size()), dim3(256), 0, s,
+                       h.d_mats, h.d_blocks, u, h.d_sums, h.d_ws);
+    if (hipGetLastError() != hipSuccess)
+        return DDL_E_HIP;
+    return h.tile == 256   ? rounds<256, G>(h, u, r, f, s)
+           : h.tile == 128 ? rounds<128, G>(h, u, r, f, s)
+                           : rounds<64, G>(h, u, r, f, s);
+}
+
+int run_typed(ddl_muon_s &h, int type, const Update &u, const Replicas &r, int f, void *stream) {
+    hipStream_t s = (hipStream_t)stream;
+    return type == DDL_F32   ? run_muon<float>(h, u, r, f, s)
+           : type == DDL_F16 ? run_muon<_Float16>(h, u, r, f, s)
+                             : run_muon<__bf16>(h, u, r, f, s);
+}
+
+}  // namespace
+}  // namespace ddl
+
+extern "C" {
+
+int ddl_muon_create(ddl_muon *out, const ddl_muon_matrix *matrices, int nmatrices) {
+    if (!out || (nmatrices > 0 && !matrices))
+        return DDL_E_NULL;
+    *out = nullptr;
+    if (nmatrices < 0)
+        return DDL_E_ARG;
+    ddl_muon h = nullptr;
+    int rc = DDL_OK;
+    try {
+        h = new ddl_muon_s;
+        std::vector<Span> spans;
+        for (int i = 0; i < nmatrices && !rc; ++i) {
+            const ddl_muon_matrix &m = matrices[i];
+            if (m.rows > kMaxSide || m.cols > kMaxSide || !std::isfinite(m.scale))
+                rc = DDL_E_ARG;
+            if (rc || !m.rows || !m.cols)
+                continue;
+            spans.push_back({m.offset, m.rows * m.cols});
+            Mat t = {};
+            t.at = m.offset;
+            t.rows = (uint32_t)m.rows;
+            t.cols = (uint32_t)m.cols;
+            t.tall = m.rows > m.cols;
+            t.s = std::min(t.rows, t.cols);
+            t.l = std::max(t.rows, t.cols);
+            t.scale = (float)m.scale;
+            h->mats.push_back(t);
+        }
+        if (!rc && !disjoint(spans))
+            rc = DDL_E_BUCKETS;
+        if (!rc) {
+            lay_out(*h);
+            if (h->slots > UINT32_MAX || h->apply[1].size() > kMaxGrid
+                || h->blocks.size() > kMaxGrid)
+                rc = DDL_E_ARG;
+        }
+        if (!rc)
+            register_handle(h);
+    } catch (...) {
+        rc = DDL_E_NOMEM;
+    }
+    if (rc) {
+        delete h;
+        return rc;
+    }
+    *out = h;
+    return DDL_OK;
+}
+
+int ddl_muon_destroy(ddl_muon h) {
+    if (!h)
+        return DDL_E_NULL;
+    if (!unregister_handle(h))
+        return DDL_E_ARG;
+    h->dev.release(h->d_mats, h->d_chunks, h->d_blocks, h->d_gram[0], h->d_gram[1], h->d_poly[0],
+                   h->d_poly[1], h->d_apply[0], h->d_apply[1], h->d_ws, h->d_partial,
+                   h->d_tickets, h->d_sums);
+    delete h;
+    return DDL_OK;
+}
+
+int ddl_muon_orthogonalise(ddl_muon h, const void *grad, void *out, int dtype, void *stream) {
+    if (!h)
+        return DDL_E_NULL;
+    std::unique_lock<std::mutex> lk;
+    if (!hold_handle(h, lk) || !float_type(dtype))
+        return DDL_E_ARG;
+    if (h->mats.empty())
+        return DDL_OK;
+    if (!grad || !out)
+        return DDL_E_NULL;
+    if (!aligned_to(grad, dtype) || !aligned_to(out, dtype))
+        return DDL_E_ALIGN;
+    const int rc = bind_muon(*h, (hipStream_t)stream);
+    if (rc)
+        return rc;
+    Update u = {};
+    u.grad = grad;
+    u.out = out;
+    u.vec = !(((uintptr_t)grad | (uintptr_t)out) % 16);
+    Replicas r = {};
+    return run_typed(*h, dtype, u, r, dtype == DDL_F32, stream);
+}
+
+int ddl_muon_step(ddl_muon h, const void *grad, int grad_dtype, float *momentum,
+                  float *const *weights, int nweights, void *copy, int copy_dtype, double lr,
+                  double momentum_decay, int nesterov, double weight_decay, void *stream) {
+    if (!h)
+        return DDL_E_NULL;
+    std::unique_lock<std::mutex> lk;
+    if (!hold_handle(h, lk) || nweights < 1 || nweights > DDL_MAX_RANKS
+        || !float_type(grad_dtype) || (copy && copy_dtype != DDL_F16 && copy_dtype != DDL_BF16)
+        || (nesterov != 0 && nesterov != 1) || !std::isfinite(lr)
+        || !std::isfinite(momentum_decay) || !std::isfinite(weight_decay))
+        return DDL_E_ARG;
+    if (h->mats.empty())
+        return DDL_OK;
+    Replicas r = {};
+    int rc = take_replicas(weights, nweights, r);
+    if (rc)
+        return rc;
+    if (!grad || !momentum)
+        return DDL_E_NULL;
+    if (!aligned_to(grad, grad_dtype) || !aligned_to(momentum, DDL_F32)
+        || (copy && !aligned_to(copy, copy_dtype)))
+        return DDL_E_ALIGN;
+    rc = bind_muon(*h, (hipStream_t)stream);
+    if (rc)
+        return rc;
+    Update u = {};
+    u.grad = grad;
+    u.momentum = momentum;
+    u.mu = (float)momentum_decay;
+    u.nesterov = nesterov;
+    u.keep = (float)(1 - lr * weight_decay);
+    u.lr = (float)lr;
+    u.copy = copy;
+    u.copy_type = copy_dtype;
+    uintptr_t any = (uintptr_t)grad | (uintptr_t)momentum | (uintptr_t)copy;
+    for (int i = 0; i < nweights; ++i)
+        any |= (uintptr_t)weights[i];
+    u.vec = any % 16 == 0;
+    return run_typed(*h, grad_dtype, u, r, 1, stream);
+}
+
+}  // extern "C"
