@@ -596,10 +596,10 @@ typedef struct ddl_muon_s *ddl_muon;
  *   tiny to the neighbourhood of 1.
  * rows, cols <= 65536; extents of 0 are allowed. */
 int ddl_muon_create(ddl_muon *out, const ddl_muon_matrix *matrices, int nmatrices);
-/* out = orthogonal(grad) for every matrix, in grad's type.  16-bit types
- * multiply binary16 values (error of the result below 0.5%, of the order of
- * bfloat16's rounding); binary32 multiplies pairs of binary16 values (22
- * significant bits).  out may be grad. */
+/* out = orthogonal(grad) for every matrix, in grad's type.  DDL_F32 and
+ * DDL_F16: products of pairs of binary16 values (22 significant bits), as
+ * close as binary32 products (2e-6 off at 4096 x 4096); DDL_BF16: fewer
+ * passes, an error of the order of bfloat16's rounding.  out may be grad. */
 int ddl_muon_orthogonalise(ddl_muon handle, const void *grad, void *out, int dtype,
                            void *stream);
 /* momentum = momentum_decay momentum + g;

@@ -24,6 +24,7 @@ using gemm::Bfloat;
 using gemm::f32x4;
 using gemm::Half;
 using gemm::Operand;
+using gemm::u32x4;
 
 // The epilogue of C[m, n] (its own m and n, not the layer's).
 struct Epilogue {
@@ -44,20 +45,31 @@ struct Epilogue {
     int vec;  // rows of every array above start on 16-byte boundaries
 };
 
-__device__ __forceinline__ float sigmoid(float v) { return 1.0f / (1.0f + __expf(-v)); }
+// The activations are a good part of a tile's time (a wave's instruction takes
+// 4 cycles for its 64 lanes, an exponential or reciprocal 16), so they are
+// written with the hardware's 2^x and 1/x (each within 1 ulp of binary32;
+// outputs are rounded to 11 bits at most) and fused multiply-adds.
+__device__ __forceinline__ float fma(float a, float b, float c) {
+    return __builtin_fmaf(a, b, c);
+}
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kTanh = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 
-constexpr float kGelu = 0.7978845608028654f;  // sqrt(2 / pi)
+// 1 / (1 + 2^-u)
+__device__ __forceinline__ float sigmoid2(float u) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-u));
+}
+// tanh's form of GELU is v sigmoid(2 sqrt(2/pi) (v + 0.044715 v^3))
+__device__ __forceinline__ float tanh_argument(float v) {
+    return v * fma(v * v, 0.044715f * kTanh * kLog2e, kTanh * kLog2e);
+}
 
-// __expf (the hardware's 2^x of a scaled argument, 2 ulp near 0 and relative
-// error |x| 2^-24 far out) is exact to well under half a step of the 16-bit
-// outputs that take it.
 __device__ __forceinline__ float activate(float v, int act) {
     switch (act) {
     case DDL_ACT_RELU: return v < 0.0f ? 0.0f : v;  // NaN stays NaN
     case DDL_ACT_GELU: return 0.5f * v * (1.0f + erff(v * 0.7071067811865476f));
-    case DDL_ACT_GELU_TANH:
-        return v * sigmoid(2.0f * kGelu * (v + 0.044715f * v * v * v));
-    case DDL_ACT_SILU: return v * sigmoid(v);
+    case DDL_ACT_GELU_TANH: return v * sigmoid2(tanh_argument(v));
+    case DDL_ACT_SILU: return v * sigmoid2(v * kLog2e);
     default: return v;
     }
 }
@@ -66,44 +78,54 @@ __device__ __forceinline__ float act_slope(float v, int act) {
     switch (act) {
     case DDL_ACT_RELU: return v > 0.0f ? 1.0f : 0.0f;
     case DDL_ACT_GELU:
-        return 0.5f * (1.0f + erff(v * 0.7071067811865476f))
-               + v * __expf(-0.5f * v * v) * 0.3989422804014327f;
+        return fma(v * 0.3989422804014327f,
+                   __builtin_amdgcn_exp2f(v * v * (-0.5f * kLog2e)),
+                   fma(0.5f, erff(v * 0.7071067811865476f), 0.5f));
     case DDL_ACT_GELU_TANH: {
-        const float s = sigmoid(2.0f * kGelu * (v + 0.044715f * v * v * v));
-        return s + v * s * (1.0f - s) * (2.0f * kGelu) * (1.0f + 0.134145f * v * v);
+        const float s = sigmoid2(tanh_argument(v));
+        const float d = fma(v * v, 3.0f * 0.044715f * kTanh, kTanh);
+        return fma(v * d * s, 1.0f - s, s);
     }
     case DDL_ACT_SILU: {
-        const float s = sigmoid(v);
-        return s * (1.0f + v * (1.0f - s));
+        const float s = sigmoid2(v * kLog2e);
+        return s * fma(v, 1.0f - s, 1.0f);
     }
     default: return 1.0f;
     }
 }
 
-template <class E, int N>
-__device__ __forceinline__ void load_n(const E *p, uint32_t have, bool vec, float (&out)[N]) {
-    typedef E V __attribute__((ext_vector_type(8)));
-    if (vec && have >= N) {
+// 8 elements as they lie; elements past `have` are 0.
+// VEC: all of them at a 16-byte boundary.
+template <bool VEC, class E>
+__device__ __forceinline__ void load8(const E *p, uint32_t have, u32x4 (&out)[sizeof(E) / 2]) {
+    constexpr int PARTS = sizeof(E) / 2;
+    if constexpr (VEC) {
 #pragma unroll
-        for (int i = 0; i < N; i += 8) {
-            const V v = *(const V *)(p + i);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                out[i + e] = (float)v[e];
-        }
+        for (int i = 0; i < PARTS; ++i)
+            out[i] = ((const u32x4 *)p)[i];
     } else {
+        E t[8];
 #pragma unroll
-        for (uint32_t i = 0; i < N; ++i)
-            out[i] = i < have ? (float)p[i] : 0.0f;
+        for (uint32_t i = 0; i < 8; ++i)
+            t[i] = i < have ? p[i] : (E)0.0f;
+        __builtin_memcpy(out, t, sizeof(t));
     }
 }
-template <class E, int N>
-__device__ __forceinline__ void store_n(E *p, uint32_t have, bool vec, const float (&v)[N]) {
+template <class E>
+__device__ __forceinline__ void widen8(const u32x4 (&in)[sizeof(E) / 2], float (&out)[8]) {
+    E t[8];
+    __builtin_memcpy(t, in, sizeof(t));
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        out[i] = (float)t[i];
+}
+template <bool VEC, class E>
+__device__ __forceinline__ void store8(E *p, uint32_t have, const float (&v)[8]) {
     constexpr int W = 16 / sizeof(E);
     typedef E V __attribute__((ext_vector_type(W)));
-    if (vec && have >= N) {
+    if constexpr (VEC) {
 #pragma unroll
-        for (int i = 0; i < N; i += W) {
+        for (int i = 0; i < 8; i += W) {
             V o;
 #pragma unroll
             for (int e = 0; e < W; ++e)
@@ -112,78 +134,86 @@ __device__ __forceinline__ void store_n(E *p, uint32_t have, bool vec, const flo
         }
     } else {
 #pragma unroll
-        for (uint32_t i = 0; i < N; ++i)
+        for (uint32_t i = 0; i < 8; ++i)
             if (i < have)
                 p[i] = (E)v[i];
     }
 }
 
-// N consecutive results of row m from column n on; n < e.n.
-template <class T, int N>
-__device__ __forceinline__ void finish(const Epilogue &e, uint64_t m, uint64_t n, float (&v)[N]) {
+// What the epilogue reads for 8 results.
+struct Fetched {
+    u32x4 bias[1], residual[1], z_prev[1], old[1], old32[2];
+};
+
+template <class T, bool VEC>
+__device__ __forceinline__ Fetched fetch8(const Epilogue &e, uint64_t m, uint64_t n) {
     using E = typename T::E;
-    const uint32_t have = e.n - n < (uint64_t)N ? (uint32_t)(e.n - n) : (uint32_t)N;
-    const bool vec = e.vec;
-    float t[N];
-    if (e.bias) {
-        load_n<E, N>((const E *)e.bias + n, have, vec, t);
+    Fetched f;
+    if (!VEC && (m >= e.m || n >= e.n))
+        return f;
+    const uint32_t have = !VEC && e.n - n < 8 ? (uint32_t)(e.n - n) : 8u;
+    if (e.bias)
+        load8<VEC>((const E *)e.bias + n, have, f.bias);
+    if (e.residual)
+        load8<VEC>((const E *)e.residual + m * e.ldr + n, have, f.residual);
+    if (e.dz_prev)
+        load8<VEC>((const E *)e.z_prev + m * e.ldzp + n, have, f.z_prev);
+    if (e.add) {
+        if (e.f32out)
+            load8<VEC>((const float *)e.c + m * e.ldc + n, have, f.old32);
+        else
+            load8<VEC>((const E *)e.c + m * e.ldc + n, have, f.old);
+    }
+    return f;
+}
+
+// 8 consecutive results of row m from column n on.
+// VEC: the 8 are inside C and every array's rows start at 16-byte boundaries.
+template <class T, bool VEC>
+__device__ __forceinline__ void finish8(const Epilogue &e, uint64_t m, uint64_t n, float (&v)[8],
+                                        const Fetched &f) {
+    using E = typename T::E;
+    if (!VEC && (m >= e.m || n >= e.n))
+        return;
+    const uint32_t have = !VEC && e.n - n < 8 ? (uint32_t)(e.n - n) : 8u;
+    float t[8];
+    auto plus = [&]() {
 #pragma unroll
-        for (int i = 0; i < N; ++i)
+        for (int i = 0; i < 8; ++i)
             v[i] += t[i];
+    };
+    if (e.bias) {
+        widen8<E>(f.bias, t);
+        plus();
     }
     if (e.z)
-        store_n<E, N>((E *)e.z + m * e.ldz + n, have, vec, v);
+        store8<VEC>((E *)e.z + m * e.ldz + n, have, v);
     if (e.act && !e.dz_prev) {
 #pragma unroll
-        for (int i = 0; i < N; ++i)
+        for (int i = 0; i < 8; ++i)
             v[i] = activate(v[i], e.act);
     }
     if (e.residual) {
-        load_n<E, N>((const E *)e.residual + m * e.ldr + n, have, vec, t);
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            v[i] += t[i];
+        widen8<E>(f.residual, t);
+        plus();
     }
-    if (e.f32out) {
-        float *c = (float *)e.c + m * e.ldc + n;
-        if (e.add) {
-#pragma unroll
-            for (uint32_t i = 0; i < N; ++i)
-                t[i] = 0.0f;
-            if (vec && have >= N) {
-#pragma unroll
-                for (int i = 0; i < N; i += 4) {
-                    const f32x4 o = *(const f32x4 *)(c + i);
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        t[i + x] = o[x];
-                }
-            } else {
-#pragma unroll
-                for (uint32_t i = 0; i < N; ++i)
-                    t[i] = i < have ? c[i] : 0.0f;
-            }
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                v[i] += t[i];
-        }
-        store_n<float, N>(c, have, vec, v);
-    } else {
-        E *c = (E *)e.c + m * e.ldc + n;
-        if (e.add) {
-            load_n<E, N>(c, have, vec, t);
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                v[i] += t[i];
-        }
-        store_n<E, N>(c, have, vec, v);
+    if (e.add) {
+        if (e.f32out)
+            widen8<float>(f.old32, t);
+        else
+            widen8<E>(f.old, t);
+        plus();
     }
+    if (e.f32out)
+        store8<VEC>((float *)e.c + m * e.ldc + n, have, v);
+    else
+        store8<VEC>((E *)e.c + m * e.ldc + n, have, v);
     if (e.dz_prev) {
-        load_n<E, N>((const E *)e.z_prev + m * e.ldzp + n, have, vec, t);
+        widen8<E>(f.z_prev, t);
 #pragma unroll
-        for (int i = 0; i < N; ++i)
+        for (int i = 0; i < 8; ++i)
             t[i] = v[i] * act_slope(t[i], e.act);
-        store_n<E, N>((E *)e.dz_prev + m * e.lddzp + n, have, vec, t);
+        store8<VEC>((E *)e.dz_prev + m * e.lddzp + n, have, t);
     }
 }
 
@@ -225,18 +255,38 @@ __global__ __launch_bounds__(Core::THREADS) void linear_kernel(GemmArgs g) {
     const uint32_t t1 = (uint32_t)((uint64_t)g.kt * (s + 1) / g.splits);
     f32x4 acc[Core::FM][Core::FN] = {};
     Core::run(g.a, g.b, t0, t1, 0, lds, acc);
-    Core::each(acc, lds, [&](uint32_t mi, uint32_t ni, float (&v)[8]) {
-        const uint64_t m = (uint64_t)g.a.row0 + mi, n = (uint64_t)g.b.row0 + ni;
-        if (m >= g.e.m || n >= g.e.n)
-            return;
-        if (g.splits > 1) {
-            const uint64_t left = g.e.n - n;
-            store_n<float, 8>(g.partial + ((uint64_t)s * g.e.m + m) * g.e.n + n,
-                              left < 8 ? (uint32_t)left : 8, g.e.n % 4 == 0, v);
-        } else {
-            finish<T, 8>(g.e, m, n, v);
-        }
-    });
+    const uint64_t m0 = g.a.row0, n0 = g.b.row0;
+    const bool whole = m0 + Core::BM <= g.e.m && n0 + Core::BN <= g.e.n;
+    auto nothing = [](uint32_t, uint32_t) { return 0; };
+    if (g.splits > 1) {
+        float *to = g.partial + ((uint64_t)s * g.e.m + m0) * g.e.n + n0;
+        if (whole && g.e.n % 4 == 0)
+            Core::each(acc, lds, nothing, [&](uint32_t mi, uint32_t ni, float (&v)[8], int) {
+                store8<true>(to + mi * g.e.n + ni, 8, v);
+            });
+        else
+            Core::template each<false, 1>(
+                acc, lds, nothing, [&](uint32_t mi, uint32_t ni, float (&v)[8], int) {
+                    if (m0 + mi < g.e.m && n0 + ni < g.e.n) {
+                        const uint64_t left = g.e.n - n0 - ni;
+                        store8<false>(to + mi * g.e.n + ni, left < 8 ? (uint32_t)left : 8u, v);
+                    }
+                });
+    } else if (whole && g.e.vec) {
+        Core::each(
+            acc, lds,
+            [&](uint32_t mi, uint32_t ni) { return fetch8<T, true>(g.e, m0 + mi, n0 + ni); },
+            [&](uint32_t mi, uint32_t ni, float (&v)[8], const Fetched &f) {
+                finish8<T, true>(g.e, m0 + mi, n0 + ni, v, f);
+            });
+    } else {
+        Core::template each<false, 1>(
+            acc, lds,
+            [&](uint32_t mi, uint32_t ni) { return fetch8<T, false>(g.e, m0 + mi, n0 + ni); },
+            [&](uint32_t mi, uint32_t ni, float (&v)[8], const Fetched &f) {
+                finish8<T, false>(g.e, m0 + mi, n0 + ni, v, f);
+            });
+    }
 }
 
 // The sums of the parts, in their order, and the epilogue.  8 columns a lane.
@@ -249,7 +299,9 @@ __global__ __launch_bounds__(256) void linear_join(Epilogue e, const float *part
         return;
     const uint64_t m = id / groups, n = id % groups * 8;
     const bool vec = e.n % 8 == 0;
+    const Fetched f = vec && e.vec ? fetch8<T, true>(e, m, n) : fetch8<T, false>(e, m, n);
     float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 4
     for (uint32_t s = 0; s < splits; ++s) {
         const float *p = partial + ((uint64_t)s * e.m + m) * e.n + n;
         if (vec) {
@@ -266,7 +318,10 @@ __global__ __launch_bounds__(256) void linear_join(Epilogue e, const float *part
                     v[i] += p[i];
         }
     }
-    finish<T, 8>(e, m, n, v);
+    if (vec && e.vec)
+        finish8<T, true>(e, m, n, v, f);
+    else
+        finish8<T, false>(e, m, n, v, f);
 }
 
 // Column sums of dz[m, n]: workgroup (c, s) sums columns 512 c .. + 512 over
@@ -342,7 +397,7 @@ uint64_t tiles(uint64_t m, uint64_t n, int t) {
 }
 
 Cut cut(uint64_t m, uint64_t n, uint64_t k) {
-    const uint64_t kt = (k + gemm::kBK - 1) / gemm::kBK;
+    const uint64_t kt = (k + 63) / 64;
     Cut c{0, 1};
     if (tiles(m, n, 0) < 192)
         c.tile = tiles(m, n, 1) >= 192 ? 1 : 2;
@@ -398,12 +453,17 @@ int launch(const GemmArgs &g, hipStream_t stream) {
 }
 
 template <class T, bool TRA, bool TRB, bool STAGED>
-int launch_tile(int tile, const GemmArgs &g, hipStream_t s) {
+int launch_tile(int tile, GemmArgs &g, uint64_t k, hipStream_t s) {
+    auto go = [&](auto core) {
+        using Core = decltype(core);
+        g.kt = (uint32_t)((k + Core::BK - 1) / Core::BK);
+        return launch<T, Core>(g, s);
+    };
     if (tile == 0)
-        return launch<T, gemm::Core<T, 256, 256, 2, 4, TRA, TRB, STAGED>>(g, s);
+        return go(gemm::Core<T, 256, 256, 2, 4, 64, 2, TRA, TRB, STAGED>());
     if (tile == 1)
-        return launch<T, gemm::Core<T, 128, 128, 2, 2, TRA, TRB, STAGED>>(g, s);
-    return launch<T, gemm::Core<T, 64, 64, 2, 2, TRA, TRB, STAGED>>(g, s);
+        return go(gemm::Core<T, 128, 128, 2, 2, 64, 2, TRA, TRB, STAGED>());
+    return go(gemm::Core<T, 64, 64, 2, 2, 64, 3, TRA, TRB, STAGED>());
 }
 
 template <class T, bool TRA, bool TRB>
@@ -416,16 +476,15 @@ int product(const Operand &a, const Operand &b, const Epilogue &e, uint64_t k, v
     const Cut c = cut(e.m, e.n, k);
     g.tm = (uint32_t)((e.m + kTile[c.tile] - 1) / kTile[c.tile]);
     g.tn = (uint32_t)((e.n + kTile[c.tile] - 1) / kTile[c.tile]);
-    g.kt = (uint32_t)((k + gemm::kBK - 1) / gemm::kBK);
-    g.splits = g.kt ? c.splits : 0;
+    g.splits = k ? c.splits : 0;
     g.partial = (float *)workspace;
-    if (g.kt) {
+    if (k) {
         // straight to LDS where every row of both starts on 16 bytes and the
         // contiguous extents are whole chunks
         const bool direct = aligned16(a.plane[0], a.ld, 2) && aligned16(b.plane[0], b.ld, 2)
                             && (TRA ? a.rows : k) % 8 == 0 && (TRB ? b.rows : k) % 8 == 0;
-        const int rc = direct ? launch_tile<T, TRA, TRB, false>(c.tile, g, s)
-                              : launch_tile<T, TRA, TRB, true>(c.tile, g, s);
+        const int rc = direct ? launch_tile<T, TRA, TRB, false>(c.tile, g, k, s)
+                              : launch_tile<T, TRA, TRB, true>(c.tile, g, k, s);
         if (rc || g.splits == 1)
             return rc;
     }

@@ -8,12 +8,13 @@
 // their shapes: a table names the matrix and the tile of every workgroup.
 //
 // Numbers.  The rounds amplify a rounding of X as they amplify its small
-// singular values (3.4445 a round), so one 16-bit product is not enough for
-// binary32 weights: with binary16 operands X ends 0.2% off, which is below
-// bfloat16's own rounding and is what 16-bit outputs get; the binary32 form
-// holds X, A and B as sums of two binary16 values (22 bits) and takes three
-// products, high*high + high*low + low*high, which ends as close as binary32
-// products do.  Values are kept times 2^14: no entry of X passes 1.3 and none
+// singular values (3.4445 a round), so one 16-bit product is not enough: with
+// binary16 operands alone X ends 0.2 to 0.4% off, more than bfloat16's own
+// rounding.  X, A and B are held as sums of two binary16 values (22 bits), and
+// a product takes three passes, high*high + high*low + low*high, which ends as
+// close as binary32 products do.  For bfloat16 results, whose rounding is
+// 0.17%, A takes one pass, A A three and B X two (B's low parts, not X's):
+// 0.11 to 0.15% off.  Values are kept times 2^14: no entry of X passes 1.3 and none
 // of A or B 2.9 in magnitude (the spectral norms bound them), so nothing
 // overflows binary16, and entries as small as 2^-28 are normal numbers.
 //
@@ -83,7 +84,7 @@ struct StepArgs {
     float *partial;
     uint32_t *tickets;
     int from;   // which of X's two copies is read
-    int passes; // 3: pairs of binary16; 1: the high halves alone
+    int passes; // of 3: see kPasses
     int last;
 };
 
@@ -109,14 +110,6 @@ __device__ __forceinline__ void store_pair(uint16_t *hi, uint16_t *lo, uint64_t 
     *(f16x8 *)(hi + at) = h;
     *(f16x8 *)(lo + at) = l;
 }
-__device__ __forceinline__ void load_pair(const uint16_t *hi, const uint16_t *lo, uint64_t at,
-                                          float (&v)[8]) {
-    const f16x8 h = *(const f16x8 *)(hi + at), l = *(const f16x8 *)(lo + at);
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        v[e] = (float)h[e] + (float)l[e];
-}
-
 // the momentum, and the sum of squares of U over each chunk
 template <class G>
 __global__ __launch_bounds__(256) void norm_kernel(const Chunk *chunks, Update u,
@@ -215,6 +208,8 @@ __global__ __launch_bounds__(256) void normalise_kernel(const Mat *mats, const W
 }
 
 enum { kGram, kPoly, kApply };
+// passes of each product, by form: bfloat16 results, all others
+constexpr int kPasses[2][3] = {{1, 3, 2}, {3, 3, 3}};
 
 // 8 results of the last round, from element `at` of the flat buffers on.
 template <class G>
@@ -280,9 +275,57 @@ __device__ __forceinline__ void apply_update(const Update &u, const Replicas &r,
     }
 }
 
-// One product over the tiles of every matrix.  A tile whose k is dealt to
-// several workgroups is finished by the last of them to arrive, which adds
-// the parts in their order, so the sums do not depend on who that is.
+// The sums of a tile whose k is dealt to several workgroups: each leaves its
+// part in memory and takes a ticket; the last has all of them, added in their
+// order.  False for the others.  The parts travel past the caches (agent-scope
+// accesses, complete before the ticket is drawn), since a fence at that scope
+// would write back and empty the die's L2 under the workgroups beside it.
+template <class Core>
+__device__ __forceinline__ bool join_parts(const StepArgs &p, const Work &w,
+                                           f32x4 (&acc)[Core::FM][Core::FN], uint32_t &arrived) {
+    constexpr uint32_t N = Core::FM * Core::FN;
+    typedef unsigned long long U;
+    U *slot = (U *)p.partial + (uint64_t)w.slot * N * 2 * Core::THREADS + threadIdx.x;
+    U *mine = slot + (uint64_t)w.part * N * 2 * Core::THREADS;
+    struct Two {
+        U v[2];
+    };
+#pragma unroll
+    for (uint32_t i = 0; i < N; ++i) {
+        const Two two = __builtin_bit_cast(Two, acc[i / Core::FN][i % Core::FN]);
+#pragma unroll
+        for (uint32_t h = 0; h < 2; ++h)
+            __hip_atomic_store(mine + (i * 2 + h) * Core::THREADS, two.v[h], __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_AGENT);
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (threadIdx.x == 0)
+        arrived = __hip_atomic_fetch_add(p.tickets + w.ticket, 1u, __ATOMIC_RELAXED,
+                                         __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    if (arrived != (uint32_t)w.parts - 1)
+        return false;
+    if (threadIdx.x == 0)  // for the next launch
+        __hip_atomic_store(p.tickets + w.ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    for (uint32_t q = 0; q < w.parts; ++q) {
+#pragma unroll
+        for (uint32_t i = 0; i < N; ++i) {
+            Two two;
+#pragma unroll
+            for (uint32_t h = 0; h < 2; ++h)
+                two.v[h] = __hip_atomic_load(slot + (i * 2 + h) * Core::THREADS,
+                                             __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            f32x4 &to = acc[i / Core::FN][i % Core::FN];
+            const f32x4 from = __builtin_bit_cast(f32x4, two);
+            to = q ? to + from : from;
+        }
+        slot += (uint64_t)N * 2 * Core::THREADS;
+    }
+    return true;
+}
+
+// One product over the tiles of every matrix.
 template <class Core, int KIND, class G>
 __global__ __launch_bounds__(Core::THREADS) void product_kernel(StepArgs p, Update u,
                                                                 Replicas r) {
@@ -315,102 +358,92 @@ __global__ __launch_bounds__(Core::THREADS) void product_kernel(StepArgs p, Upda
     }
     right.ld = KIND == kPoly ? t.sp : t.lp;
     right.k = left.k;
-    const uint32_t kt = (uint32_t)(left.k / gemm::kBK), all = kt * p.passes;
+    const uint32_t kt = (uint32_t)(left.k / Core::BK), all = kt * p.passes;
+    const uint32_t skipped = kt * (3 - p.passes);
     f32x4 acc[Core::FM][Core::FN] = {};
-    Core::run(left, right, all * w.part / w.parts, all * (w.part + 1) / w.parts,
-              p.passes == 3 ? kt : 0, lds, acc);
-    if (w.parts > 1) {
-        constexpr uint32_t N = Core::FM * Core::FN;
-        f32x4 *mine = (f32x4 *)p.partial + (uint64_t)(w.slot + w.part) * N * Core::THREADS;
-#pragma unroll
-        for (uint32_t i = 0; i < N; ++i)
-            mine[i * Core::THREADS + threadIdx.x] = acc[i / Core::FN][i % Core::FN];
-        __threadfence();
-        __syncthreads();
-        if (threadIdx.x == 0)
-            arrived = __hip_atomic_fetch_add(p.tickets + w.ticket, 1u, __ATOMIC_ACQ_REL,
-                                             __HIP_MEMORY_SCOPE_AGENT);
-        __syncthreads();
-        if (arrived != (uint32_t)w.parts - 1)
-            return;
-        __threadfence();
-        if (threadIdx.x == 0)  // for the next launch
-            __hip_atomic_store(p.tickets + w.ticket, 0u, __ATOMIC_RELAXED,
-                               __HIP_MEMORY_SCOPE_AGENT);
-        const f32x4 *part = (const f32x4 *)p.partial + (uint64_t)w.slot * N * Core::THREADS;
-#pragma unroll
-        for (uint32_t i = 0; i < N; ++i)
-            acc[i / Core::FN][i % Core::FN] = part[i * Core::THREADS + threadIdx.x];
-        for (uint32_t q = 1; q < w.parts; ++q) {
-            part += N * Core::THREADS;
-#pragma unroll
-            for (uint32_t i = 0; i < N; ++i)
-                acc[i / Core::FN][i % Core::FN] += part[i * Core::THREADS + threadIdx.x];
-        }
-    }
+    Core::run(left, right, skipped + all * w.part / w.parts,
+              skipped + all * (w.part + 1) / w.parts, kt, lds, acc);
+    if (w.parts > 1 && !join_parts<Core>(p, w, acc, arrived))
+        return;
+    struct Pair {
+        f16x8 h, l;
+    };
+    auto pair_at = [](const uint16_t *hi, uint64_t low, uint64_t at) {
+        return Pair{*(const f16x8 *)(hi + at), *(const f16x8 *)(hi + low + at)};
+    };
+    const uint32_t m0 = left.row0, n0 = right.row0;
     if constexpr (KIND == kApply) {
-        auto next = [&](uint32_t m, uint32_t n, float (&v)[8]) {
-            float old[8];
-            load_pair(x, x + nx, (uint64_t)m * t.lp + n, old);
+        auto old = [&](uint32_t mi, uint32_t ni) {
+            return pair_at(x, nx, (uint64_t)(m0 + mi) * t.lp + n0 + ni);
+        };
+        auto next = [&](float (&v)[8], const Pair &o) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                v[e] = kA * old[e] + v[e] * kUnscale;
+                v[e] = kA * ((float)o.h[e] + (float)o.l[e]) + v[e] * kUnscale;
         };
         if (!p.last) {
-            Core::each(acc, lds, [&](uint32_t mi, uint32_t ni, float (&v)[8]) {
-                const uint32_t m = left.row0 + mi, n = right.row0 + ni;
-                next(m, n, v);
-                store_pair(y, y + nx, (uint64_t)m * t.lp + n, v);
+            Core::each(acc, lds, old, [&](uint32_t mi, uint32_t ni, float (&v)[8], const Pair &o) {
+                next(v, o);
+                store_pair(y, y + nx, (uint64_t)(m0 + mi) * t.lp + n0 + ni, v);
             });
         } else if (!t.tall) {
-            Core::each(acc, lds, [&](uint32_t mi, uint32_t ni, float (&v)[8]) {
-                const uint32_t m = left.row0 + mi, n = right.row0 + ni;
+            Core::each(acc, lds, old, [&](uint32_t mi, uint32_t ni, float (&v)[8], const Pair &o) {
+                const uint32_t m = m0 + mi, n = n0 + ni;
                 if (m >= t.s || n >= t.l)
                     return;
-                next(m, n, v);
+                next(v, o);
                 apply_update<G>(u, r, t.at + (uint64_t)m * t.cols + n,
                                 t.l - n < 8 ? t.l - n : 8, u.lr * t.scale, v);
             });
         } else {
-            Core::template each<true>(acc, lds, [&](uint32_t mi, uint32_t ni, float (&v)[8]) {
-                const uint32_t m = left.row0 + mi, n = right.row0 + ni;
-                if (m >= t.s || n >= t.l)
-                    return;
-                const _Float16 *h = (const _Float16 *)x + (uint64_t)m * t.lp + n;
+            Core::template each<true>(
+                acc, lds,
+                [&](uint32_t mi, uint32_t ni) {
+                    const _Float16 *h = (const _Float16 *)x + (uint64_t)(m0 + mi) * t.lp + n0 + ni;
+                    Pair o;
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    v[e] = kA * ((float)h[(uint64_t)e * t.lp] + (float)h[nx + (uint64_t)e * t.lp])
-                           + v[e] * kUnscale;
-                apply_update<G>(u, r, t.at + (uint64_t)n * t.cols + m,
-                                t.s - m < 8 ? t.s - m : 8, u.lr * t.scale, v);
-            });
+                    for (int e = 0; e < 8; ++e) {
+                        o.h[e] = h[(uint64_t)e * t.lp];
+                        o.l[e] = h[nx + (uint64_t)e * t.lp];
+                    }
+                    return o;
+                },
+                [&](uint32_t mi, uint32_t ni, float (&v)[8], const Pair &o) {
+                    const uint32_t m = m0 + mi, n = n0 + ni;
+                    if (m >= t.s || n >= t.l)
+                        return;
+                    next(v, o);
+                    apply_update<G>(u, r, t.at + (uint64_t)n * t.cols + m,
+                                    t.s - m < 8 ? t.s - m : 8, u.lr * t.scale, v);
+                });
         }
     } else {
         uint16_t *o = KIND == kGram ? a : b;
-        auto value = [&](uint64_t at, float (&v)[8]) {
-            if (KIND == kGram) {
+        // the results of row m (or, A being symmetric, of column m) at `at`
+        auto fetch = [&](uint64_t at) { return KIND == kGram ? Pair{} : pair_at(a, na, at); };
+        auto put = [&](uint64_t at, float (&v)[8], const Pair &q) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    v[e] *= kUnscale;
-            } else {
-                float old[8];
-                load_pair(a, a + na, at, old);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    v[e] = kB * old[e] + kC * (v[e] * kUnscale);
-            }
-        };
-        Core::each(acc, lds, [&](uint32_t mi, uint32_t ni, float (&v)[8]) {
-            const uint64_t at = (uint64_t)(left.row0 + mi) * t.sp + right.row0 + ni;
-            value(at, v);
+            for (int e = 0; e < 8; ++e)
+                v[e] = KIND == kGram
+                           ? v[e] * kUnscale
+                           : kB * ((float)q.h[e] + (float)q.l[e]) + kC * (v[e] * kUnscale);
             store_pair(o, o + na, at, v);
-        });
-        if (w.ti != w.tj)  // the mirror image
-            Core::template each<true>(acc, lds, [&](uint32_t mi, uint32_t ni, float (&v)[8]) {
-                const uint64_t at = (uint64_t)(right.row0 + ni) * t.sp + left.row0 + mi;
-                value(at, v);  // A is symmetric
-                store_pair(o, o + na, at, v);
+        };
+        auto row = [&](uint32_t mi, uint32_t ni) { return (uint64_t)(m0 + mi) * t.sp + n0 + ni; };
+        auto column = [&](uint32_t mi, uint32_t ni) {
+            return (uint64_t)(n0 + ni) * t.sp + m0 + mi;
+        };
+        Core::each(
+            acc, lds, [&](uint32_t mi, uint32_t ni) { return fetch(row(mi, ni)); },
+            [&](uint32_t mi, uint32_t ni, float (&v)[8], const Pair &q) {
+                put(row(mi, ni), v, q);
             });
+        if (w.ti != w.tj)  // the mirror image
+            Core::template each<true>(
+                acc, lds, [&](uint32_t mi, uint32_t ni) { return fetch(column(mi, ni)); },
+                [&](uint32_t mi, uint32_t ni, float (&v)[8], const Pair &q) {
+                    put(column(mi, ni), v, q);
+                });
     }
 }
 
@@ -431,9 +464,10 @@ struct ddl_muon_s {
     std::vector<Mat> mats;
     std::vector<Chunk> chunks;
     std::vector<Work> blocks;       // normalise
-    // the products' tables, for one pass over k and for three
+    // the products' tables, by form (kPasses)
     std::vector<Work> gram[2], poly[2], apply[2];
     uint32_t tile = 64;
+    bool small = true;  // no side above 128
     uint64_t ws = 0;     // elements of the workspace
     uint64_t slots = 0;  // partial tiles
     uint32_t tickets = 0;
@@ -464,7 +498,7 @@ void deal(ddl_muon_s &h, int kind, int passes, std::vector<Work> &out) {
     };
     uint64_t steps = 0;  // k tiles over all tiles
     auto depth = [&](const Mat &m) {
-        return (uint64_t)(kind == kGram ? m.lp : m.sp) / gemm::kBK * passes;
+        return (uint64_t)(kind == kGram ? m.lp : m.sp) / 64 * passes;
     };
     for (const Mat &m : h.mats)
         count(m, [&](uint32_t, uint32_t) {
@@ -494,14 +528,27 @@ void deal(ddl_muon_s &h, int kind, int passes, std::vector<Work> &out) {
 }
 
 void lay_out(ddl_muon_s &h) {
-    uint64_t large = 0, middle = 0;
-    for (const Mat &m : h.mats) {
-        large += (uint64_t)up(m.s, 256) / 256 * (up(m.l, 256) / 256);
-        middle += (uint64_t)up(m.s, 128) / 128 * (up(m.l, 128) / 128);
+    // The tile size whose products take the least time, by the padded work and
+    // the rates that full cards of tiles reach (TFLOP/s: 1200, 1060 and 700),
+    // of which fewer tiles than compute units reach their share.
+    double best = 0;
+    for (uint32_t T : {256u, 128u, 64u}) {
+        double work = 0, tiles = 0;
+        for (const Mat &m : h.mats) {
+            const double s = up(m.s, T), l = up(m.l, T);
+            work += 3 * s * s * l + s * s * s;
+            tiles += s / T * (l / T);
+        }
+        const double rate = (T == 256 ? 1200 : T == 128 ? 1060 : 700)
+                            * std::min(1.0, tiles / (T == 64 ? 512 : 256));
+        if (!best || work / rate < best) {
+            best = work / rate;
+            h.tile = T;
+        }
     }
-    h.tile = large >= 256 ? 256 : middle >= 64 ? 128 : 64;
     for (uint32_t i = 0; i < h.mats.size(); ++i) {
         Mat &m = h.mats[i];
+        h.small = h.small && m.l <= 128;
         m.sp = up(m.s, h.tile);
         m.lp = up(m.l, h.tile);
         m.x = h.ws;
@@ -518,10 +565,9 @@ void lay_out(ddl_muon_s &h) {
                 h.blocks.push_back({i, (uint16_t)a, (uint16_t)b, 0, 1, 0, 0});
     }
     for (int f = 0; f < 2; ++f) {
-        const int passes = f ? 3 : 1;
-        deal(h, kGram, passes, h.gram[f]);
-        deal(h, kPoly, passes, h.poly[f]);
-        deal(h, kApply, passes, h.apply[f]);
+        deal(h, kGram, kPasses[f][kGram], h.gram[f]);
+        deal(h, kPoly, kPasses[f][kPoly], h.poly[f]);
+        deal(h, kApply, kPasses[f][kApply], h.apply[f]);
     }
 }
 
@@ -574,24 +620,27 @@ int launch_product(const StepArgs &p, const Update &u, const Replicas &r, hipStr
 template <int T, class G>
 int rounds(ddl_muon_s &h, const Update &u, const Replicas &r, int f, hipStream_t s) {
     constexpr int WR = 2, WC = T == 256 ? 4 : 2;
-    using Rows = gemm::Core<gemm::Half, T, T, WR, WC, false, false, false>;
-    using Cols = gemm::Core<gemm::Half, T, T, WR, WC, false, true, false>;
+    constexpr int BK = 64, S = T == 64 ? 3 : 2;
+    using Rows = gemm::Core<gemm::Half, T, T, WR, WC, BK, S, false, false, false>;
+    using Cols = gemm::Core<gemm::Half, T, T, WR, WC, BK, S, false, true, false>;
     StepArgs p;
     p.mats = h.d_mats;
     p.ws = h.d_ws;
     p.partial = h.d_partial;
     p.tickets = h.d_tickets;
-    p.passes = f ? 3 : 1;
     int rc = DDL_OK;
     for (int i = 0; i < kRounds && !rc; ++i) {
         p.from = i & 1;
         p.last = i == kRounds - 1;
+        p.passes = kPasses[f][kGram];
         p.work = h.d_gram[f];
         p.count = (uint32_t)h.gram[f].size();
         rc = launch_product<Rows, kGram, float>(p, u, r, s);
+        p.passes = kPasses[f][kPoly];
         p.work = h.d_poly[f];
         p.count = (uint32_t)h.poly[f].size();
         rc = rc ? rc : launch_product<Rows, kPoly, float>(p, u, r, s);
+        p.passes = kPasses[f][kApply];
         p.work = h.d_apply[f];
         p.count = (uint32_t)h.apply[f].size();
         rc = rc ? rc : launch_product<Cols, kApply, G>(p, u, r, s);
@@ -705,7 +754,9 @@ int ddl_muon_orthogonalise(ddl_muon h, const void *grad, void *out, int dtype, v
     u.out = out;
     u.vec = !(((uintptr_t)grad | (uintptr_t)out) % 16);
     Replicas r = {};
-    return run_typed(*h, dtype, u, r, dtype == DDL_F32, stream);
+    // small matrices, where launches are all the time, take the exacter form
+    const int f = dtype != DDL_BF16 || h->small;
+    return run_typed(*h, dtype, u, r, f, stream);
 }
 
 int ddl_muon_step(ddl_muon h, const void *grad, int grad_dtype, float *momentum,
