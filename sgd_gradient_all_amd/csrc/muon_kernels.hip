@@ -331,10 +331,12 @@ __global__ __launch_bounds__(Core::THREADS) void product_kernel(StepArgs p, Upda
                                                                 Replicas r) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     __shared__ uint32_t arrived;
-    // consecutive entries of the table on one die, which share operands
-    constexpr uint32_t kDies = 8;
-    const uint32_t die = blockIdx.x % kDies, per = p.count / kDies, more = p.count % kDies;
-    const Work w = p.work[die * per + (die < more ? die : more) + blockIdx.x / kDies];
+    // Workgroups go round the 8 dies; runs of 8 entries, which share operands,
+    // stay on one.  The table has the longest sums first.
+    uint32_t entry = blockIdx.x;
+    if ((entry | 63u) < p.count)
+        entry = (entry & ~63u) | (entry & 7u) << 3 | (entry >> 3 & 7u);
+    const Work w = p.work[entry];
     const Mat t = p.mats[w.mat];
     const uint64_t nx = (uint64_t)t.sp * t.lp, na = (uint64_t)t.sp * t.sp;
     uint16_t *x = p.ws + t.x + p.from * 2 * nx, *y = p.ws + t.x + (p.from ^ 1) * 2 * nx;
@@ -509,7 +511,13 @@ void deal(ddl_muon_s &h, int kind, int passes, std::vector<Work> &out) {
     const uint64_t share = std::max<uint64_t>((steps + 511) / 512, 16);
     uint64_t slots = 0;
     uint32_t tickets = 0;
-    for (uint32_t i = 0; i < h.mats.size(); ++i) {
+    std::vector<uint32_t> order(h.mats.size());
+    for (uint32_t i = 0; i < order.size(); ++i)
+        order[i] = i;
+    std::stable_sort(order.begin(), order.end(), [&](uint32_t x, uint32_t y) {
+        return depth(h.mats[x]) > depth(h.mats[y]);
+    });
+    for (uint32_t i : order) {
         const uint64_t d = depth(h.mats[i]);
         const uint16_t parts =
             tiles >= 512 ? 1 : (uint16_t)std::max<uint64_t>(1, std::min<uint64_t>(d / share, 32));
@@ -528,24 +536,17 @@ void deal(ddl_muon_s &h, int kind, int passes, std::vector<Work> &out) {
 }
 
 void lay_out(ddl_muon_s &h) {
-    // The tile size whose products take the least time, by the padded work and
-    // the rates that full cards of tiles reach (TFLOP/s: 1200, 1060 and 700),
-    // of which fewer tiles than compute units reach their share.
-    double best = 0;
-    for (uint32_t T : {256u, 128u, 64u}) {
-        double work = 0, tiles = 0;
-        for (const Mat &m : h.mats) {
-            const double s = up(m.s, T), l = up(m.l, T);
-            work += 3 * s * s * l + s * s * s;
-            tiles += s / T * (l / T);
-        }
-        const double rate = (T == 256 ? 1200 : T == 128 ? 1060 : 700)
-                            * std::min(1.0, tiles / (T == 64 ? 512 : 256));
-        if (!best || work / rate < best) {
-            best = work / rate;
-            h.tile = T;
-        }
-    }
+    // The largest tile of which A's lower triangles still give every other
+    // compute unit one (128, 64) or all of them (256): with fewer, the sums
+    // over k are cut into more parts, and joining those costs more than the
+    // larger tile saves (the matrices of ResNet-50: TILES).
+    auto triangles = [&](uint32_t T) {
+        uint64_t n = 0;
+        for (const Mat &m : h.mats)
+            n += (uint64_t)(up(m.s, T) / T) * (up(m.s, T) / T + 1) / 2;
+        return n;
+    };
+    h.tile = triangles(256) >= 256 ? 256 : triangles(128) >= 32 ? 128 : 64;
     for (uint32_t i = 0; i < h.mats.size(); ++i) {
         Mat &m = h.mats[i];
         h.small = h.small && m.l <= 128;

@@ -1,0 +1,202 @@
+"""The linear layer and the optimizers without a GPU: sizes, refusals, handles."""
+import ctypes
+
+import pytest
+import torch
+
+import sgd_gradient_all_amd as ddl
+from sgd_gradient_all_amd import _operators as ops
+
+E_NULL, E_ARG, E_BUCKETS, E_ALIGN, E_SCRATCH = -1, -2, -3, -4, -10
+# an address that is only checked, never used: every call below is refused
+SOME = 1 << 20
+
+
+def lib():
+    return ops._lib()
+
+
+def forward_args(**kw):
+    a = ops.ddl_linear_args()
+    a.m, a.n, a.k, a.dtype, a.act = 4, 8, 16, ddl.DDL_F16, 0
+    a.x, a.ldx, a.w, a.ldw, a.y, a.ldy = SOME, 16, SOME, 16, SOME, 8
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dtype=ddl.DDL_F32), E_ARG), (dict(dtype=7), E_ARG), (dict(act=5), E_ARG),
+    (dict(act=-1), E_ARG), (dict(n=(1 << 22) + 1), E_ARG), (dict(m=(1 << 30) + 1), E_ARG),
+    (dict(ldx=15), E_ARG), (dict(ldw=15), E_ARG), (dict(ldy=7), E_ARG),
+    (dict(residual=SOME, ldr=7), E_ARG), (dict(z=SOME, ldz=7), E_ARG),
+    (dict(x=None), E_NULL), (dict(w=None), E_NULL), (dict(y=None), E_NULL),
+    (dict(x=SOME + 1), E_ALIGN), (dict(bias=SOME + 1), E_ALIGN), (dict(y=SOME + 1), E_ALIGN),
+])
+def test_linear_refusals(kw, code):
+    assert lib().ddl_linear(ctypes.byref(forward_args(**kw)), None, 0, None) == code
+
+
+def test_null_arguments():
+    assert lib().ddl_linear(None, None, 0, None) == E_NULL
+    assert lib().ddl_linear_dgrad(None, None, 0, None) == E_NULL
+    assert lib().ddl_linear_wgrad(None, None, 0, None) == E_NULL
+    assert lib().ddl_linear_workspace(0, 1, 1, 1, None) == E_NULL
+
+
+def test_dgrad_refusals():
+    def call(**kw):
+        a = ops.ddl_dgrad_args()
+        a.m, a.n, a.k, a.dtype, a.act = 4, 8, 16, ddl.DDL_BF16, 0
+        a.dz, a.lddz, a.w, a.ldw, a.dx, a.lddx = SOME, 8, SOME, 16, SOME, 16
+        for k, v in kw.items():
+            setattr(a, k, v)
+        return lib().ddl_linear_dgrad(ctypes.byref(a), None, 0, None)
+    assert call(act=1) == E_NULL  # an activation without z_prev
+    assert call(z_prev=SOME, ldz_prev=16) == E_NULL  # without dz_prev
+    assert call(z_prev=SOME, ldz_prev=15, dz_prev=SOME, lddz_prev=16) == E_ARG
+    assert call(lddx=15) == E_ARG
+    assert call(dx=SOME + 1) == E_ALIGN
+
+
+def test_wgrad_refusals():
+    def call(**kw):
+        a = ops.ddl_wgrad_args()
+        a.m, a.n, a.k, a.dtype, a.out_dtype = 4, 8, 16, ddl.DDL_BF16, ddl.DDL_F32
+        a.dz, a.lddz, a.x, a.ldx, a.dw, a.lddw = SOME, 8, SOME, 16, SOME, 16
+        ws, size = kw.pop("workspace", (SOME, 1 << 30))
+        for k, v in kw.items():
+            setattr(a, k, v)
+        return lib().ddl_linear_wgrad(ctypes.byref(a), ws, size, None)
+    assert call(out_dtype=ddl.DDL_F16) == E_ARG  # neither f32 nor the operands' type
+    assert call(accumulate=2) == E_ARG
+    assert call(dw=None) == E_NULL
+    assert call(dw=SOME + 2) == E_ALIGN  # f32 wants 4
+    assert call(workspace=(None, 0)) == E_NULL
+    assert call(workspace=(SOME, 1)) == E_SCRATCH
+    assert call(workspace=(SOME + 8, 1 << 30)) == E_ALIGN
+
+
+def test_empty_outputs_need_nothing():
+    assert lib().ddl_linear(ctypes.byref(forward_args(m=0, x=None, y=None)), None, 0, None) == 0
+    assert lib().ddl_linear(ctypes.byref(forward_args(n=0, w=None, y=None)), None, 0, None) == 0
+
+
+def test_workspace_sizes():
+    assert ddl.linear_workspace("forward", 8192, 16384, 4096) == 0  # the card is full as it is
+    assert ddl.linear_workspace("forward", 0, 16, 16) == 0
+    assert ddl.linear_workspace("wgrad", 100, 64, 64) >= 64 * 4  # db's partial sums
+    # parts of a sum are cut only where they cost less than 64 outputs' worth
+    one = ddl.linear_workspace("forward", 1, 4096, 4096)
+    assert 0 <= one <= 64 * 4096 * 4 + 256
+    with pytest.raises(ValueError):
+        ddl.linear_workspace("backward", 1, 1, 1)
+    with pytest.raises(ValueError):
+        ddl.linear_workspace("forward", -1, 1, 1)
+    with pytest.raises(ddl.DDLError) as e:
+        ddl.linear_workspace("forward", 1, 1 << 23, 1)
+    assert e.value.code == E_ARG
+
+
+def test_python_refuses_cpu_tensors_and_shapes():
+    x, w, y = torch.zeros(2, 3).half(), torch.zeros(4, 3).half(), torch.zeros(2, 4).half()
+    with pytest.raises(ValueError, match="GPU tensor"):
+        ddl.linear(x, w, y)
+    with pytest.raises(ValueError, match="shape"):
+        ddl.linear(x[0], w, y)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        ddl.linear_dgrad(y, w, x)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        ddl.linear_wgrad(y, x, w)
+    with pytest.raises(ValueError, match="activation"):
+        ops._act("tanh")
+    a = ddl.AdamW([(0, 4)])
+    v = torch.zeros(4)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        a.step(v, v, v, [v], lr=1.0)
+    m = ddl.Muon([(0, 2, 2, 1.0)])
+    with pytest.raises(ValueError, match="GPU tensor"):
+        m.orthogonalise(v, v)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        m.step(v, v, [v], lr=1.0)
+
+
+def test_handles():
+    a = ddl.AdamW([(5, 7), (12, 0), (20, 3)])
+    assert a.need == 23
+    h = a.handle
+    a.destroy()
+    a.destroy()  # twice is once
+    assert lib().ddl_adamw_destroy(h) == E_ARG  # not a live handle
+    assert lib().ddl_adamw_destroy(None) == E_NULL
+    m = ddl.Muon([(0, 3, 5, 1.0), (15, 5, 3, 2.0), (30, 0, 4, 1.0)])
+    assert m.need == 30
+    h = m.handle
+    m.destroy()
+    assert lib().ddl_muon_destroy(h) == E_ARG
+    assert lib().ddl_muon_orthogonalise(h, SOME, SOME, 0, None) == E_ARG
+    for spans in ([(0, 8), (7, 2)], [(0, 1 << 41)], [(4, 2), (4, 2)]):
+        with pytest.raises(ddl.DDLError) as e:
+            ddl.AdamW(spans)
+        assert e.value.code == E_BUCKETS
+    with pytest.raises(ddl.DDLError) as e:
+        ddl.Muon([(0, 4, 4, 1.0), (15, 2, 2, 1.0)])
+    assert e.value.code == E_BUCKETS
+    for bad in ((0, 1 << 17, 2, 1.0), (0, 2, 2, float("nan")), (0, 2, 2, float("inf"))):
+        with pytest.raises(ddl.DDLError) as e:
+            ddl.Muon([bad])
+        assert e.value.code == E_ARG
+    with pytest.raises(ValueError):
+        ddl.Muon([(0, -1, 2, 1.0)])
+    with pytest.raises(ValueError):
+        ddl.AdamW([(-1, 2)])
+    ddl.AdamW([]).destroy()
+    ddl.Muon([]).destroy()
+
+
+def adamw_call(h, **kw):
+    d = dict(grad=SOME, type=0, m=SOME, v=SOME, w=[SOME], copy=None, copy_type=0, lr=1e-3,
+             b1=0.9, b2=0.99, eps=1e-8, wd=0.0, step=1)
+    d.update(kw)
+    w = (ctypes.c_void_p * max(1, len(d["w"])))(*d["w"])
+    return lib().ddl_adamw_step(h, d["grad"], d["type"], d["m"], d["v"], w, len(d["w"]),
+                                d["copy"], d["copy_type"], d["lr"], d["b1"], d["b2"], d["eps"],
+                                d["wd"], d["step"], None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(type=3), E_ARG), (dict(step=0), E_ARG), (dict(b1=1.0), E_ARG), (dict(b2=-0.1), E_ARG),
+    (dict(eps=-1.0), E_ARG), (dict(lr=float("nan")), E_ARG), (dict(wd=float("inf")), E_ARG),
+    (dict(w=[]), E_ARG), (dict(copy=SOME, copy_type=0), E_ARG), (dict(grad=None), E_NULL),
+    (dict(m=None), E_NULL), (dict(w=[SOME, None]), E_NULL), (dict(m=SOME + 2), E_ALIGN),
+    (dict(w=[SOME + 1]), E_ALIGN), (dict(copy=SOME + 1, copy_type=1), E_ALIGN),
+])
+def test_adamw_refusals(kw, code):
+    a = ddl.AdamW([(0, 4)])
+    assert adamw_call(a.handle, **kw) == code
+
+
+def test_nothing_to_step_is_no_work():
+    assert adamw_call(ddl.AdamW([]).handle, grad=None, m=None, v=None, w=[SOME]) == 0
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(type=3), E_ARG), (dict(lr=float("nan")), E_ARG), (dict(nesterov=2), E_ARG),
+    (dict(mu=float("inf")), E_ARG), (dict(w=[]), E_ARG), (dict(grad=None), E_NULL),
+    (dict(momentum=None), E_NULL), (dict(grad=SOME + 1), E_ALIGN),
+    (dict(copy=SOME, copy_type=0), E_ARG),
+])
+def test_muon_refusals(kw, code):
+    h = ddl.Muon([(0, 2, 2, 1.0)])
+    d = dict(grad=SOME, type=0, momentum=SOME, w=[SOME], copy=None, copy_type=0, lr=1e-3, mu=0.9,
+             nesterov=1)
+    d.update(kw)
+    w = (ctypes.c_void_p * max(1, len(d["w"])))(*d["w"])
+    assert lib().ddl_muon_step(h.handle, d["grad"], d["type"], d["momentum"], w, len(d["w"]),
+                               d["copy"], d["copy_type"], d["lr"], d["mu"], d["nesterov"], 0.0,
+                               None) == code
+
+
+def test_exchange_still_refuses_bfloat16():
+    with pytest.raises(ddl.DDLError):
+        ddl.Plan(2, 16, ddl.DDL_BF16)
