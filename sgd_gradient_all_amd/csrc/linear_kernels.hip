@@ -324,22 +324,83 @@ __global__ __launch_bounds__(256) void linear_join(Epilogue e, const float *part
         finish8<T, false>(e, m, n, v, f);
 }
 
-// Column sums of dz[m, n]: workgroup (c, s) sums columns 512 c .. + 512 over
-// the rows of slice s, its four waves every fourth row each.
+// A few rows (a decoded token, or up to 16): the weights are read once and
+// bound the time, so every lane loads them straight into the matrix
+// instruction's registers, without LDS.  A workgroup of 8 waves takes 16
+// columns, each wave an eighth of k; the waves' sums are added in their order.
+constexpr int kSkinnyWaves = 8;
+constexpr uint64_t kSkinnyRows = 16;
+
 template <class T>
+__global__ __launch_bounds__(kSkinnyWaves * 64) void skinny_kernel(Operand x, Operand w,
+                                                                   Epilogue e) {
+    __shared__ f32x4 sums[kSkinnyWaves][16][5];  // [wave][m][n / 4], a chunk of padding
+    const uint32_t l = threadIdx.x & 63u, wave = threadIdx.x >> 6, r = l & 15u, g = l >> 4;
+    const uint32_t n0 = blockIdx.x * 16;
+    const uint32_t steps = (uint32_t)((w.k + 31) / 32);
+    const uint32_t s0 = steps * wave / kSkinnyWaves, s1 = steps * (wave + 1) / kSkinnyWaves;
+    // rows past the end repeat the last one; their results are not stored
+    const uint32_t rw = n0 + r < w.rows ? n0 + r : w.rows - 1, rx = r < x.rows ? r : x.rows - 1;
+    const uint16_t *pw = w.plane[0] + (uint64_t)rw * w.ld + g * 8;
+    const uint16_t *px = x.plane[0] + (uint64_t)rx * x.ld + g * 8;
+    f32x4 acc = {0, 0, 0, 0};
+    constexpr uint32_t U = 8;
+    uint32_t s = s0;
+    for (; s + U <= s1 && (uint64_t)(s + U) * 32 <= w.k; s += U) {
+        gemm::s16x8 a[U], b[U];
+#pragma unroll
+        for (uint32_t i = 0; i < U; ++i) {
+            b[i] = *(const gemm::s16x8 *)(pw + (uint64_t)(s + i) * 32);
+            a[i] = *(const gemm::s16x8 *)(px + (uint64_t)(s + i) * 32);
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < U; ++i)
+            acc = T::mfma(b[i], a[i], acc);
+    }
+    for (; s < s1; ++s) {
+        gemm::s16x8 a = {}, b = {};
+        if ((uint64_t)s * 32 + g * 8 < w.k) {  // k is a multiple of 8
+            b = *(const gemm::s16x8 *)(pw + (uint64_t)s * 32);
+            a = *(const gemm::s16x8 *)(px + (uint64_t)s * 32);
+        }
+        acc = T::mfma(b, a, acc);
+    }
+    sums[wave][r][g] = acc;
+    __syncthreads();
+    const uint32_t m = threadIdx.x >> 1, h = threadIdx.x & 1u;
+    if (threadIdx.x >= 32 || m >= e.m || n0 + h * 8 >= e.n)
+        return;
+    const bool vec = e.vec && n0 + h * 8 + 8 <= e.n;
+    const Fetched f = vec ? fetch8<T, true>(e, m, n0 + h * 8) : fetch8<T, false>(e, m, n0 + h * 8);
+    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+    for (int q = 0; q < kSkinnyWaves; ++q)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] += sums[q][m][h * 2 + i / 4][i % 4];
+    if (vec)
+        finish8<T, true>(e, m, n0 + h * 8, v, f);
+    else
+        finish8<T, false>(e, m, n0 + h * 8, v, f);
+}
+
+// Column sums of dz[m, n]: workgroup (c, s) sums 64 columns over the rows of
+// slice s, 8 lanes by 32 row groups.  One slice writes db itself, several
+// leave their sums to column_join.
+template <class T, class O>
 __global__ __launch_bounds__(256) void column_sums(const typename T::E *dz, uint64_t ld,
                                                    uint64_t m, uint64_t n, uint32_t slices,
-                                                   float *partial) {
+                                                   float *partial, O *db, int add) {
     using E = typename T::E;
-    __shared__ float sum[4][512];
-    const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
-    const uint64_t col = (uint64_t)blockIdx.x * 512 + lane * 8;
+    __shared__ float sum[32][65];
+    const uint32_t lane = threadIdx.x & 7u, group = threadIdx.x >> 3;
+    const uint64_t first = (uint64_t)blockIdx.x * 64, col = first + lane * 8;
     const uint64_t r0 = m * blockIdx.y / slices, r1 = m * (blockIdx.y + 1) / slices;
     const uint32_t have = col >= n ? 0 : n - col < 8 ? (uint32_t)(n - col) : 8;
     float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     if (have == 8) {
-#pragma unroll 4
-        for (uint64_t r = r0 + wave; r < r1; r += 4) {
+#pragma unroll 8
+        for (uint64_t r = r0 + group; r < r1; r += 32) {
             E h[8];
             __builtin_memcpy(h, dz + r * ld + col, 16);
 #pragma unroll
@@ -347,7 +408,7 @@ __global__ __launch_bounds__(256) void column_sums(const typename T::E *dz, uint
                 v[i] += (float)h[i];
         }
     } else if (have) {
-        for (uint64_t r = r0 + wave; r < r1; r += 4)
+        for (uint64_t r = r0 + group; r < r1; r += 32)
 #pragma unroll
             for (uint32_t i = 0; i < 8; ++i)
                 if (i < have)
@@ -355,13 +416,19 @@ __global__ __launch_bounds__(256) void column_sums(const typename T::E *dz, uint
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        sum[wave][lane * 8 + i] = v[i];
+        sum[group][lane * 8 + i] = v[i];
     __syncthreads();
-    for (uint32_t c = threadIdx.x; c < 512; c += 256) {
-        const uint64_t at = (uint64_t)blockIdx.x * 512 + c;
-        if (at < n)
-            partial[(uint64_t)blockIdx.y * n + at] = sum[0][c] + sum[1][c] + sum[2][c] + sum[3][c];
-    }
+    const uint64_t at = first + threadIdx.x;
+    if (threadIdx.x >= 64 || at >= n)
+        return;
+    float t = 0.0f;
+#pragma unroll
+    for (int q = 0; q < 32; ++q)
+        t += sum[q][threadIdx.x];
+    if (slices > 1)
+        partial[(uint64_t)blockIdx.y * n + at] = t;
+    else
+        db[at] = (O)(add ? (float)db[at] + t : t);
 }
 
 template <class O>
@@ -371,6 +438,7 @@ __global__ __launch_bounds__(256) void column_join(const float *partial, uint32_
     if (c >= n)
         return;
     float v = 0.0f;
+#pragma unroll 8
     for (uint32_t s = 0; s < slices; ++s)
         v += partial[s * n + c];
     db[c] = (O)(add ? (float)db[c] + v : v);
@@ -408,8 +476,16 @@ Cut cut(uint64_t m, uint64_t n, uint64_t k) {
     return c;
 }
 
+// Slices of db's sums: up to 2048 rows one workgroup per 64 columns takes all
+// (a second launch costs more than it saves).
 uint32_t db_slices(uint64_t m) {
-    return (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>(m / 64, 64));
+    return m <= 2048 ? 1 : (uint32_t)std::min<uint64_t>(m / 512, 32);
+}
+
+// Forward products of so few rows that reading the weights is all the time,
+// and of enough columns for every other compute unit.
+bool skinny(uint64_t m, uint64_t n, uint64_t k) {
+    return m <= kSkinnyRows && n >= 2048 && k >= 256;
 }
 
 // C's shape and the length of the sums, by operation.
@@ -429,7 +505,7 @@ size_t partial_bytes(int op, size_t m, size_t n, size_t k) {
 }
 
 size_t workspace_bytes(int op, size_t m, size_t n, size_t k) {
-    return partial_bytes(op, m, n, k) + (op == kWgrad ? db_slices(m) * n * 4 : 0);
+    return partial_bytes(op, m, n, k) + (op == kWgrad && db_slices(m) > 1 ? db_slices(m) * n * 4 : 0);
 }
 
 bool sizes_ok(size_t m, size_t n, size_t k) {
@@ -575,6 +651,15 @@ int ddl_linear(const ddl_linear_args *a, void *workspace, size_t workspace_bytes
             && (!a->residual || aligned16(a->residual, a->ldr, 2))
             && (!a->z || aligned16(a->z, a->ldz, 2));
     const Operand x = operand(a->x, a->ldx, m, k), w = operand(a->w, a->ldw, n, k);
+    if (skinny(m, n, k) && k % 8 == 0 && aligned16(a->x, a->ldx, 2) && aligned16(a->w, a->ldw, 2)) {
+        const dim3 grid((uint32_t)((n + 15) / 16)), block(kSkinnyWaves * 64);
+        if (a->dtype == DDL_F16)
+            hipLaunchKernelGGL(skinny_kernel<Half>, grid, block, 0, (hipStream_t)stream, x, w, e);
+        else
+            hipLaunchKernelGGL(skinny_kernel<Bfloat>, grid, block, 0, (hipStream_t)stream, x, w,
+                               e);
+        return hipGetLastError() == hipSuccess ? DDL_OK : DDL_E_HIP;
+    }
     return a->dtype == DDL_F16
                ? product<Half, false, false>(x, w, e, k, workspace, (hipStream_t)stream)
                : product<Bfloat, false, false>(x, w, e, k, workspace, (hipStream_t)stream);
@@ -641,15 +726,19 @@ int weight_gradient(const ddl_wgrad_args *a, uint8_t *ws, hipStream_t s) {
     if (a->db && n) {
         float *partial = (float *)(ws + partial_bytes(kWgrad, m, n, k));
         const uint32_t slices = db_slices(m);
-        hipLaunchKernelGGL(column_sums<T>, dim3((uint32_t)((n + 511) / 512), slices), dim3(256),
-                           0, s, (const E *)a->dz, a->lddz, m, n, slices, partial);
-        const dim3 grid((uint32_t)((n + 255) / 256));
+        const dim3 sums((uint32_t)((n + 63) / 64), slices), join((uint32_t)((n + 255) / 256));
+        auto go = [&](auto o) {
+            using O = decltype(o);
+            hipLaunchKernelGGL((column_sums<T, O>), sums, dim3(256), 0, s, (const E *)a->dz,
+                               a->lddz, m, n, slices, partial, (O *)a->db, a->accumulate);
+            if (slices > 1)
+                hipLaunchKernelGGL(column_join<O>, join, dim3(256), 0, s, partial, slices, n,
+                                   (O *)a->db, a->accumulate);
+        };
         if (f32)
-            hipLaunchKernelGGL(column_join<float>, grid, dim3(256), 0, s, partial, slices, n,
-                               (float *)a->db, a->accumulate);
+            go(float());
         else
-            hipLaunchKernelGGL(column_join<E>, grid, dim3(256), 0, s, partial, slices, n,
-                               (E *)a->db, a->accumulate);
+            go(E());
         if (hipGetLastError() != hipSuccess)
             return DDL_E_HIP;
     }

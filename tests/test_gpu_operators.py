@@ -64,7 +64,8 @@ def near(got, want, slack):
 
 SIZES = [(1, 1, 1), (1, 64, 64), (2, 8, 2047), (5, 9, 7), (17, 130, 72), (64, 64, 64),
          (65, 63, 65), (129, 257, 130), (256, 256, 320), (300, 520, 2056), (1, 1000, 4096),
-         (16, 4096, 512), (33, 1000, 2048), (2049, 2056, 64)]
+         (16, 4096, 512), (33, 1000, 2048), (2049, 2056, 64),
+         (3, 2050, 264), (1, 2048, 2056)]
 LAYOUTS = {"dense": (0, 0), "odd rows": (3, 0), "padded": (8, 0), "off by one": (0, 1)}
 
 

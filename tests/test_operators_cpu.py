@@ -62,7 +62,7 @@ def test_dgrad_refusals():
 def test_wgrad_refusals():
     def call(**kw):
         a = ops.ddl_wgrad_args()
-        a.m, a.n, a.k, a.dtype, a.out_dtype = 4, 8, 16, ddl.DDL_BF16, ddl.DDL_F32
+        a.m, a.n, a.k, a.dtype, a.out_dtype = 4096, 8, 16, ddl.DDL_BF16, ddl.DDL_F32
         a.dz, a.lddz, a.x, a.ldx, a.dw, a.lddw = SOME, 8, SOME, 16, SOME, 16
         ws, size = kw.pop("workspace", (SOME, 1 << 30))
         for k, v in kw.items():
@@ -85,7 +85,7 @@ def test_empty_outputs_need_nothing():
 def test_workspace_sizes():
     assert ddl.linear_workspace("forward", 8192, 16384, 4096) == 0  # the card is full as it is
     assert ddl.linear_workspace("forward", 0, 16, 16) == 0
-    assert ddl.linear_workspace("wgrad", 100, 64, 64) >= 64 * 4  # db's partial sums
+    assert ddl.linear_workspace("wgrad", 4096, 4096, 4096) >= 4096 * 4  # db's partial sums
     # parts of a sum are cut only where they cost less than 64 outputs' worth
     one = ddl.linear_workspace("forward", 1, 4096, 4096)
     assert 0 <= one <= 64 * 4096 * 4 + 256
