@@ -76,57 +76,79 @@ def _lib():
     return _bound
 
 
+# The checks below run before every call, and a decoded token's product is done
+# in a few microseconds: types are looked up by object, devices by index.
+_type_codes = {}
+
+
 def _type(t, what):
-    code = _TYPES.get(str(t.dtype))
+    code = _type_codes.get(t.dtype)
     if code is None:
-        raise ValueError(f"{what} has type {t.dtype}: expected float32, float16 or bfloat16")
+        code = _TYPES.get(str(t.dtype))
+        if code is None:
+            raise ValueError(f"{what} has type {t.dtype}: expected float32, float16 or bfloat16")
+        _type_codes[t.dtype] = code
     return code
 
 
 def _act(act):
-    if act not in ACTS:
+    code = ACTS.get(act)
+    if code is None:
         raise ValueError(f"unknown activation {act!r}: expected one of {', '.join(ACTS)}")
-    return ACTS[act]
+    return code
 
 
-def _matrix(t, shape, like, what):
-    """(pointer, row stride) of a 2-D tensor whose rows are contiguous."""
+def _device(t, what):
+    """The index of the GPU that t is on."""
+    d = t.get_device()
+    if d < 0:
+        raise ValueError(f"{what} is on {t.device}: expected a GPU tensor")
+    return d
+
+
+def _matrix(t, rows, cols, device, dtype, what):
+    """(pointer, row stride) of a rows x cols tensor whose rows are contiguous."""
     if t is None:
         return None, 0
-    if len(t.shape) != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
-        raise ValueError(f"{what} has shape {tuple(t.shape)}: expected {shape}")
-    if not t.is_cuda or (like is not None and t.device != like.device):
-        raise ValueError(f"{what} is on {t.device}: expected a GPU tensor"
-                         + (f" on {like.device}" if like is not None else ""))
-    if t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"{what}'s rows are not contiguous (strides {tuple(t.stride())})")
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-        raise ValueError(f"{what}'s rows overlap (strides {tuple(t.stride())})")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows or shape[1] != cols:
+        raise ValueError(f"{what} has shape {tuple(shape)}: expected ({rows}, {cols})")
+    if t.get_device() != device:
+        raise ValueError(f"{what} is on {t.device}: expected a GPU tensor on device {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{what} has type {t.dtype}: expected {dtype}")
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{what}'s rows are not contiguous (strides {t.stride()})")
+    if rows <= 1:
+        return t.data_ptr(), cols
+    if ld < cols:
+        raise ValueError(f"{what}'s rows overlap (strides {t.stride()})")
+    return t.data_ptr(), ld
 
 
-def _vector(t, n, like, what):
+def _two(t, what):
+    if len(t.shape) != 2:
+        raise ValueError(f"{what} has shape {tuple(t.shape)}: expected two dimensions")
+    return t.shape
+
+
+def _vector(t, n, device, dtype, what):
     if t is None:
         return None
-    if tuple(t.shape) != (n,) or (n > 1 and t.stride(0) != 1):
+    if len(t.shape) != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{what} has shape {tuple(t.shape)}, strides {tuple(t.stride())}: "
                          f"expected {n} contiguous elements")
-    if not t.is_cuda or t.device != like.device:
-        raise ValueError(f"{what} is on {t.device}: expected {like.device}")
+    if t.get_device() != device or t.dtype != dtype:
+        raise ValueError(f"{what} is {t.dtype} on {t.device}: expected {dtype} on device {device}")
     return t.data_ptr()
 
 
-def _same_type(like, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.dtype != like.dtype:
-            raise ValueError(f"{name} has type {t.dtype}: expected {like.dtype}")
-
-
-def _workspace(ws, like):
+def _workspace(ws, device):
     if ws is None:
         return None, 0
-    if not ws.is_cuda or ws.device != like.device or not ws.is_contiguous():
-        raise ValueError(f"workspace: expected contiguous memory on {like.device}")
+    if ws.get_device() != device or not ws.is_contiguous():
+        raise ValueError(f"workspace: expected contiguous memory on device {device}")
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
@@ -147,19 +169,21 @@ def linear(x, w, y, bias=None, act="none", residual=None, z=None, workspace=None
     """y = act(x w^T + bias) + residual into y; the activation's argument into
     z, where given (ddl_linear).  x (m, k), w (n, k), y, residual and z (m, n),
     bias (n), all float16 or all bfloat16."""
-    a = ddl_linear_args()
-    a.x, a.ldx = _matrix(x, None, None, "x")
-    a.m, a.k = x.shape
-    a.w, a.ldw = _matrix(w, (w.shape[0], a.k), x, "w")
-    a.n = w.shape[0]
-    a.dtype, a.act = _type(x, "x"), _act(act)
-    _same_type(x, w=w, y=y, bias=bias, residual=residual, z=z)
-    a.y, a.ldy = _matrix(y, (a.m, a.n), x, "y")
-    a.bias = _vector(bias, a.n, x, "bias")
-    a.residual, a.ldr = _matrix(residual, (a.m, a.n), x, "residual")
-    a.z, a.ldz = _matrix(z, (a.m, a.n), x, "z")
-    ws, size = _workspace(workspace, x)
-    _check(_lib().ddl_linear(ctypes.byref(a), ws, size, _ptr(stream)), "ddl_linear")
+    m, k = _two(x, "x")
+    n = _two(w, "w")[0]
+    code, act = _type(x, "x"), _act(act)
+    d, t = _device(x, "x"), x.dtype
+    px, ldx = _matrix(x, m, k, d, t, "x")
+    pw, ldw = _matrix(w, n, k, d, t, "w")
+    py, ldy = _matrix(y, m, n, d, t, "y")
+    pr, ldr = _matrix(residual, m, n, d, t, "residual")
+    pz, ldz = _matrix(z, m, n, d, t, "z")
+    a = ddl_linear_args(m, n, k, code, act, px, ldx, pw, ldw, _vector(bias, n, d, t, "bias"), pr,
+                        ldr, py, ldy, pz, ldz)
+    ws, size = _workspace(workspace, d)
+    rc = (_bound or _lib()).ddl_linear(ctypes.byref(a), ws, size, _ptr(stream))
+    if rc:
+        _check(rc, "ddl_linear")
 
 
 def linear_dgrad(dz, w, dx, residual=None, act="none", z_prev=None, dz_prev=None, workspace=None,
@@ -167,64 +191,69 @@ def linear_dgrad(dz, w, dx, residual=None, act="none", z_prev=None, dz_prev=None
     """dx = dz w + residual into dx and, where z_prev is given, dx act'(z_prev)
     into dz_prev: the gradient of the layer before, whose activation is act
     (ddl_linear_dgrad).  dz (m, n), w (n, k), the others (m, k)."""
-    a = ddl_dgrad_args()
-    a.dz, a.lddz = _matrix(dz, None, None, "dz")
-    a.m, a.n = dz.shape
-    a.w, a.ldw = _matrix(w, (a.n, w.shape[-1]), dz, "w")
-    a.k = w.shape[1]
-    a.dtype, a.act = _type(dz, "dz"), _act(act)
+    m, n = _two(dz, "dz")
+    k = _two(w, "w")[1]
+    code, act_code = _type(dz, "dz"), _act(act)
     if (z_prev is None) != (dz_prev is None) or (z_prev is None and act != "none"):
         raise ValueError("z_prev and dz_prev go together, and with an activation")
-    _same_type(dz, w=w, dx=dx, residual=residual, z_prev=z_prev, dz_prev=dz_prev)
-    a.dx, a.lddx = _matrix(dx, (a.m, a.k), dz, "dx")
-    a.residual, a.ldr = _matrix(residual, (a.m, a.k), dz, "residual")
-    a.z_prev, a.ldz_prev = _matrix(z_prev, (a.m, a.k), dz, "z_prev")
-    a.dz_prev, a.lddz_prev = _matrix(dz_prev, (a.m, a.k), dz, "dz_prev")
-    ws, size = _workspace(workspace, dz)
-    _check(_lib().ddl_linear_dgrad(ctypes.byref(a), ws, size, _ptr(stream)), "ddl_linear_dgrad")
+    d, t = _device(dz, "dz"), dz.dtype
+    pz, ldz = _matrix(dz, m, n, d, t, "dz")
+    pw, ldw = _matrix(w, n, k, d, t, "w")
+    px, ldx = _matrix(dx, m, k, d, t, "dx")
+    pr, ldr = _matrix(residual, m, k, d, t, "residual")
+    pzp, ldzp = _matrix(z_prev, m, k, d, t, "z_prev")
+    pdzp, lddzp = _matrix(dz_prev, m, k, d, t, "dz_prev")
+    a = ddl_dgrad_args(m, n, k, code, act_code, pz, ldz, pw, ldw, pr, ldr, px, ldx, pzp, ldzp,
+                       pdzp, lddzp)
+    ws, size = _workspace(workspace, d)
+    rc = (_bound or _lib()).ddl_linear_dgrad(ctypes.byref(a), ws, size, _ptr(stream))
+    if rc:
+        _check(rc, "ddl_linear_dgrad")
 
 
 def linear_wgrad(dz, x, dw, db=None, accumulate=False, workspace=None, stream=None):
     """dw = dz^T x and db = dz's column sums, or added to them (ddl_linear_wgrad).
     dz (m, n), x (m, k); dw (n, k) and db (n) in float32 or in dz's type."""
-    a = ddl_wgrad_args()
-    a.dz, a.lddz = _matrix(dz, None, None, "dz")
-    a.m, a.n = dz.shape
-    a.x, a.ldx = _matrix(x, (a.m, x.shape[-1]), dz, "x")
-    a.k = x.shape[1]
-    a.dtype, a.out_dtype, a.accumulate = _type(dz, "dz"), _type(dw, "dw"), int(bool(accumulate))
-    _same_type(dz, x=x)
-    _same_type(dw, db=db)
-    a.dw, a.lddw = _matrix(dw, (a.n, a.k), dz, "dw")
-    a.db = _vector(db, a.n, dz, "db")
-    ws, size = _workspace(workspace, dz)
-    _check(_lib().ddl_linear_wgrad(ctypes.byref(a), ws, size, _ptr(stream)), "ddl_linear_wgrad")
+    m, n = _two(dz, "dz")
+    k = _two(x, "x")[1]
+    code, out = _type(dz, "dz"), _type(dw, "dw")
+    d, t = _device(dz, "dz"), dz.dtype
+    pz, ldz = _matrix(dz, m, n, d, t, "dz")
+    px, ldx = _matrix(x, m, k, d, t, "x")
+    pw, ldw = _matrix(dw, n, k, d, dw.dtype, "dw")
+    a = ddl_wgrad_args(m, n, k, code, out, int(bool(accumulate)), pz, ldz, px, ldx, pw, ldw,
+                       _vector(db, n, d, dw.dtype, "db"))
+    ws, size = _workspace(workspace, d)
+    rc = (_bound or _lib()).ddl_linear_wgrad(ctypes.byref(a), ws, size, _ptr(stream))
+    if rc:
+        _check(rc, "ddl_linear_wgrad")
 
 
-def _flat(t, need, what, types=None, like=None):
+def _flat(t, need, what, codes=None, device=None):
     """The pointer of a flat buffer of at least `need` elements."""
     if t is None:
         return None
-    if not t.is_cuda or (like is not None and t.device != like.device):
-        raise ValueError(f"{what} is on {t.device}: expected a GPU tensor"
-                         + (f" on {like.device}" if like is not None else ""))
+    if device is None:
+        _device(t, what)
+    elif t.get_device() != device:
+        raise ValueError(f"{what} is on {t.device}: expected a GPU tensor on device {device}")
     if not t.is_contiguous() or t.numel() < need:
         raise ValueError(f"{what} has {t.numel()} elements, strides {tuple(t.stride())}: "
                          f"expected at least {need}, contiguous")
-    if types is not None and str(t.dtype) not in types:
-        raise ValueError(f"{what} has type {t.dtype}: expected {' or '.join(types)}")
+    if codes is not None and _type(t, what) not in codes:
+        raise ValueError(f"{what} has type {t.dtype}, which this argument does not take")
     return t.data_ptr()
 
 
-_F32 = ("torch.float32",)
-_F16S = ("torch.float16", "torch.bfloat16")
+_F32 = (DDL_F32,)
+_F16S = (DDL_F16, DDL_BF16)
 
 
-def _weights(weights, need, like):
+def _weights(weights, need, device):
     if not weights:
         raise ValueError("expected at least one replica of the weights")
     return (ctypes.c_void_p * len(weights))(
-        *[_flat(w, need, f"weights[{i}]", _F32, like) for i, w in enumerate(weights)])
+        *[_flat(w, need, "weights", _F32, device) for w in weights])
 
 
 class _Optimizer:
@@ -263,14 +292,15 @@ class AdamW(_Optimizer):
              step=1, copy=None, stream=None):
         """One step on every replica in `weights`; `step` counts from 1; copy: a
         16-bit buffer that receives the new weights, or None."""
-        n = self.need
-        _check(_lib().ddl_adamw_step(
-            self.handle, _flat(grad, n, "grad"), _type(grad, "grad"),
-            _flat(m, n, "m", _F32, grad), _flat(v, n, "v", _F32, grad),
-            _weights(weights, n, grad), len(weights), _flat(copy, n, "copy", _F16S, grad),
-            _type(copy, "copy") if copy is not None else 0, float(lr), float(beta1),
-            float(beta2), float(eps), float(weight_decay), int(step), _ptr(stream)),
-            "ddl_adamw_step")
+        n, d = self.need, _device(grad, "grad")
+        rc = _lib().ddl_adamw_step(
+            self.handle, _flat(grad, n, "grad", None, d), _type(grad, "grad"),
+            _flat(m, n, "m", _F32, d), _flat(v, n, "v", _F32, d), _weights(weights, n, d),
+            len(weights), _flat(copy, n, "copy", _F16S, d),
+            _type(copy, "copy") if copy is not None else 0, lr, beta1, beta2, eps, weight_decay,
+            step, _ptr(stream))
+        if rc:
+            _check(rc, "ddl_adamw_step")
 
 
 class Muon(_Optimizer):
@@ -293,19 +323,24 @@ class Muon(_Optimizer):
 
     def orthogonalise(self, grad, out, stream=None):
         """out = the nearly orthogonal form of every matrix of grad (same type)."""
-        _same_type(grad, out=out)
-        _check(_lib().ddl_muon_orthogonalise(
-            self.handle, _flat(grad, self.need, "grad"), _flat(out, self.need, "out", None, grad),
-            _type(grad, "grad"), _ptr(stream)), "ddl_muon_orthogonalise")
+        if grad.dtype != out.dtype:
+            raise ValueError(f"out has type {out.dtype}: expected {grad.dtype}")
+        d = _device(grad, "grad")
+        rc = _lib().ddl_muon_orthogonalise(
+            self.handle, _flat(grad, self.need, "grad", None, d),
+            _flat(out, self.need, "out", None, d), _type(grad, "grad"), _ptr(stream))
+        if rc:
+            _check(rc, "ddl_muon_orthogonalise")
 
     def step(self, grad, momentum, weights, lr, momentum_decay=0.95, nesterov=True,
              weight_decay=0.0, copy=None, stream=None):
         """momentum = momentum_decay momentum + grad, then the orthogonalised
         update of every replica in `weights` (see ddl_muon_step)."""
-        n = self.need
-        _check(_lib().ddl_muon_step(
-            self.handle, _flat(grad, n, "grad"), _type(grad, "grad"),
-            _flat(momentum, n, "momentum", _F32, grad), _weights(weights, n, grad), len(weights),
-            _flat(copy, n, "copy", _F16S, grad), _type(copy, "copy") if copy is not None else 0,
-            float(lr), float(momentum_decay), int(bool(nesterov)), float(weight_decay),
-            _ptr(stream)), "ddl_muon_step")
+        n, d = self.need, _device(grad, "grad")
+        rc = _lib().ddl_muon_step(
+            self.handle, _flat(grad, n, "grad", None, d), _type(grad, "grad"),
+            _flat(momentum, n, "momentum", _F32, d), _weights(weights, n, d), len(weights),
+            _flat(copy, n, "copy", _F16S, d), _type(copy, "copy") if copy is not None else 0, lr,
+            momentum_decay, int(bool(nesterov)), weight_decay, _ptr(stream))
+        if rc:
+            _check(rc, "ddl_muon_step")
