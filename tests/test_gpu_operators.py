@@ -463,3 +463,17 @@ def test_first_call_in_a_capture_is_refused():
         with pytest.raises(ddl.DDLError) as e:
             h.step(v[0], v[1], v[2], [v[3]], lr=1e-3, stream=s)
     assert e.value.code == -9
+
+
+def test_training_example():
+    """The example's loss falls, and two runs give the same numbers."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "train_mlp.py")
+    spec = importlib.util.spec_from_file_location("train_mlp", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    losses = mod.train(steps=12)
+    assert losses == mod.train(steps=12)
+    assert losses[-1] < 0.5 * losses[0]
