@@ -596,16 +596,19 @@ typedef struct ddl_muon_s *ddl_muon;
  *   tiny to the neighbourhood of 1.
  * rows, cols <= 65536; extents of 0 are allowed. */
 int ddl_muon_create(ddl_muon *out, const ddl_muon_matrix *matrices, int nmatrices);
-/* out = orthogonal(grad) for every matrix, in grad's type.  DDL_F32 and
- * DDL_F16: products of pairs of binary16 values (22 significant bits), as
- * close as binary32 products (2e-6 off at 4096 x 4096); DDL_BF16: fewer
- * passes, an error of the order of bfloat16's rounding.  out may be grad. */
+/* out = orthogonal(grad) for every matrix, in grad's type.  DDL_F32 is
+ * computed in binary64 (its workspace, four times the matrices' size and
+ * more, is allocated by the first such call); DDL_F16 with products of pairs
+ * of binary16 values (22 significant bits), as close as binary32 products;
+ * DDL_BF16 with fewer passes, an error of the order of bfloat16's rounding.
+ * out may be grad. */
 int ddl_muon_orthogonalise(ddl_muon handle, const void *grad, void *out, int dtype,
                            void *stream);
 /* momentum = momentum_decay momentum + g;
  * u = g + momentum_decay momentum (nesterov 1) or momentum (0);
  * w = (1 - lr weight_decay) w - lr scale orthogonal(u), with the precision of
- * the binary32 form whatever the gradients' type. */
+ * binary32 products (2e-6 of the update at 4096 x 4096) whatever the
+ * gradients' type. */
 int ddl_muon_step(ddl_muon handle, const void *grad, int grad_dtype, float *momentum,
                   float *const *weights, int nweights, void *copy, int copy_dtype, double lr,
                   double momentum_decay, int nesterov, double weight_decay, void *stream);

@@ -355,7 +355,7 @@ struct Core {
     // What the epilogue reads comes from fetch, AHEAD pieces before the
     // stores of the first: one at a time, each piece waits for memory, which
     // took a tenth of the time of a tile of 4096 k.
-    template <bool TURNED = false, int AHEAD = (BM_ / WR_ > 64 ? 2 : 4), class G, class F>
+    template <bool TURNED = false, int AHEAD = (BM_ / WR_ > 64 ? 2 : BM_ / WR_ > 32 ? 4 : 1), class G, class F>
     __device__ __forceinline__ static void each(const f32x4 (&acc)[FM][FN], uint8_t *lds,
                                                 G &&fetch, F &&then) {
         constexpr int H = FM < 4 ? FM : 4;         // fragments of rows at a time

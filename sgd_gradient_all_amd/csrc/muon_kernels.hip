@@ -450,6 +450,144 @@ __global__ __launch_bounds__(Core::THREADS) void product_kernel(StepArgs p, Upda
 }
 
 // ---------------------------------------------------------------------------
+// binary64 products, for orthogonalising binary32 matrices
+//
+// Pairs of binary16 values leave 1 to 2e-6 after the five rounds, some 20
+// steps of a binary32 result; the form that returns binary32 therefore works
+// in binary64 throughout, on v_mfma_f64_16x16x4.  A workgroup of 4 waves takes
+// a 64 x 64 tile, 16 k at a time through LDS, the next 16 on their way to
+// registers meanwhile; rows of LDS are 2 doubles longer than their contents,
+// which spreads the banks.
+// ---------------------------------------------------------------------------
+
+typedef double f64x4 __attribute__((ext_vector_type(4)));
+typedef double f64x2 __attribute__((ext_vector_type(2)));
+
+template <int KIND>
+__global__ __launch_bounds__(256) void product64_kernel(const Mat *mats, const Work *work,
+                                                        double *ws, int from, int last,
+                                                        float *out) {
+    constexpr int K = 16;
+    __shared__ __attribute__((aligned(16))) double la[64][K + 2];
+    __shared__ __attribute__((aligned(16))) double lb[64][K + 2];  // [n][k]
+    const Work w = work[blockIdx.x];
+    const Mat t = mats[w.mat];
+    const uint64_t nx = (uint64_t)t.sp * t.lp;
+    // X twice, A and B, each half as many doubles as the pairs' halves
+    double *x = ws + t.x / 2 + from * nx, *y = ws + t.x / 2 + (from ^ 1) * nx;
+    double *a = ws + t.a / 2, *b = ws + t.b / 2;
+    const double *left = KIND == kGram ? x : KIND == kPoly ? a : b;
+    const double *right = KIND == kPoly ? a : x;
+    const uint64_t ldl = KIND == kGram ? t.lp : t.sp, ldr = KIND == kPoly ? t.sp : t.lp;
+    const uint32_t k = KIND == kGram ? t.lp : t.sp, m0 = w.ti * 64u, n0 = w.tj * 64u;
+    const uint32_t l = threadIdx.x & 63u, wave = threadIdx.x >> 6, r = l & 15u, g = l >> 4;
+    const uint32_t mw = (wave >> 1) * 32, nw = (wave & 1u) * 32;
+    // loads: 64 rows of 16 (two 8-lane pieces of a row), or 16 rows of 64
+    const uint32_t row = threadIdx.x >> 2, piece = (threadIdx.x & 3u) * 4;
+    const uint32_t krow = threadIdx.x >> 4, col = (threadIdx.x & 15u) * 4;
+    f64x2 ra[2], rb[2];
+    auto fetch = [&](uint32_t k0) {
+        const double *p = left + (uint64_t)(m0 + row) * ldl + k0 + piece;
+        ra[0] = *(const f64x2 *)p;
+        ra[1] = *(const f64x2 *)(p + 2);
+        p = KIND == kApply ? right + (uint64_t)(k0 + krow) * ldr + n0 + col
+                           : right + (uint64_t)(n0 + row) * ldr + k0 + piece;
+        rb[0] = *(const f64x2 *)p;
+        rb[1] = *(const f64x2 *)(p + 2);
+    };
+    f64x4 acc[2][2] = {};
+    fetch(0);
+    for (uint32_t k0 = 0; k0 < k; k0 += K) {
+        __syncthreads();
+        *(f64x2 *)&la[row][piece] = ra[0];
+        *(f64x2 *)&la[row][piece + 2] = ra[1];
+        if (KIND == kApply) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                lb[col + e][krow] = rb[e / 2][e % 2];
+        } else {
+            *(f64x2 *)&lb[row][piece] = rb[0];
+            *(f64x2 *)&lb[row][piece + 2] = rb[1];
+        }
+        __syncthreads();
+        if (k0 + K < k)
+            fetch(k0 + K);
+#pragma unroll
+        for (int kk = 0; kk < K; kk += 4) {
+            double fa[2], fb[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                fa[i] = la[mw + 16 * i + r][kk + g];
+                fb[i] = lb[nw + 16 * i + r][kk + g];
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f64_16x16x4f64(fa[i], fb[j], acc[i][j], 0,
+                                                                     0, 0);
+        }
+    }
+    // a lane's results: column r, rows 4 e + g of each 16 x 16
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t m = m0 + mw + 16 * i + 4 * e + g, n = n0 + nw + 16 * j + r;
+                const double v = acc[i][j][e];
+                if (KIND == kApply) {
+                    const uint64_t at = (uint64_t)m * t.lp + n;
+                    const double q = 3.4445 * x[at] + v;
+                    if (!last)
+                        y[at] = q;
+                    else if (m < t.s && n < t.l)
+                        out[t.at + (t.tall ? (uint64_t)n * t.cols + m
+                                           : (uint64_t)m * t.cols + n)] = (float)q;
+                } else {
+                    const uint64_t at = (uint64_t)m * t.sp + n;
+                    const double q = KIND == kGram ? v : -4.7750 * a[at] + 2.0315 * v;
+                    double *o = KIND == kGram ? a : b;
+                    o[at] = q;
+                    if (w.ti != w.tj)
+                        o[(uint64_t)n * t.sp + m] = q;
+                }
+            }
+}
+
+// X = U / norm in binary64, as normalise_kernel does in pairs.
+__global__ __launch_bounds__(256) void normalise64_kernel(const Mat *mats, const Work *work,
+                                                          const float *u, const double *partial,
+                                                          double *ws) {
+    __shared__ double lds[4];
+    __shared__ double norm_lds;
+    __shared__ float block[64][65];
+    const Work w = work[blockIdx.x];
+    const Mat t = mats[w.mat];
+    double sum = 0.0;
+    for (uint32_t i = t.chunk0 + threadIdx.x; i < t.chunk1; i += 256)
+        sum += partial[i];
+    sum = dev::block_sum(sum, lds);
+    if (threadIdx.x == 0)
+        norm_lds = 1.0 / (sqrt(sum) + kNormEps);
+    const uint32_t s0 = w.ti * 64u, l0 = w.tj * 64u;
+    const uint32_t r0 = t.tall ? l0 : s0, c0 = t.tall ? s0 : l0;
+    const uint32_t cc = threadIdx.x & 63u;
+#pragma unroll 4
+    for (uint32_t rr = threadIdx.x >> 6; rr < 64; rr += 4)
+        block[rr][cc] = r0 + rr < t.rows && c0 + cc < t.cols
+                            ? u[t.at + (uint64_t)(r0 + rr) * t.cols + c0 + cc]
+                            : 0.0f;
+    __syncthreads();
+    const double inv = norm_lds;
+    double *x = ws + t.x / 2;
+    for (uint32_t q = threadIdx.x >> 6; q < 64; q += 4)
+        x[(uint64_t)(s0 + q) * t.lp + l0 + cc] =
+            inv * (double)(t.tall ? block[cc][q] : block[q][cc]);
+}
+
+// ---------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------
 
@@ -470,7 +608,11 @@ struct ddl_muon_s {
     std::vector<Work> gram[2], poly[2], apply[2];
     uint32_t tile = 64;
     bool small = true;  // no side above 128
-    uint64_t ws = 0;     // elements of the workspace
+    uint64_t ws = 0;     // 16-bit elements of the workspace
+    // binary64: the tables of 64 x 64 tiles, made by the first call
+    std::vector<Work> tri64, all64;
+    Work *d_tri64 = nullptr, *d_all64 = nullptr;
+    double *d_ws64 = nullptr;
     uint64_t slots = 0;  // partial tiles
     uint32_t tickets = 0;
 
@@ -564,6 +706,12 @@ void lay_out(ddl_muon_s &h) {
         for (uint32_t a = 0; a < m.sp / 64; ++a)
             for (uint32_t b = 0; b < m.lp / 64; ++b)
                 h.blocks.push_back({i, (uint16_t)a, (uint16_t)b, 0, 1, 0, 0});
+        for (uint32_t b = 0; b < m.lp / 64; ++b)
+            for (uint32_t a = 0; a < m.sp / 64; ++a) {
+                h.all64.push_back({i, (uint16_t)a, (uint16_t)b, 0, 1, 0, 0});
+                if (b <= a)
+                    h.tri64.push_back(h.all64.back());
+            }
     }
     for (int f = 0; f < 2; ++f) {
         deal(h, kGram, kPasses[f][kGram], h.gram[f]);
@@ -649,6 +797,41 @@ int rounds(ddl_muon_s &h, const Update &u, const Replicas &r, int f, hipStream_t
     return rc;
 }
 
+// orthogonalise in binary32: the binary64 workspace (8 bytes for 4 of the
+// pairs' planes) is allocated by the first such call.
+int run64(ddl_muon_s &h, const Update &u, hipStream_t s) {
+    if (!h.d_ws64) {
+        hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
+        if (hipStreamIsCapturing(s, &st) != hipSuccess)
+            return DDL_E_HIP;
+        if (st != hipStreamCaptureStatusNone)
+            return DDL_E_UNBOUND;
+        int rc = h.d_tri64 ? DDL_OK : upload(h.tri64, &h.d_tri64);
+        rc = rc || h.d_all64 ? rc : upload(h.all64, &h.d_all64);
+        if (rc)
+            return rc;
+        if (hipMalloc((void **)&h.d_ws64, h.ws / 2 * 8) != hipSuccess) {
+            h.d_ws64 = nullptr;
+            return DDL_E_NOMEM;
+        }
+    }
+    hipLaunchKernelGGL(norm_kernel<float>, dim3((uint32_t)h.chunks.size()), dim3(256), 0, s,
+                       h.d_chunks, u, h.d_sums);
+    hipLaunchKernelGGL(normalise64_kernel, dim3((uint32_t)h.blocks.size()), dim3(256), 0, s,
+                       h.d_mats, h.d_blocks, (const float *)u.grad, h.d_sums, h.d_ws64);
+    const dim3 tri((uint32_t)h.tri64.size()), all((uint32_t)h.all64.size()), block(256);
+    for (int i = 0; i < kRounds; ++i) {
+        const int last = i == kRounds - 1;
+        hipLaunchKernelGGL(product64_kernel<kGram>, tri, block, 0, s, h.d_mats, h.d_tri64,
+                           h.d_ws64, i & 1, last, (float *)u.out);
+        hipLaunchKernelGGL(product64_kernel<kPoly>, tri, block, 0, s, h.d_mats, h.d_tri64,
+                           h.d_ws64, i & 1, last, (float *)u.out);
+        hipLaunchKernelGGL(product64_kernel<kApply>, all, block, 0, s, h.d_mats, h.d_all64,
+                           h.d_ws64, i & 1, last, (float *)u.out);
+    }
+    return hipGetLastError() == hipSuccess ? DDL_OK : DDL_E_HIP;
+}
+
 template <class G>
 int run_muon(ddl_muon_s &h, const Update &u, const Replicas &r, int f, hipStream_t s) {
     hipLaunchKernelGGL(norm_kernel<G>, dim3((uint32_t)h.chunks.size()), dim3(256), 0, s,
@@ -730,7 +913,7 @@ int ddl_muon_destroy(ddl_muon h) {
         return DDL_E_ARG;
     h->dev.release(h->d_mats, h->d_chunks, h->d_blocks, h->d_gram[0], h->d_gram[1], h->d_poly[0],
                    h->d_poly[1], h->d_apply[0], h->d_apply[1], h->d_ws, h->d_partial,
-                   h->d_tickets, h->d_sums);
+                   h->d_tickets, h->d_sums, h->d_tri64, h->d_all64, h->d_ws64);
     delete h;
     return DDL_OK;
 }
@@ -755,6 +938,8 @@ int ddl_muon_orthogonalise(ddl_muon h, const void *grad, void *out, int dtype, v
     u.out = out;
     u.vec = !(((uintptr_t)grad | (uintptr_t)out) % 16);
     Replicas r = {};
+    if (dtype == DDL_F32)
+        return run64(*h, u, (hipStream_t)stream);
     // small matrices, where launches are all the time, take the exacter form
     const int f = dtype != DDL_BF16 || h->small;
     return run_typed(*h, dtype, u, r, f, stream);

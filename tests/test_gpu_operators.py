@@ -477,3 +477,13 @@ def test_training_example():
     losses = mod.train(steps=12)
     assert losses == mod.train(steps=12)
     assert losses[-1] < 0.5 * losses[0]
+
+
+@pytest.mark.parametrize("r,c", [(1, 3), (40, 40), (200, 70), (130, 513)])
+def test_binary32_orthogonalise_is_rounded_once(r, c):
+    """Computed in binary64: what is left is the result's own rounding (five
+    rounds of binary64 products leave below 485 * 1e3 * 2^-53 = 6e-11)."""
+    x, out = normal(gen(r * c), r * c), torch.empty(r * c, device="cuda")
+    ddl.Muon([(0, r, c, 1.0)]).orthogonalise(x, out)
+    want = orthogonal64(x.view(r, c))
+    near(out.view(r, c), want, 1e-10 * float(want.norm()))
