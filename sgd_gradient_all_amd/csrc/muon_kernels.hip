@@ -678,17 +678,18 @@ void deal(ddl_muon_s &h, int kind, int passes, std::vector<Work> &out) {
 }
 
 void lay_out(ddl_muon_s &h) {
-    // The largest tile of which A's lower triangles still give every other
-    // compute unit one (128, 64) or all of them (256): with fewer, the sums
-    // over k are cut into more parts, and joining those costs more than the
-    // larger tile saves (the matrices of ResNet-50: TILES).
+    // The largest tile of which A's lower triangles give every compute unit
+    // one (256) or every other (128): with fewer, too few workgroups hide each
+    // other's waits, and the sums over k are cut into more parts to join
+    // (ResNet-50's matrices: 2.4 ms with 256, 1.3 ms with 128; one 4096 x 1024
+    // in bfloat16: 475 us with 128, 400 us with 64).
     auto triangles = [&](uint32_t T) {
         uint64_t n = 0;
         for (const Mat &m : h.mats)
             n += (uint64_t)(up(m.s, T) / T) * (up(m.s, T) / T + 1) / 2;
         return n;
     };
-    h.tile = triangles(256) >= 256 ? 256 : triangles(128) >= 32 ? 128 : 64;
+    h.tile = triangles(256) >= 256 ? 256 : triangles(128) >= 128 ? 128 : 64;
     for (uint32_t i = 0; i < h.mats.size(); ++i) {
         Mat &m = h.mats[i];
         h.small = h.small && m.l <= 128;
