@@ -149,7 +149,7 @@ template <class T, bool VEC>
 __device__ __forceinline__ Fetched fetch8(const Epilogue &e, uint64_t m, uint64_t n) {
     using E = typename T::E;
     Fetched f;
-    if (!VEC && (m >= e.m || n >= e.n))
+    if (m >= e.m || n >= e.n)
         return f;
     const uint32_t have = !VEC && e.n - n < 8 ? (uint32_t)(e.n - n) : 8u;
     if (e.bias)
@@ -168,12 +168,13 @@ __device__ __forceinline__ Fetched fetch8(const Epilogue &e, uint64_t m, uint64_
 }
 
 // 8 consecutive results of row m from column n on.
-// VEC: the 8 are inside C and every array's rows start at 16-byte boundaries.
+// VEC: all 8 are inside C or none, and every array's rows start at 16-byte
+// boundaries.
 template <class T, bool VEC>
 __device__ __forceinline__ void finish8(const Epilogue &e, uint64_t m, uint64_t n, float (&v)[8],
                                         const Fetched &f) {
     using E = typename T::E;
-    if (!VEC && (m >= e.m || n >= e.n))
+    if (m >= e.m || n >= e.n)
         return;
     const uint32_t have = !VEC && e.n - n < 8 ? (uint32_t)(e.n - n) : 8u;
     float t[8];
@@ -256,13 +257,15 @@ __global__ __launch_bounds__(Core::THREADS) void linear_kernel(GemmArgs g) {
     f32x4 acc[Core::FM][Core::FN] = {};
     Core::run(g.a, g.b, t0, t1, 0, lds, acc);
     const uint64_t m0 = g.a.row0, n0 = g.b.row0;
-    const bool whole = m0 + Core::BM <= g.e.m && n0 + Core::BN <= g.e.n;
+    // every 8 columns of the tile lie inside C or outside
+    const bool whole = g.e.n % 8 == 0 || n0 + Core::BN <= g.e.n;
     auto nothing = [](uint32_t, uint32_t) { return 0; };
     if (g.splits > 1) {
         float *to = g.partial + ((uint64_t)s * g.e.m + m0) * g.e.n + n0;
         if (whole && g.e.n % 4 == 0)
             Core::each(acc, lds, nothing, [&](uint32_t mi, uint32_t ni, float (&v)[8], int) {
-                store8<true>(to + mi * g.e.n + ni, 8, v);
+                if (m0 + mi < g.e.m && n0 + ni < g.e.n)
+                    store8<true>(to + mi * g.e.n + ni, 8, v);
             });
         else
             Core::template each<false, 1>(
