@@ -352,10 +352,12 @@ struct Core {
     // wave's results (both within the tile); TURNED: for every 8 consecutive m
     // of a column n.  They go through the wave's own part of LDS, so that 8
     // lanes (4 with FN = 2) hold whole 128-byte pieces of a row or column.
-    // What the epilogue reads comes from fetch, AHEAD pieces before the
-    // stores of the first: one at a time, each piece waits for memory, which
-    // took a tenth of the time of a tile of 4096 k.
-    template <bool TURNED = false, int AHEAD = (BM_ / WR_ > 64 ? 2 : BM_ / WR_ > 32 ? 4 : 1), class G, class F>
+    // What the epilogue reads comes from fetch, AHEAD pieces before the stores
+    // of the first, so that a piece need not wait for memory by itself: four
+    // with waves of 64 rows (128 x 128 tiles); with 128 rows the registers
+    // spill (8192 x 16384 x 4096 with GELU: 1036 us two ahead, 1000 us one), with 32
+    // there are two pieces.
+    template <bool TURNED = false, int AHEAD = (BM_ / WR_ == 64 ? 4 : 1), class G, class F>
     __device__ __forceinline__ static void each(const f32x4 (&acc)[FM][FN], uint8_t *lds,
                                                 G &&fetch, F &&then) {
         constexpr int H = FM < 4 ? FM : 4;         // fragments of rows at a time
