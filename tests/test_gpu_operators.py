@@ -487,3 +487,31 @@ def test_binary32_orthogonalise_is_rounded_once(r, c):
     ddl.Muon([(0, r, c, 1.0)]).orthogonalise(x, out)
     want = orthogonal64(x.view(r, c))
     near(out.view(r, c), want, 1e-10 * float(want.norm()))
+
+
+def test_offsets_past_32_bits():
+    """The last rows of arrays of more than 2^32 elements."""
+    t, g = torch.bfloat16, gen(21)
+    m, n, k = (1 << 21) + 5, 16, 2056
+    x = torch.empty(m, k, device="cuda", dtype=t).normal_(generator=g)
+    w = normal(g, n, k, sigma=k ** -0.5, dtype=t)
+    y = torch.empty(m, n, device="cuda", dtype=t)
+    print("forward past 32 bits", flush=True)
+    ddl.linear(x, w, y, workspace=workspace("forward", m, n, k))
+    tail = slice(m - 300, m)
+    xd, wd = x[tail].double(), w.double()
+    near(y[tail], xd @ wd.t().contiguous(),
+         (k + 4) * F32 * (xd.abs() @ wd.abs().t().contiguous()))
+    print("dgrad past 32 bits", flush=True)
+    ddl.linear_dgrad(y, w, x, workspace=workspace("dgrad", m, n, k))
+    yd = y[tail].double()
+    near(x[tail], yd @ wd, (n + 4) * F32 * (yd.abs() @ wd.abs()))
+    print("wgrad past 32 bits", flush=True)
+    # one row in the far end of dz alone: dw is that row's outer product
+    y.zero_()
+    y[m - 2] = normal(g, 16, dtype=t)
+    dw, db = torch.empty(n, k, device="cuda"), torch.empty(n, device="cuda")
+    ddl.linear_wgrad(y, x, dw, db=db, workspace=workspace("wgrad", m, n, k))
+    assert torch.equal(db, y[m - 2].float())
+    near(dw, y[m - 2].double()[:, None] * x[m - 2].double()[None, :],
+         torch.zeros((), device="cuda", dtype=torch.float64))
