@@ -598,10 +598,9 @@ typedef struct ddl_muon_s *ddl_muon;
 int ddl_muon_create(ddl_muon *out, const ddl_muon_matrix *matrices, int nmatrices);
 /* out = orthogonal(grad) for every matrix, in grad's type.  DDL_F32 is
  * computed in binary64 (its workspace, four times the matrices' size and
- * more, is allocated by the first such call); DDL_F16 with products of pairs
- * of binary16 values (22 significant bits), as close as binary32 products;
- * DDL_BF16 with fewer passes, an error of the order of bfloat16's rounding.
- * out may be grad. */
+ * more, is allocated by the first such call); the 16-bit types with products
+ * of pairs of binary16 values (22 significant bits), as close as binary32
+ * products, and rounded once.  out may be grad. */
 int ddl_muon_orthogonalise(ddl_muon handle, const void *grad, void *out, int dtype,
                            void *stream);
 /* momentum = momentum_decay momentum + g;

@@ -267,8 +267,7 @@ struct Core {
     // acc += the k tiles [t0, t1), t0 < t1.  Plain operands: pairs = 0.  Pairs
     // of high and low parts: pairs = the tiles of one pass over k; tiles go
     // through high * low, low * high, and high * high last, so that the sums
-    // that all the large terms meet are rounded a third as often.  (Starting
-    // at pairs leaves A's low parts in and B's out, at 2 pairs both out.)
+    // that all the large terms meet are rounded a third as often.
     __device__ __forceinline__ static void run(const Operand &a, const Operand &b, uint32_t t0,
                                                uint32_t t1, uint32_t pairs, uint8_t *lds,
                                                f32x4 (&acc)[FM][FN]) {

@@ -12,10 +12,10 @@
 // binary16 operands alone X ends 0.2 to 0.4% off, more than bfloat16's own
 // rounding.  X, A and B are held as sums of two binary16 values (22 bits), and
 // a product takes three passes, high*high + high*low + low*high, which ends as
-// close as binary32 products do.  For bfloat16 results, whose rounding is
-// 0.17%, A takes one pass, A A three and B X two (B's low parts, not X's):
-// 0.11 to 0.15% off.  Values are kept times 2^14: no entry of X passes 1.3 and none
-// of A or B 2.9 in magnitude (the spectral norms bound them), so nothing
+// close as binary32 products do, whatever the type of the result: fewer passes
+// for bfloat16 (one for A, two for B X) were 0.11 to 0.15% off beside its
+// rounding of 0.17%.  Values are kept times 2^14: no entry of X passes 1.3 and
+// none of A or B 2.9 in magnitude (the spectral norms bound them), so nothing
 // overflows binary16, and entries as small as 2^-28 are normal numbers.
 //
 // A and B are symmetric: tiles on and below the diagonal are computed and
@@ -83,8 +83,7 @@ struct StepArgs {
     uint16_t *ws;
     float *partial;
     uint32_t *tickets;
-    int from;   // which of X's two copies is read
-    int passes; // of 3: see kPasses
+    int from;  // which of X's two copies is read
     int last;
 };
 
@@ -208,8 +207,7 @@ __global__ __launch_bounds__(256) void normalise_kernel(const Mat *mats, const W
 }
 
 enum { kGram, kPoly, kApply };
-// passes of each product, by form: bfloat16 results, all others
-constexpr int kPasses[2][3] = {{1, 3, 2}, {3, 3, 3}};
+constexpr uint32_t kPasses = 3;  // over k in a product
 
 // 8 results of the last round, from element `at` of the flat buffers on.
 template <class G>
@@ -360,11 +358,9 @@ __global__ __launch_bounds__(Core::THREADS) void product_kernel(StepArgs p, Upda
     }
     right.ld = KIND == kPoly ? t.sp : t.lp;
     right.k = left.k;
-    const uint32_t kt = (uint32_t)(left.k / Core::BK), all = kt * p.passes;
-    const uint32_t skipped = kt * (3 - p.passes);
+    const uint32_t kt = (uint32_t)(left.k / Core::BK), all = kt * kPasses;
     f32x4 acc[Core::FM][Core::FN] = {};
-    Core::run(left, right, skipped + all * w.part / w.parts,
-              skipped + all * (w.part + 1) / w.parts, kt, lds, acc);
+    Core::run(left, right, all * w.part / w.parts, all * (w.part + 1) / w.parts, kt, lds, acc);
     if (w.parts > 1 && !join_parts<Core>(p, w, acc, arrived))
         return;
     struct Pair {
@@ -604,11 +600,9 @@ struct ddl_muon_s {
     std::vector<Mat> mats;
     std::vector<Chunk> chunks;
     std::vector<Work> blocks;       // normalise
-    // the products' tables, by form (kPasses)
-    std::vector<Work> gram[2], poly[2], apply[2];
+    std::vector<Work> gram, poly, apply;  // the products
     uint32_t tile = 64;
-    bool small = true;  // no side above 128
-    uint64_t ws = 0;     // 16-bit elements of the workspace
+    uint64_t ws = 0;  // 16-bit elements of the workspace
     // binary64: the tables of 64 x 64 tiles, made by the first call
     std::vector<Work> tri64, all64;
     Work *d_tri64 = nullptr, *d_all64 = nullptr;
@@ -619,7 +613,7 @@ struct ddl_muon_s {
     Handle dev;
     Mat *d_mats = nullptr;
     Chunk *d_chunks = nullptr;
-    Work *d_blocks = nullptr, *d_gram[2] = {}, *d_poly[2] = {}, *d_apply[2] = {};
+    Work *d_blocks = nullptr, *d_gram = nullptr, *d_poly = nullptr, *d_apply = nullptr;
     uint16_t *d_ws = nullptr;
     float *d_partial = nullptr;
     uint32_t *d_tickets = nullptr;
@@ -631,7 +625,7 @@ namespace {
 
 // Tiles of a product over all matrices, k cut into parts where the tiles
 // alone do not fill the card.
-void deal(ddl_muon_s &h, int kind, int passes, std::vector<Work> &out) {
+void deal(ddl_muon_s &h, int kind, std::vector<Work> &out) {
     const uint32_t T = h.tile;
     uint64_t tiles = 0;
     auto count = [&](const Mat &m, auto &&then) {
@@ -642,7 +636,7 @@ void deal(ddl_muon_s &h, int kind, int passes, std::vector<Work> &out) {
     };
     uint64_t steps = 0;  // k tiles over all tiles
     auto depth = [&](const Mat &m) {
-        return (uint64_t)(kind == kGram ? m.lp : m.sp) / 64 * passes;
+        return (uint64_t)(kind == kGram ? m.lp : m.sp) / 64 * kPasses;
     };
     for (const Mat &m : h.mats)
         count(m, [&](uint32_t, uint32_t) {
@@ -682,7 +676,7 @@ void lay_out(ddl_muon_s &h) {
     // one (256) or every other (128): with fewer, too few workgroups hide each
     // other's waits, and the sums over k are cut into more parts to join
     // (ResNet-50's matrices: 2.4 ms with 256, 1.3 ms with 128; one 4096 x 1024
-    // in bfloat16: 475 us with 128, 400 us with 64).
+    // in bfloat16: 645 us with 128, 590 us with 64).
     auto triangles = [&](uint32_t T) {
         uint64_t n = 0;
         for (const Mat &m : h.mats)
@@ -692,7 +686,6 @@ void lay_out(ddl_muon_s &h) {
     h.tile = triangles(256) >= 256 ? 256 : triangles(128) >= 128 ? 128 : 64;
     for (uint32_t i = 0; i < h.mats.size(); ++i) {
         Mat &m = h.mats[i];
-        h.small = h.small && m.l <= 128;
         m.sp = up(m.s, h.tile);
         m.lp = up(m.l, h.tile);
         m.x = h.ws;
@@ -714,11 +707,9 @@ void lay_out(ddl_muon_s &h) {
                     h.tri64.push_back(h.all64.back());
             }
     }
-    for (int f = 0; f < 2; ++f) {
-        deal(h, kGram, kPasses[f][kGram], h.gram[f]);
-        deal(h, kPoly, kPasses[f][kPoly], h.poly[f]);
-        deal(h, kApply, kPasses[f][kApply], h.apply[f]);
-    }
+    deal(h, kGram, h.gram);
+    deal(h, kPoly, h.poly);
+    deal(h, kApply, h.apply);
 }
 
 int bind_muon(ddl_muon_s &h, hipStream_t s) {
@@ -726,11 +717,9 @@ int bind_muon(ddl_muon_s &h, hipStream_t s) {
         int rc = upload(h.mats, &h.d_mats);
         rc = rc ? rc : upload(h.chunks, &h.d_chunks);
         rc = rc ? rc : upload(h.blocks, &h.d_blocks);
-        for (int f = 0; f < 2; ++f) {
-            rc = rc ? rc : upload(h.gram[f], &h.d_gram[f]);
-            rc = rc ? rc : upload(h.poly[f], &h.d_poly[f]);
-            rc = rc ? rc : upload(h.apply[f], &h.d_apply[f]);
-        }
+        rc = rc ? rc : upload(h.gram, &h.d_gram);
+        rc = rc ? rc : upload(h.poly, &h.d_poly);
+        rc = rc ? rc : upload(h.apply, &h.d_apply);
         rc = rc ? rc : upload(std::vector<uint32_t>(h.tickets, 0), &h.d_tickets);
         if (!rc
             && (hipMalloc((void **)&h.d_ws, h.ws * 2) != hipSuccess
@@ -742,14 +731,11 @@ int bind_muon(ddl_muon_s &h, hipStream_t s) {
         if (rc) {  // nothing half made: the next call starts anew
             (void)hipFree(h.d_mats), (void)hipFree(h.d_chunks), (void)hipFree(h.d_blocks);
             (void)hipFree(h.d_tickets), (void)hipFree(h.d_ws), (void)hipFree(h.d_partial);
-            (void)hipFree(h.d_sums);
+            (void)hipFree(h.d_sums), (void)hipFree(h.d_gram), (void)hipFree(h.d_poly);
+            (void)hipFree(h.d_apply);
             h.d_mats = nullptr, h.d_chunks = nullptr, h.d_blocks = nullptr;
             h.d_tickets = nullptr, h.d_ws = nullptr, h.d_partial = nullptr, h.d_sums = nullptr;
-            for (int f = 0; f < 2; ++f) {
-                (void)hipFree(h.d_gram[f]), (void)hipFree(h.d_poly[f]);
-                (void)hipFree(h.d_apply[f]);
-                h.d_gram[f] = h.d_poly[f] = h.d_apply[f] = nullptr;
-            }
+            h.d_gram = h.d_poly = h.d_apply = nullptr;
         }
         return rc;
     });
@@ -768,7 +754,7 @@ int launch_product(const StepArgs &p, const Update &u, const Replicas &r, hipStr
 }
 
 template <int T, class G>
-int rounds(ddl_muon_s &h, const Update &u, const Replicas &r, int f, hipStream_t s) {
+int rounds(ddl_muon_s &h, const Update &u, const Replicas &r, hipStream_t s) {
     constexpr int WR = 2, WC = T == 256 ? 4 : 2;
     constexpr int BK = 64, S = T == 64 ? 3 : 2;
     using Rows = gemm::Core<gemm::Half, T, T, WR, WC, BK, S, false, false, false>;
@@ -782,17 +768,14 @@ int rounds(ddl_muon_s &h, const Update &u, const Replicas &r, int f, hipStream_t
     for (int i = 0; i < kRounds && !rc; ++i) {
         p.from = i & 1;
         p.last = i == kRounds - 1;
-        p.passes = kPasses[f][kGram];
-        p.work = h.d_gram[f];
-        p.count = (uint32_t)h.gram[f].size();
+        p.work = h.d_gram;
+        p.count = (uint32_t)h.gram.size();
         rc = launch_product<Rows, kGram, float>(p, u, r, s);
-        p.passes = kPasses[f][kPoly];
-        p.work = h.d_poly[f];
-        p.count = (uint32_t)h.poly[f].size();
+        p.work = h.d_poly;
+        p.count = (uint32_t)h.poly.size();
         rc = rc ? rc : launch_product<Rows, kPoly, float>(p, u, r, s);
-        p.passes = kPasses[f][kApply];
-        p.work = h.d_apply[f];
-        p.count = (uint32_t)h.apply[f].size();
+        p.work = h.d_apply;
+        p.count = (uint32_t)h.apply.size();
         rc = rc ? rc : launch_product<Cols, kApply, G>(p, u, r, s);
     }
     return rc;
@@ -834,23 +817,23 @@ int run64(ddl_muon_s &h, const Update &u, hipStream_t s) {
 }
 
 template <class G>
-int run_muon(ddl_muon_s &h, const Update &u, const Replicas &r, int f, hipStream_t s) {
+int run_muon(ddl_muon_s &h, const Update &u, const Replicas &r, hipStream_t s) {
     hipLaunchKernelGGL(norm_kernel<G>, dim3((uint32_t)h.chunks.size()), dim3(256), 0, s,
                        h.d_chunks, u, h.d_sums);
     hipLaunchKernelGGL(normalise_kernel<G>, dim3((uint32_t)h.blocks.size()), dim3(256), 0, s,
                        h.d_mats, h.d_blocks, u, h.d_sums, h.d_ws);
     if (hipGetLastError() != hipSuccess)
         return DDL_E_HIP;
-    return h.tile == 256   ? rounds<256, G>(h, u, r, f, s)
-           : h.tile == 128 ? rounds<128, G>(h, u, r, f, s)
-                           : rounds<64, G>(h, u, r, f, s);
+    return h.tile == 256   ? rounds<256, G>(h, u, r, s)
+           : h.tile == 128 ? rounds<128, G>(h, u, r, s)
+                           : rounds<64, G>(h, u, r, s);
 }
 
-int run_typed(ddl_muon_s &h, int type, const Update &u, const Replicas &r, int f, void *stream) {
+int run_typed(ddl_muon_s &h, int type, const Update &u, const Replicas &r, void *stream) {
     hipStream_t s = (hipStream_t)stream;
-    return type == DDL_F32   ? run_muon<float>(h, u, r, f, s)
-           : type == DDL_F16 ? run_muon<_Float16>(h, u, r, f, s)
-                             : run_muon<__bf16>(h, u, r, f, s);
+    return type == DDL_F32   ? run_muon<float>(h, u, r, s)
+           : type == DDL_F16 ? run_muon<_Float16>(h, u, r, s)
+                             : run_muon<__bf16>(h, u, r, s);
 }
 
 }  // namespace
@@ -890,7 +873,7 @@ int ddl_muon_create(ddl_muon *out, const ddl_muon_matrix *matrices, int nmatrice
             rc = DDL_E_BUCKETS;
         if (!rc) {
             lay_out(*h);
-            if (h->slots > UINT32_MAX || h->apply[1].size() > kMaxGrid
+            if (h->slots > UINT32_MAX || h->apply.size() > kMaxGrid
                 || h->blocks.size() > kMaxGrid)
                 rc = DDL_E_ARG;
         }
@@ -912,9 +895,8 @@ int ddl_muon_destroy(ddl_muon h) {
         return DDL_E_NULL;
     if (!unregister_handle(h))
         return DDL_E_ARG;
-    h->dev.release(h->d_mats, h->d_chunks, h->d_blocks, h->d_gram[0], h->d_gram[1], h->d_poly[0],
-                   h->d_poly[1], h->d_apply[0], h->d_apply[1], h->d_ws, h->d_partial,
-                   h->d_tickets, h->d_sums, h->d_tri64, h->d_all64, h->d_ws64);
+    h->dev.release(h->d_mats, h->d_chunks, h->d_blocks, h->d_gram, h->d_poly, h->d_apply, h->d_ws,
+                   h->d_partial, h->d_tickets, h->d_sums, h->d_tri64, h->d_all64, h->d_ws64);
     delete h;
     return DDL_OK;
 }
@@ -941,9 +923,7 @@ int ddl_muon_orthogonalise(ddl_muon h, const void *grad, void *out, int dtype, v
     Replicas r = {};
     if (dtype == DDL_F32)
         return run64(*h, u, (hipStream_t)stream);
-    // small matrices, where launches are all the time, take the exacter form
-    const int f = dtype != DDL_BF16 || h->small;
-    return run_typed(*h, dtype, u, r, f, stream);
+    return run_typed(*h, dtype, u, r, stream);
 }
 
 int ddl_muon_step(ddl_muon h, const void *grad, int grad_dtype, float *momentum,
@@ -984,7 +964,7 @@ int ddl_muon_step(ddl_muon h, const void *grad, int grad_dtype, float *momentum,
     for (int i = 0; i < nweights; ++i)
         any |= (uintptr_t)weights[i];
     u.vec = any % 16 == 0;
-    return run_typed(*h, grad_dtype, u, r, 1, stream);
+    return run_typed(*h, grad_dtype, u, r, stream);
 }
 
 }  // extern "C"

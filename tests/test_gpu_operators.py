@@ -515,3 +515,35 @@ def test_offsets_past_32_bits():
     assert torch.equal(db, y[m - 2].float())
     near(dw, y[m - 2].double()[:, None] * x[m - 2].double()[None, :],
          torch.zeros((), device="cuda", dtype=torch.float64))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_a_result_does_not_depend_on_the_other_matrices(dtype):
+    """The same bits alone and beside a larger matrix: both handles take 64 x 64
+    tiles, and none of the sums is long enough to be cut."""
+    t, (r, c) = T[dtype], (100, 120)
+    x = normal(gen(31), r * c + 200 * 200, sigma=1e-2, dtype=t)
+    alone, beside = torch.empty_like(x), torch.empty_like(x)
+    ddl.Muon([(0, r, c, 1.0)]).orthogonalise(x, alone)
+    ddl.Muon([(0, r, c, 1.0), (r * c, 200, 200, 1.0)]).orthogonalise(x, beside)
+    assert torch.equal(alone[:r * c], beside[:r * c])
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("r,c", [(300, 640), (640, 300), (256, 256)])
+def test_orthogonalise_is_rounded_once(r, c, dtype):
+    """Pairs of binary16 values leave e with |e| <= 64 * 2^-22 of the result in
+    norm, so a 16-bit result is the exact one's rounding but where e crosses
+    the border between two: in |e| / step of the places on the average.  Steps
+    are u to 2 u of the value, so with values over a quarter of their mean
+    square root, e / step is at most 4 * 64 * 2^-22 / u."""
+    t = T[dtype]
+    x = normal(gen(r + c), r * c, sigma=1e-2, dtype=t)
+    out = torch.empty_like(x)
+    ddl.Muon([(0, r, c, 1.0)]).orthogonalise(x, out)
+    want = orthogonal64(x.view(r, c)).reshape(-1)
+    ref = want.to(t)
+    big = want.abs() >= want.square().mean().sqrt() / 4
+    crossed = (out != ref) & big
+    assert ((out.double() - ref.double()).abs()[big] <= 2 * u(t) * ref.double().abs()[big]).all()
+    assert float(crossed.sum()) <= 4 * 64 * 2.0 ** -22 / u(t) * float(big.sum())
