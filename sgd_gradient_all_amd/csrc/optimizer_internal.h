@@ -34,11 +34,11 @@ inline bool disjoint(std::vector<Span> s) {
     for (const Span &x : s)
         if (x.at > kMaxElements || x.count > kMaxElements)
             return false;
-    std::sort(s.begin(), s.end(), [](const Span &a, const Span &b) {
-        return a.at != b.at ? a.at < b.at : a.count < b.count;
-    });
+    // empty spans overlap nothing, and between two others would part them
+    s.erase(std::remove_if(s.begin(), s.end(), [](const Span &x) { return !x.count; }), s.end());
+    std::sort(s.begin(), s.end(), [](const Span &a, const Span &b) { return a.at < b.at; });
     for (size_t i = 1; i < s.size(); ++i)
-        if (s[i - 1].at + s[i - 1].count > s[i].at && s[i - 1].count && s[i].count)
+        if (s[i - 1].at + s[i - 1].count > s[i].at)
             return false;
     return true;
 }

@@ -200,3 +200,16 @@ def test_muon_refusals(kw, code):
 def test_exchange_still_refuses_bfloat16():
     with pytest.raises(ddl.DDLError):
         ddl.Plan(2, 16, ddl.DDL_BF16)
+
+
+@pytest.mark.parametrize("spans", [[(0, 10), (5, 0), (6, 3)], [(0, 10), (0, 0), (0, 1)],
+                                   [(4, 0), (4, 4), (6, 0), (7, 0), (7, 1)]])
+def test_empty_spans_hide_no_overlap(spans):
+    with pytest.raises(ddl.DDLError) as e:
+        ddl.AdamW(spans)
+    assert e.value.code == E_BUCKETS
+
+
+def test_empty_spans_overlap_nothing():
+    a = ddl.AdamW([(0, 10), (5, 0), (10, 3), (13, 0), (12, 0)])
+    assert a.need == 13
