@@ -74,7 +74,11 @@ __device__ __forceinline__ float activate(float v, int act) {
     }
 }
 
+// Past |v| = 128 every slope is 0 or 1 in binary32; farther out, infinities
+// included, its terms pass binary32's range and meet zeros (inf 0 is NaN), so
+// the argument stops there.  NaN stays NaN.
 __device__ __forceinline__ float act_slope(float v, int act) {
+    v = v > 128.0f ? 128.0f : v < -128.0f ? -128.0f : v;
     switch (act) {
     case DDL_ACT_RELU: return v > 0.0f ? 1.0f : 0.0f;
     case DDL_ACT_GELU:

@@ -547,3 +547,32 @@ def test_orthogonalise_is_rounded_once(r, c, dtype):
     crossed = (out != ref) & big
     assert ((out.double() - ref.double()).abs()[big] <= 2 * u(t) * ref.double().abs()[big]).all()
     assert float(crossed.sum()) <= 4 * 64 * 2.0 ** -22 / u(t) * float(big.sum())
+
+
+SMOOTH = ["gelu", "gelu_tanh", "silu"]
+
+
+def slopes(values, act, t):
+    """dz_prev at z_prev = values where dx is 1."""
+    m, k = values.numel(), 8
+    dz, w = torch.zeros(m, 8, device="cuda", dtype=t), torch.zeros(8, k, device="cuda", dtype=t)
+    dz[:, 0], w[0] = 1, 1
+    z = values[:, None].expand(m, k).contiguous()
+    dx, dp = torch.empty_like(z), torch.empty_like(z)
+    ddl.linear_dgrad(dz, w, dx, act=act, z_prev=z, dz_prev=dp,
+                     workspace=workspace("dgrad", m, 8, k))
+    assert (dx == 1).all()
+    return dp
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("act", SMOOTH)
+def test_slopes_far_out(act, dtype):
+    """The slope is 1 far to the right, 0 far to the left, and NaN at NaN."""
+    t = T[dtype]
+    far = [200.0, 1e4, 6e4, float("inf")] + ([1e12, 2e13, 1e19, 3e19, 1e30, 3e38]
+                                             if dtype == "bf16" else [])
+    v = torch.tensor(far, device="cuda").to(t)
+    assert (slopes(v, act, t) == 1).all()
+    assert (slopes(-v, act, t) == 0).all()
+    assert torch.isnan(slopes(torch.full_like(v, float("nan")), act, t)).all()
