@@ -64,10 +64,16 @@ __device__ __forceinline__ float tanh_argument(float v) {
     return v * fma(v * v, 0.044715f * kTanh * kLog2e, kTanh * kLog2e);
 }
 
+// Phi(v) by erfc: 1 + erf cancels in the left tail (4% off at -5), though it is
+// shorter (8192 x 16384 x 4096 in bfloat16: 1107 us by erfc, 1078 by erf).
+__device__ __forceinline__ float normal_cdf(float v) {
+    return 0.5f * erfcf(v * -0.7071067811865476f);
+}
+
 __device__ __forceinline__ float activate(float v, int act) {
     switch (act) {
     case DDL_ACT_RELU: return v < 0.0f ? 0.0f : v;  // NaN stays NaN
-    case DDL_ACT_GELU: return 0.5f * v * (1.0f + erff(v * 0.7071067811865476f));
+    case DDL_ACT_GELU: return v * normal_cdf(v);
     case DDL_ACT_GELU_TANH: return v * sigmoid2(tanh_argument(v));
     case DDL_ACT_SILU: return v * sigmoid2(v * kLog2e);
     default: return v;
@@ -84,7 +90,7 @@ __device__ __forceinline__ float act_slope(float v, int act) {
     case DDL_ACT_GELU:
         return fma(v * 0.3989422804014327f,
                    __builtin_amdgcn_exp2f(v * v * (-0.5f * kLog2e)),
-                   fma(0.5f, erff(v * 0.7071067811865476f), 0.5f));
+                   normal_cdf(v));
     case DDL_ACT_GELU_TANH: {
         const float s = sigmoid2(tanh_argument(v));
         const float d = fma(v * v, 3.0f * 0.044715f * kTanh, kTanh);

@@ -576,3 +576,57 @@ def test_slopes_far_out(act, dtype):
     assert (slopes(v, act, t) == 1).all()
     assert (slopes(-v, act, t) == 0).all()
     assert torch.isnan(slopes(torch.full_like(v, float("nan")), act, t)).all()
+
+
+def cdf64(z):
+    """Phi(z) without the cancellation that torch.special.ndtr has on the left."""
+    return 0.5 * torch.special.erfc(z * -math.sqrt(0.5))
+
+
+def grid(t):
+    """Arguments of the activations, and the size of the exponent that each
+    form takes at them (the rounding of the exponent is that much of the
+    result's relative error)."""
+    v = torch.cat([torch.linspace(-12, 12, 769, device="cuda"),
+                   torch.linspace(-1e-3, 1e-3, 21, device="cuda")]).to(t)
+    a = v.double().abs()
+    return v, {"gelu": a * a / 2, "gelu_tanh": 1.6 * a + 0.0714 * a ** 3, "silu": a}
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("act", SMOOTH)
+def test_activations_in_their_tails(act, dtype):
+    """Every value to its own relative error, the small ones of the left tail
+    too: 8 roundings and 4 of the exponent.  Results under 2^-125 |v| may be 0
+    (2^x leaves binary32's range)."""
+    t = T[dtype]
+    v, a = grid(t)
+    m, n, k = v.numel(), 8, 8
+    x, w = torch.zeros(m, k, device="cuda", dtype=t), torch.zeros(n, k, device="cuda", dtype=t)
+    x[:, 0], w[:, 0] = v, 1
+    y = torch.empty(m, n, device="cuda", dtype=t)
+    ddl.linear(x, w, y, act=act, workspace=workspace("forward", m, n, k))
+    z = v.double()
+    want = z * cdf64(z) if act == "gelu" else act64(z, act)
+    slack = (4 * a[act] + 8) * F32 * want.abs() + 2.0 ** -125 * z.abs()
+    near(y, want[:, None].expand(m, n), slack[:, None])
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("act", SMOOTH)
+def test_slopes_in_their_tails(act, dtype):
+    """Slopes are a sum of two terms, each to its own relative error."""
+    t = T[dtype]
+    v, a = grid(t)
+    z = v.double()
+    if act == "gelu":
+        p, q = cdf64(z), z * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+    else:
+        k = 2 * math.sqrt(2 / math.pi)
+        arg, d = (z, 1.0) if act == "silu" else (k * (z + 0.044715 * z ** 3),
+                                                 k * (1 + 0.134145 * z * z))
+        p = torch.sigmoid(arg)
+        q = z * d * p * torch.sigmoid(-arg)
+    slack = (4 * a[act] + 8) * F32 * (p + q.abs()) + 2.0 ** -125 * (1 + z.abs() ** 3)
+    got = slopes(v, act, t)
+    near(got, (p + q)[:, None].expand(got.shape), slack[:, None])
