@@ -204,20 +204,16 @@ int ddl_adamw_step(ddl_adamw h, const void *grad, int grad_dtype, float *m, floa
     hipStream_t s = (hipStream_t)stream;
     auto go = [&](auto g) {
         using G = decltype(g);
-        if (copy && copy_dtype == DDL_BF16)
-            hipLaunchKernelGGL((adamw_kernel<G, __bf16>), grid, block, 0, s, a);
-        else
-            hipLaunchKernelGGL((adamw_kernel<G, _Float16>), grid, block, 0, s, a);
+        return launch(copy && copy_dtype == DDL_BF16 ? adamw_kernel<G, __bf16>
+                                                     : adamw_kernel<G, _Float16>,
+                      grid, block, 0, s, a);
     };
-    if (grad_dtype == DDL_F32)
-        go(float());
-    else if (grad_dtype == DDL_F16)
-        go(_Float16());
-    else
-        go(__bf16());
-    if (r.count > 1)
-        hipLaunchKernelGGL(replica_kernel, grid, block, 0, s, h->d_chunks, r.w[0], r);
-    return hipGetLastError() == hipSuccess ? DDL_OK : DDL_E_HIP;
+    rc = grad_dtype == DDL_F32   ? go(float())
+         : grad_dtype == DDL_F16 ? go(_Float16())
+                                 : go(__bf16());
+    return rc || r.count == 1
+               ? rc
+               : launch(replica_kernel, grid, block, 0, s, h->d_chunks, r.w[0], r);
 }
 
 }  // extern "C"

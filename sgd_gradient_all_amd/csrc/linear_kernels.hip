@@ -16,6 +16,7 @@
 
 #include "../../include/ddl.h"
 #include "gemm_core.h"
+#include "hip_call.h"
 
 namespace ddl {
 namespace {
@@ -529,24 +530,15 @@ bool aligned16(const void *p, size_t ld, size_t esz) {
     return ((uintptr_t)p | ld * esz) % 16 == 0;
 }
 
-template <class T, class Core>
-int launch(const GemmArgs &g, hipStream_t stream) {
-    const void *f = (const void *)&linear_kernel<T, Core>;
-    if (Core::LDS > 65536
-        && hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, Core::LDS)
-               != hipSuccess)
-        return DDL_E_HIP;
-    hipLaunchKernelGGL((linear_kernel<T, Core>), dim3(g.tm * g.tn, g.splits),
-                       dim3(Core::THREADS), Core::LDS, stream, g);
-    return hipGetLastError() == hipSuccess ? DDL_OK : DDL_E_HIP;
-}
-
 template <class T, bool TRA, bool TRB, bool STAGED>
 int launch_tile(int tile, GemmArgs &g, uint64_t k, hipStream_t s) {
     auto go = [&](auto core) {
         using Core = decltype(core);
         g.kt = (uint32_t)((k + Core::BK - 1) / Core::BK);
-        return launch<T, Core>(g, s);
+        const int rc = allow_lds(linear_kernel<T, Core>, Core::LDS);
+        return rc ? rc
+                  : launch(linear_kernel<T, Core>, dim3(g.tm * g.tn, g.splits),
+                           dim3(Core::THREADS), Core::LDS, s, g);
     };
     if (tile == 0)
         return go(gemm::Core<T, 256, 256, 2, 4, 64, 2, TRA, TRB, STAGED>());
@@ -578,9 +570,8 @@ int product(const Operand &a, const Operand &b, const Epilogue &e, uint64_t k, v
             return rc;
     }
     const uint64_t lanes = (e.n + 7) / 8 * e.m;
-    hipLaunchKernelGGL(linear_join<T>, dim3((uint32_t)((lanes + 255) / 256)), dim3(256), 0, s, e,
-                       g.partial, g.splits);
-    return hipGetLastError() == hipSuccess ? DDL_OK : DDL_E_HIP;
+    return launch(linear_join<T>, dim3((uint32_t)((lanes + 255) / 256)), dim3(256), 0, s, e,
+                  g.partial, g.splits);
 }
 
 bool row_ok(const void *p, size_t ld, size_t cols, size_t rows) {
@@ -666,12 +657,8 @@ int ddl_linear(const ddl_linear_args *a, void *workspace, size_t workspace_bytes
     const Operand x = operand(a->x, a->ldx, m, k), w = operand(a->w, a->ldw, n, k);
     if (skinny(m, n, k) && k % 8 == 0 && aligned16(a->x, a->ldx, 2) && aligned16(a->w, a->ldw, 2)) {
         const dim3 grid((uint32_t)((n + 15) / 16)), block(kSkinnyWaves * 64);
-        if (a->dtype == DDL_F16)
-            hipLaunchKernelGGL(skinny_kernel<Half>, grid, block, 0, (hipStream_t)stream, x, w, e);
-        else
-            hipLaunchKernelGGL(skinny_kernel<Bfloat>, grid, block, 0, (hipStream_t)stream, x, w,
-                               e);
-        return hipGetLastError() == hipSuccess ? DDL_OK : DDL_E_HIP;
+        return launch(a->dtype == DDL_F16 ? skinny_kernel<Half> : skinny_kernel<Bfloat>, grid,
+                      block, 0, (hipStream_t)stream, x, w, e);
     }
     return a->dtype == DDL_F16
                ? product<Half, false, false>(x, w, e, k, workspace, (hipStream_t)stream)
@@ -742,18 +729,15 @@ int weight_gradient(const ddl_wgrad_args *a, uint8_t *ws, hipStream_t s) {
         const dim3 sums((uint32_t)((n + 63) / 64), slices), join((uint32_t)((n + 255) / 256));
         auto go = [&](auto o) {
             using O = decltype(o);
-            hipLaunchKernelGGL((column_sums<T, O>), sums, dim3(256), 0, s, (const E *)a->dz,
-                               a->lddz, m, n, slices, partial, (O *)a->db, a->accumulate);
-            if (slices > 1)
-                hipLaunchKernelGGL(column_join<O>, join, dim3(256), 0, s, partial, slices, n,
-                                   (O *)a->db, a->accumulate);
+            const int rc = launch(column_sums<T, O>, sums, dim3(256), 0, s, (const E *)a->dz,
+                                  a->lddz, m, n, slices, partial, (O *)a->db, a->accumulate);
+            return rc || slices == 1 ? rc
+                                     : launch(column_join<O>, join, dim3(256), 0, s, partial,
+                                              slices, n, (O *)a->db, a->accumulate);
         };
-        if (f32)
-            go(float());
-        else
-            go(E());
-        if (hipGetLastError() != hipSuccess)
-            return DDL_E_HIP;
+        const int rc = f32 ? go(float()) : go(E());
+        if (rc)
+            return rc;
     }
     if (!n || !k)
         return DDL_OK;

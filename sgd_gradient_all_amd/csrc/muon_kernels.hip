@@ -721,13 +721,11 @@ int bind_muon(ddl_muon_s &h, hipStream_t s) {
         rc = rc ? rc : upload(h.poly, &h.d_poly);
         rc = rc ? rc : upload(h.apply, &h.d_apply);
         rc = rc ? rc : upload(std::vector<uint32_t>(h.tickets, 0), &h.d_tickets);
-        if (!rc
-            && (hipMalloc((void **)&h.d_ws, h.ws * 2) != hipSuccess
-                || hipMalloc((void **)&h.d_partial,
-                             std::max<uint64_t>(1, h.slots) * h.tile * h.tile * 4)
-                       != hipSuccess
-                || hipMalloc((void **)&h.d_sums, h.chunks.size() * 8) != hipSuccess))
-            rc = DDL_E_NOMEM;
+        rc = rc ? rc : device_memory(&h.d_ws, h.ws);
+        rc = rc ? rc
+                : device_memory(&h.d_partial,
+                                std::max<uint64_t>(1, h.slots) * h.tile * h.tile);
+        rc = rc ? rc : device_memory(&h.d_sums, h.chunks.size());
         if (rc) {  // nothing half made: the next call starts anew
             (void)hipFree(h.d_mats), (void)hipFree(h.d_chunks), (void)hipFree(h.d_blocks);
             (void)hipFree(h.d_tickets), (void)hipFree(h.d_ws), (void)hipFree(h.d_partial);
@@ -743,14 +741,10 @@ int bind_muon(ddl_muon_s &h, hipStream_t s) {
 
 template <class Core, int KIND, class G>
 int launch_product(const StepArgs &p, const Update &u, const Replicas &r, hipStream_t s) {
-    if (Core::LDS > 65536
-        && hipFuncSetAttribute((const void *)&product_kernel<Core, KIND, G>,
-                               hipFuncAttributeMaxDynamicSharedMemorySize, Core::LDS)
-               != hipSuccess)
-        return DDL_E_HIP;
-    hipLaunchKernelGGL((product_kernel<Core, KIND, G>), dim3(p.count), dim3(Core::THREADS),
+    const int rc = allow_lds(product_kernel<Core, KIND, G>, Core::LDS);
+    return rc ? rc
+              : launch(product_kernel<Core, KIND, G>, dim3(p.count), dim3(Core::THREADS),
                        Core::LDS, s, p, u, r);
-    return hipGetLastError() == hipSuccess ? DDL_OK : DDL_E_HIP;
 }
 
 template <int T, class G>
@@ -785,45 +779,41 @@ int rounds(ddl_muon_s &h, const Update &u, const Replicas &r, hipStream_t s) {
 // pairs' planes) is allocated by the first such call.
 int run64(ddl_muon_s &h, const Update &u, hipStream_t s) {
     if (!h.d_ws64) {
-        hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
-        if (hipStreamIsCapturing(s, &st) != hipSuccess)
-            return DDL_E_HIP;
-        if (st != hipStreamCaptureStatusNone)
-            return DDL_E_UNBOUND;
-        int rc = h.d_tri64 ? DDL_OK : upload(h.tri64, &h.d_tri64);
+        int rc = Handle::not_capturing(s);
+        rc = rc || h.d_tri64 ? rc : upload(h.tri64, &h.d_tri64);
         rc = rc || h.d_all64 ? rc : upload(h.all64, &h.d_all64);
+        rc = rc ? rc : device_memory(&h.d_ws64, h.ws / 2);
         if (rc)
             return rc;
-        if (hipMalloc((void **)&h.d_ws64, h.ws / 2 * 8) != hipSuccess) {
-            h.d_ws64 = nullptr;
-            return DDL_E_NOMEM;
-        }
     }
-    hipLaunchKernelGGL(norm_kernel<float>, dim3((uint32_t)h.chunks.size()), dim3(256), 0, s,
-                       h.d_chunks, u, h.d_sums);
-    hipLaunchKernelGGL(normalise64_kernel, dim3((uint32_t)h.blocks.size()), dim3(256), 0, s,
-                       h.d_mats, h.d_blocks, (const float *)u.grad, h.d_sums, h.d_ws64);
-    const dim3 tri((uint32_t)h.tri64.size()), all((uint32_t)h.all64.size()), block(256);
-    for (int i = 0; i < kRounds; ++i) {
-        const int last = i == kRounds - 1;
-        hipLaunchKernelGGL(product64_kernel<kGram>, tri, block, 0, s, h.d_mats, h.d_tri64,
-                           h.d_ws64, i & 1, last, (float *)u.out);
-        hipLaunchKernelGGL(product64_kernel<kPoly>, tri, block, 0, s, h.d_mats, h.d_tri64,
-                           h.d_ws64, i & 1, last, (float *)u.out);
-        hipLaunchKernelGGL(product64_kernel<kApply>, all, block, 0, s, h.d_mats, h.d_all64,
-                           h.d_ws64, i & 1, last, (float *)u.out);
+    int rc = launch(norm_kernel<float>, dim3((uint32_t)h.chunks.size()), dim3(256), 0, s,
+                    h.d_chunks, u, h.d_sums);
+    rc = rc ? rc
+            : launch(normalise64_kernel, dim3((uint32_t)h.blocks.size()), dim3(256), 0, s,
+                     h.d_mats, h.d_blocks, (const float *)u.grad, h.d_sums, h.d_ws64);
+    const dim3 tri((uint32_t)h.tri64.size()), all((uint32_t)h.all64.size());
+    for (int i = 0; i < kRounds && !rc; ++i) {
+        auto product = [&](auto kernel, dim3 grid, const Work *work) {
+            rc = rc ? rc
+                    : launch(kernel, grid, dim3(256), 0, s, h.d_mats, work, h.d_ws64, i & 1,
+                             i == kRounds - 1, (float *)u.out);
+        };
+        product(product64_kernel<kGram>, tri, h.d_tri64);
+        product(product64_kernel<kPoly>, tri, h.d_tri64);
+        product(product64_kernel<kApply>, all, h.d_all64);
     }
-    return hipGetLastError() == hipSuccess ? DDL_OK : DDL_E_HIP;
+    return rc;
 }
 
 template <class G>
 int run_muon(ddl_muon_s &h, const Update &u, const Replicas &r, hipStream_t s) {
-    hipLaunchKernelGGL(norm_kernel<G>, dim3((uint32_t)h.chunks.size()), dim3(256), 0, s,
-                       h.d_chunks, u, h.d_sums);
-    hipLaunchKernelGGL(normalise_kernel<G>, dim3((uint32_t)h.blocks.size()), dim3(256), 0, s,
-                       h.d_mats, h.d_blocks, u, h.d_sums, h.d_ws);
-    if (hipGetLastError() != hipSuccess)
-        return DDL_E_HIP;
+    int rc = launch(norm_kernel<G>, dim3((uint32_t)h.chunks.size()), dim3(256), 0, s, h.d_chunks,
+                    u, h.d_sums);
+    rc = rc ? rc
+            : launch(normalise_kernel<G>, dim3((uint32_t)h.blocks.size()), dim3(256), 0, s,
+                     h.d_mats, h.d_blocks, u, h.d_sums, h.d_ws);
+    if (rc)
+        return rc;
     return h.tile == 256   ? rounds<256, G>(h, u, r, s)
            : h.tile == 128 ? rounds<128, G>(h, u, r, s)
                            : rounds<64, G>(h, u, r, s);

@@ -11,6 +11,7 @@
 #include <vector>
 
 #include "../../include/ddl.h"
+#include "hip_call.h"
 
 namespace ddl {
 
@@ -89,20 +90,22 @@ struct Handle {
 
     template <class F>
     int bind(hipStream_t stream, F &&make) {
-        int now;
-        if (hipGetDevice(&now) != hipSuccess)
-            return DDL_E_HIP;
+        int now, rc = hip_result(hipGetDevice(&now));
+        if (rc)
+            return rc;
         if (device >= 0)
             return now == device ? DDL_OK : DDL_E_DEVICE;
-        hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
-        if (hipStreamIsCapturing(stream, &st) != hipSuccess)
-            return DDL_E_HIP;
-        if (st != hipStreamCaptureStatusNone)
-            return DDL_E_UNBOUND;  // the memory has to be there before a capture
-        const int rc = make();
+        rc = not_capturing(stream);
+        rc = rc ? rc : make();
         if (!rc)
             device = now;
         return rc;
+    }
+    // the memory has to be there before a capture
+    static int not_capturing(hipStream_t stream) {
+        hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
+        const int rc = hip_result(hipStreamIsCapturing(stream, &st));
+        return rc ? rc : st == hipStreamCaptureStatusNone ? DDL_OK : DDL_E_UNBOUND;
     }
     // hipFree waits for the device's work
     template <class... P>
@@ -121,15 +124,15 @@ struct Handle {
 
 template <class V>
 int upload(const std::vector<V> &v, V **d) {
-    void *p = nullptr;
-    if (hipMalloc(&p, std::max<size_t>(v.size(), 1) * sizeof(V)) != hipSuccess)
-        return DDL_E_NOMEM;
-    if (hipMemcpy(p, v.data(), v.size() * sizeof(V), hipMemcpyHostToDevice) != hipSuccess) {
-        (void)hipFree(p);
-        return DDL_E_HIP;
+    int rc = device_memory(d, std::max<size_t>(v.size(), 1));
+    if (rc)
+        return rc;
+    rc = hip_result(hipMemcpy(*d, v.data(), v.size() * sizeof(V), hipMemcpyHostToDevice));
+    if (rc) {
+        (void)hipFree(*d);
+        *d = nullptr;
     }
-    *d = (V *)p;
-    return DDL_OK;
+    return rc;
 }
 
 }  // namespace ddl

@@ -5,6 +5,7 @@ are binary32: k terms of magnitude |x||w| leave at most k u(f32) sum|x||w|,
 and each output is rounded once; activations are within 8 u(f32) of their
 value and their slopes at most 1.13.
 """
+import ctypes
 import math
 
 import pytest
@@ -630,3 +631,30 @@ def test_slopes_in_their_tails(act, dtype):
     slack = (4 * a[act] + 8) * F32 * (p + q.abs()) + 2.0 ** -125 * (1 + z.abs() ** 3)
     got = slopes(v, act, t)
     near(got, (p + q)[:, None].expand(got.shape), slack[:, None])
+
+
+def test_an_older_error_is_not_the_calls():
+    """An error that an earlier call of the HIP runtime left behind (here an
+    allocation of 2^60 bytes) is not reported by calls that succeed."""
+    hip, p = ddl.lib(), ctypes.c_void_p()
+    t, g_ = torch.bfloat16, gen(33)
+    x, w, dz = (normal(g_, 64, 64, dtype=t) for _ in range(3))
+    y, dw = torch.empty_like(x), torch.empty(64, 64, device="cuda")
+    db = torch.empty(64, device="cuda")
+    flat = [torch.zeros(4096, device="cuda") for _ in range(4)]
+    muon, adam = ddl.Muon([(0, 64, 64, 1.0)]), ddl.AdamW([(0, 4096)])
+    ws = workspace("wgrad", 64, 64, 64)
+    torch.cuda.synchronize()
+    calls = [lambda: ddl.linear(x, w, y, workspace=ws),
+             lambda: ddl.linear_dgrad(dz, w, y, workspace=ws),
+             lambda: ddl.linear_wgrad(dz, x, dw, db=db, workspace=ws),
+             lambda: muon.step(flat[0], flat[1], [flat[2]], lr=0.1),
+             lambda: muon.orthogonalise(flat[0], flat[1]),
+             lambda: adam.step(flat[0], flat[1], flat[2], [flat[3]], lr=0.1)]
+    try:
+        for call in calls:
+            assert hip.hipMalloc(ctypes.byref(p), ctypes.c_size_t(1 << 60)) != 0
+            call()
+    finally:
+        hip.hipGetLastError()
+        torch.cuda.synchronize()
