@@ -99,20 +99,26 @@ __device__ __forceinline__ uint32_t chunk_key(uint32_t row) {
 // 16 bytes of every lane to LDS at `lds` + 16 lane, without registers between.
 // Written in assembly because the compiler, which cannot tell the two buffers
 // apart, would make every LDS read wait for the copy into the other one; the
-// wait is wait_loads, before the barrier that opens the buffer.  The wait
+// wait is wait_and_meet, before the barrier that opens the buffer.  The wait
 // state between the write of m0 and its use is the s_nop.
+// m0 is declared, since the compiler merges its own writes of it; that it is a
+// reserved register, which the compiler warns of, is no harm: nothing of its
+// own lives there.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void load16_to_lds(const uint8_t *base, uint32_t off, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                  :
                  : "s"(lds), "v"(off), "s"(base)
-                 : "memory");
+                 : "m0", "memory");
 }
 __device__ __forceinline__ void load16_to_lds(const uint8_t *p, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
                  :
                  : "s"(lds), "v"(p)
-                 : "memory");
+                 : "m0", "memory");
 }
+#pragma clang diagnostic pop
 // Waits until at most N of the wave's copies to LDS are in flight and its own
 // LDS accesses are done, then for the workgroup's other waves.
 template <int N>

@@ -1,5 +1,8 @@
 """The linear layer and the optimizers without a GPU: sizes, refusals, handles."""
 import ctypes
+import glob
+import os
+import re
 
 import pytest
 import torch
@@ -213,3 +216,17 @@ def test_empty_spans_hide_no_overlap(spans):
 def test_empty_spans_overlap_nothing():
     a = ddl.AdamW([(0, 10), (5, 0), (10, 3), (13, 0), (12, 0)])
     assert a.need == 13
+
+
+def test_assembly_declares_m0():
+    """Inline assembly that writes m0 names it among its clobbers."""
+    csrc = os.path.join(os.path.dirname(ddl.__file__), "csrc")
+    found = 0
+    for path in glob.glob(os.path.join(csrc, "*")):
+        with open(path) as f:
+            text = f.read()
+        for asm in re.findall(r"\basm\b[^;]*;", text):
+            if re.search(r"s_mov_b32 m0", asm):
+                found += 1
+                assert re.search(r':[^:]*"m0"[^:]*$', asm), f"{path}: {asm}"
+    assert found == 2
