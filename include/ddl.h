@@ -473,8 +473,8 @@ int ddl_get_tuning(int knob, int *value);
  * workspace: device memory, 16-byte aligned, of at least
  * ddl_linear_workspace(op, m, n, k) bytes (NULL where that is 0), the call's
  * own until the work is done.  Everything is enqueued on `stream` on the
- * current device; no call allocates, synchronises or keeps state, so all of
- * them can be captured into a HIP graph.
+ * current device, where the arrays have to be; no call allocates, synchronises
+ * or keeps state, so all of them can be captured into a HIP graph.
  * Errors: DDL_E_NULL, DDL_E_ARG, DDL_E_ALIGN (an array not aligned to its
  * element, or the workspace not to 16 bytes), DDL_E_SCRATCH (workspace too
  * small), DDL_E_HIP. */

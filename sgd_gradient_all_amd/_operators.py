@@ -1,7 +1,7 @@
 """The linear layer's products and the Muon and AdamW steps (include/ddl.h).
 
-Argument checks and marshalling only.  Arrays are torch tensors on the GPU (or
-objects like them); streams as elsewhere (None = the null stream).
+Argument checks and marshalling only.  Arrays are torch tensors (or objects
+like them) on the current GPU; streams as elsewhere (None = the null stream).
 """
 import ctypes
 
@@ -98,11 +98,28 @@ def _act(act):
     return code
 
 
+_get_device = None
+
+
+def _current_device():
+    """The index of the GPU that kernels are launched on."""
+    global _get_device
+    if _get_device is None:
+        _get_device = _lib().hipGetDevice
+    now = ctypes.c_int()
+    if _get_device(ctypes.byref(now)):
+        raise RuntimeError("no current GPU")
+    return now.value
+
+
 def _device(t, what):
-    """The index of the GPU that t is on."""
+    """The index of the GPU that t is on, which has to be the current one."""
     d = t.get_device()
     if d < 0:
         raise ValueError(f"{what} is on {t.device}: expected a GPU tensor")
+    now = _current_device()
+    if d != now:
+        raise ValueError(f"{what} is on {t.device}: expected a tensor of the current GPU, {now}")
     return d
 
 

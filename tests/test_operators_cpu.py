@@ -230,3 +230,51 @@ def test_assembly_declares_m0():
                 found += 1
                 assert re.search(r':[^:]*"m0"[^:]*$', asm), f"{path}: {asm}"
     assert found == 2
+
+
+class OnDevice:
+    """A tensor's shape and place, without memory: every call below is refused
+    before it would use it."""
+
+    def __init__(self, index, *shape, dtype=torch.float16):
+        self.index, self.shape, self.dtype = index, shape, dtype
+        self.device = f"cuda:{index}"
+
+    def get_device(self):
+        return self.index
+
+    def stride(self, i=None):
+        s = [1]
+        for n in self.shape[:0:-1]:
+            s.insert(0, s[0] * n)
+        return tuple(s) if i is None else s[i]
+
+    def numel(self):
+        return int(torch.Size(self.shape).numel())
+
+    def is_contiguous(self):
+        return True
+
+    def element_size(self):
+        return self.dtype.itemsize
+
+    def data_ptr(self):
+        return None  # refused below the binding too
+
+
+@pytest.mark.parametrize("index,current", [(1, 0), (0, 1)])
+def test_arrays_of_another_device_are_refused(index, current, monkeypatch):
+    """Kernels are launched on the current device; arrays of another one would
+    be used from there without its streams' order."""
+    monkeypatch.setattr(ops, "_current_device", lambda: current, raising=False)
+    h = lambda *s: OnDevice(index, *s)  # noqa: E731
+    f = lambda *s: OnDevice(index, *s, dtype=torch.float32)  # noqa: E731
+    adam, muon = ddl.AdamW([(0, 4)]), ddl.Muon([(0, 2, 2, 1.0)])
+    for call in (lambda: ddl.linear(h(2, 8), h(4, 8), h(2, 4)),
+                 lambda: ddl.linear_dgrad(h(2, 4), h(4, 8), h(2, 8)),
+                 lambda: ddl.linear_wgrad(h(2, 4), h(2, 8), f(4, 8)),
+                 lambda: adam.step(f(4), f(4), f(4), [f(4)], lr=1.0),
+                 lambda: muon.orthogonalise(f(4), f(4)),
+                 lambda: muon.step(f(4), f(4), [f(4)], lr=1.0)):
+        with pytest.raises(ValueError, match="current"):
+            call()
