@@ -303,15 +303,10 @@ __global__ __launch_bounds__(Core::THREADS) void linear_kernel(GemmArgs g) {
     }
 }
 
-// The sums of the parts, in their order, and the epilogue.  8 columns a lane.
+// 8 columns of linear_join.
 template <class T>
-__global__ __launch_bounds__(256) void linear_join(Epilogue e, const float *partial,
-                                                   uint32_t splits) {
-    const uint64_t groups = (e.n + 7) / 8;
-    const uint64_t id = (uint64_t)blockIdx.x * 256 + threadIdx.x;
-    if (id >= groups * e.m)
-        return;
-    const uint64_t m = id / groups, n = id % groups * 8;
+__device__ __forceinline__ void join8(const Epilogue &e, const float *partial, uint32_t splits,
+                                      uint64_t m, uint64_t n) {
     const bool vec = e.n % 8 == 0;
     const Fetched f = vec && e.vec ? fetch8<T, true>(e, m, n) : fetch8<T, false>(e, m, n);
     float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -336,6 +331,20 @@ __global__ __launch_bounds__(256) void linear_join(Epilogue e, const float *part
         finish8<T, true>(e, m, n, v, f);
     else
         finish8<T, false>(e, m, n, v, f);
+}
+
+// The sums of the parts (none: empty sums), in their order, and the epilogue.
+// 8 columns a lane, and more than once only past kJoinLanes (empty sums of
+// very large outputs).
+constexpr uint64_t kJoinLanes = 1u << 31;  // a launch takes fewer than 2^32
+
+template <class T>
+__global__ __launch_bounds__(256) void linear_join(Epilogue e, const float *partial,
+                                                   uint32_t splits) {
+    const uint64_t groups = (e.n + 7) / 8;
+    for (uint64_t id = (uint64_t)blockIdx.x * 256 + threadIdx.x; id < groups * e.m;
+         id += kJoinLanes)
+        join8<T>(e, partial, splits, id / groups, id % groups * 8);
 }
 
 // A few rows (a decoded token, or up to 16): the weights are read once and
@@ -569,7 +578,7 @@ int product(const Operand &a, const Operand &b, const Epilogue &e, uint64_t k, v
         if (rc || g.splits == 1)
             return rc;
     }
-    const uint64_t lanes = (e.n + 7) / 8 * e.m;
+    const uint64_t lanes = std::min((e.n + 7) / 8 * e.m, kJoinLanes);
     return launch(linear_join<T>, dim3((uint32_t)((lanes + 255) / 256)), dim3(256), 0, s, e,
                   g.partial, g.splits);
 }

@@ -658,3 +658,15 @@ def test_an_older_error_is_not_the_calls():
     finally:
         hip.hipGetLastError()
         torch.cuda.synchronize()
+
+
+def test_empty_sums_over_many_rows():
+    """An empty sum's outputs (the bias alone) over more than 2^32 pieces of 8."""
+    m, n, t = 1 << 30, 25, torch.bfloat16
+    b = normal(gen(34), n, dtype=t)
+    y = torch.zeros(m, n, device="cuda", dtype=t)
+    e = torch.empty(m, 0, device="cuda", dtype=t)
+    ddl.linear(e, torch.empty(n, 0, device="cuda", dtype=t), y, bias=b)
+    for at in (0, m // 2, m - 1000):
+        assert torch.equal(y[at:at + 1000], b.expand(1000, n))
+    assert int((y[:, n - 1] != b[n - 1]).sum()) == 0
