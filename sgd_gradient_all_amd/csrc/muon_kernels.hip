@@ -609,6 +609,7 @@ struct ddl_muon_s {
     double *d_ws64 = nullptr;
     uint64_t slots = 0;  // partial tiles
     uint32_t tickets = 0;
+    std::vector<uint32_t> zeros;  // the tickets' start; made here: a step does not throw
 
     Handle dev;
     Mat *d_mats = nullptr;
@@ -710,6 +711,7 @@ void lay_out(ddl_muon_s &h) {
     deal(h, kGram, h.gram);
     deal(h, kPoly, h.poly);
     deal(h, kApply, h.apply);
+    h.zeros.assign(h.tickets, 0);
 }
 
 int bind_muon(ddl_muon_s &h, hipStream_t s) {
@@ -720,7 +722,7 @@ int bind_muon(ddl_muon_s &h, hipStream_t s) {
         rc = rc ? rc : upload(h.gram, &h.d_gram);
         rc = rc ? rc : upload(h.poly, &h.d_poly);
         rc = rc ? rc : upload(h.apply, &h.d_apply);
-        rc = rc ? rc : upload(std::vector<uint32_t>(h.tickets, 0), &h.d_tickets);
+        rc = rc ? rc : upload(h.zeros, &h.d_tickets);
         rc = rc ? rc : device_memory(&h.d_ws, h.ws);
         rc = rc ? rc
                 : device_memory(&h.d_partial,

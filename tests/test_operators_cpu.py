@@ -3,6 +3,7 @@ import ctypes
 import glob
 import os
 import re
+import subprocess
 
 import pytest
 import torch
@@ -278,3 +279,24 @@ def test_arrays_of_another_device_are_refused(index, current, monkeypatch):
                  lambda: muon.step(f(4), f(4), [f(4)], lr=1.0)):
         with pytest.raises(ValueError, match="current"):
             call()
+
+
+def test_handles_where_memory_runs_out(tmp_path):
+    """The optimizers' host code against a fake runtime that refuses every
+    allocation once (operators_host_driver.cpp)."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+    csrc, objects = os.path.join(root, "sgd_gradient_all_amd", "csrc"), []
+    for name in ("adamw_kernels.hip", "muon_kernels.hip"):
+        objects.append(str(tmp_path / (name + ".o")))
+        subprocess.run([hipcc, "--offload-arch=gfx950", "--offload-host-only", "-O1", "-std=c++17",
+                        "-fPIC", "-c", os.path.join(csrc, name), "-o", objects[-1]], check=True)
+    exe = str(tmp_path / "operators_host")
+    # the kernels' code, which is not built here, is the one name left open
+    subprocess.run(["g++", "-std=c++17", "-O1", "-D__HIP_PLATFORM_AMD__", "-I/opt/rocm/include",
+                    os.path.join(root, "tests", "operators_host_driver.cpp"),
+                    os.path.join(csrc, "optimizer.cpp"), *objects, "-o", exe,
+                    "-Wl,--unresolved-symbols=ignore-in-object-files"], check=True)
+    out = subprocess.run([exe], capture_output=True, text=True, timeout=60)
+    assert out.returncode == 0, out.stdout + out.stderr
+    assert re.fullmatch(r"ok \d\d+ refusals\n", out.stdout), out.stdout
