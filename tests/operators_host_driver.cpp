@@ -1,8 +1,13 @@
-// operators_host_driver.cpp -- the optimizers' handles where memory runs out.
+// operators_host_driver.cpp -- the operators' host code on a fake HIP runtime.
 //
-// The host code of the optimizers (no GPU code) is linked against a fake HIP
+// The host code of the operators (no GPU code) is linked against a fake HIP
 // runtime: device memory is host memory, launches are counted and run nothing.
-// Every allocation that a create or a first call makes, of the host or of the
+//
+// With arguments: the names of the kernels that a call launches, one a line.
+//   linear OP M N K          (OP 0, 1, 2: forward, dgrad, wgrad)
+//   muon ROWS COLS [ROWS COLS ..]
+//
+// Without: the optimizers' handles where memory runs out.  Every allocation that a create or a first call makes, of the host or of the
 // device, is refused once: the call has to return DDL_E_NOMEM, launch nothing,
 // leave no device memory (a first call), no host memory (a create) and no
 // error of the runtime behind, and succeed when it is made again.
@@ -12,7 +17,9 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <map>
 #include <new>
+#include <string>
 #include <vector>
 
 #include "../include/ddl.h"
@@ -20,6 +27,13 @@
 static long g_host_left = -1, g_device_left = -1;  // until one is refused; < 0: none
 static long g_host_live = 0, g_device_live = 0, g_launches = 0;
 static hipError_t g_last = hipSuccess;
+static bool g_print = false;
+
+// the kernels by the address that launches name; never destroyed
+static std::map<const void *, std::string> &kernels() {
+    static auto *m = new std::map<const void *, std::string>;
+    return *m;
+}
 
 static bool refuse(long &left) { return left >= 0 && left-- == 0; }
 
@@ -79,8 +93,10 @@ hipError_t hipGetLastError(void) {
     return e;
 }
 hipError_t hipFuncSetAttribute(const void *, hipFuncAttribute, int) { return hipSuccess; }
-hipError_t hipLaunchKernel(const void *, dim3, dim3, void **, size_t, hipStream_t) {
+hipError_t hipLaunchKernel(const void *f, dim3, dim3, void **, size_t, hipStream_t) {
     ++g_launches;
+    if (g_print)
+        std::printf("%s\n", kernels()[f].c_str());
     return hipSuccess;
 }
 // what the compiler's start-up code asks for
@@ -89,8 +105,10 @@ void **__hipRegisterFatBinary(const void *) {
     return &handle;
 }
 void __hipUnregisterFatBinary(void **) {}
-void __hipRegisterFunction(void **, const void *, char *, const char *, unsigned, void *, void *,
-                           void *, void *, int *) {}
+void __hipRegisterFunction(void **, const void *f, char *, const char *name, unsigned, void *,
+                           void *, void *, void *, int *) {
+    kernels()[f] = name;
+}
 void __hipRegisterVar(void **, void *, char *, char *, int, size_t, int, int) {}
 hipError_t __hipPopCallConfiguration(dim3 *, dim3 *, size_t *, hipStream_t *) {
     return hipSuccess;
@@ -135,7 +153,55 @@ static void each_refusal(const char *what, long &left, Make make, Call call, End
     }
 }
 
-int main() {
+// The kernels of one linear product over dense binary16 arrays, never touched.
+static int linear(int op, size_t m, size_t n, size_t k) {
+    void *p = (void *)(uintptr_t)4096;
+    const size_t all = (size_t)1 << 40;
+    if (op == DDL_LINEAR_FORWARD) {
+        ddl_linear_args a = {};
+        a.m = m, a.n = n, a.k = k, a.dtype = DDL_F16;
+        a.x = a.w = a.y = p;
+        a.ldx = a.ldw = k, a.ldy = n;
+        return ddl_linear(&a, p, all, nullptr);
+    }
+    if (op == DDL_LINEAR_DGRAD) {
+        ddl_dgrad_args a = {};
+        a.m = m, a.n = n, a.k = k, a.dtype = DDL_F16;
+        a.dz = a.w = a.dx = p;
+        a.lddz = n, a.ldw = a.lddx = k;
+        return ddl_linear_dgrad(&a, p, all, nullptr);
+    }
+    ddl_wgrad_args a = {};
+    a.m = m, a.n = n, a.k = k, a.dtype = DDL_F16, a.out_dtype = DDL_F32;
+    a.dz = a.x = a.dw = p;
+    a.lddz = n, a.ldx = a.lddw = k;
+    return ddl_linear_wgrad(&a, p, all, nullptr);
+}
+
+static int muon(int count, char **sides) {
+    std::vector<ddl_muon_matrix> mats;
+    size_t at = 0;
+    for (int i = 0; i + 1 < count; i += 2) {
+        mats.push_back({at, std::strtoull(sides[i], nullptr, 10),
+                        std::strtoull(sides[i + 1], nullptr, 10), 1.0});
+        at += mats.back().rows * mats.back().cols;
+    }
+    ddl_muon h = nullptr;
+    int rc = ddl_muon_create(&h, mats.data(), (int)mats.size());
+    float some = 0.0f, *w[] = {&some};
+    rc = rc ? rc
+            : ddl_muon_step(h, &some, DDL_F32, &some, w, 1, nullptr, 0, 0.1, 0.9, 1, 0.0, nullptr);
+    return rc ? rc : ddl_muon_destroy(h);
+}
+
+int main(int argc, char **argv) {
+    if (argc > 1) {
+        g_print = true;
+        auto number = [&](int i) { return std::strtoull(argv[i], nullptr, 10); };
+        return std::string(argv[1]) == "linear"
+                   ? linear((int)number(2), number(3), number(4), number(5))
+                   : muon(argc - 2, argv + 2);
+    }
     // two short matrices and a long one, whose sums are cut into parts
     const ddl_muon_matrix mats[] = {{0, 40, 48, 1.0}, {1920, 48, 40, 1.0}, {3840, 40, 20000, 1.0}};
     const size_t offs[] = {3, 5000}, counts[] = {4097, 11};

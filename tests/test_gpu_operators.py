@@ -670,3 +670,135 @@ def test_empty_sums_over_many_rows():
     for at in (0, m // 2, m - 1000):
         assert torch.equal(y[at:at + 1000], b.expand(1000, n))
     assert int((y[:, n - 1] != b[n - 1]).sum()) == 0
+
+
+# ---------------------------------------------------------------------------
+# the tiles of large products
+# ---------------------------------------------------------------------------
+
+def tiles(m, n, t):
+    return -(-m // t) * -(-n // t)
+
+
+def linear_tile(m, n, k):
+    """(side of the tile, parts of k) by the library's rule for an m x n output."""
+    t = 256 if tiles(m, n, 256) >= 192 else 128 if tiles(m, n, 128) >= 192 else 64
+    have, kt = tiles(m, n, t), -(-k // 64)
+    return t, max(1, min(512 // have, kt // 8, 64)) if have < 256 and kt >= 16 else 1
+
+
+def muon_tile(shapes):
+    def lower(t):
+        return sum(-(-min(s) // t) * (-(-min(s) // t) + 1) // 2 for s in shapes)
+    return 256 if lower(256) >= 256 else 128 if lower(128) >= 128 else 64
+
+
+# (side, parts, rows and columns of the output, length of the sums)
+LARGE = [(128, 1, 1496, 2104, 200), (128, 2, 1496, 2104, 1096), (256, 1, 3600, 3400, 264),
+         (256, 2, 3600, 3400, 1096), (128, 2, 1501, 2099, 1097), (256, 1, 3601, 3403, 203),
+         (256, 2, 3601, 3403, 1097)]
+LARGE_IDS = [f"{s[0]}x{s[1]}-{s[2]}x{s[3]}x{s[4]}" for s in LARGE]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("side,parts,m,n,k", LARGE, ids=LARGE_IDS)
+def test_linear_large_tiles(side, parts, m, n, k, dtype):
+    assert linear_tile(m, n, k) == (side, parts)
+    t, g_ = T[dtype], gen(m + n + k)
+    x, w = normal(g_, m, k, dtype=t), normal(g_, n, k, sigma=k ** -0.5, dtype=t)
+    b, r = normal(g_, n, sigma=0.1, dtype=t), normal(g_, m, n, dtype=t)
+    zw = x.double() @ w.double().t().contiguous() + b.double()
+    slack = (k + 4) * F32 * (x.double().abs() @ w.double().abs().t().contiguous()
+                             + b.double().abs())
+    y, z = (torch.empty(m, n, device="cuda", dtype=t) for _ in range(2))
+    ws = workspace("forward", m, n, k)
+    for act in ("none", "gelu", "gelu_tanh"):
+        print(f"linear {m} {n} {k} {dtype} {act}", flush=True)
+        ddl.linear(x, w, y, bias=b, act=act, residual=r, z=z, workspace=ws)
+        a = act64(zw, act)
+        near(z, zw, slack)
+        near(y, a + r.double(), 1.13 * slack + 8 * F32 * (a.abs() + r.double().abs()))
+    print(f"linear {m} {n} {k} {dtype} alone", flush=True)
+    ddl.linear(x, w, y, workspace=ws)
+    near(y, zw - b.double(), slack)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("side,parts,m,k,n", LARGE, ids=LARGE_IDS)
+def test_input_gradient_large_tiles(side, parts, m, k, n, dtype):
+    assert linear_tile(m, k, n) == (side, parts)
+    t, g_ = T[dtype], gen(m + n + k)
+    dz, w = normal(g_, m, n, dtype=t), normal(g_, n, k, sigma=n ** -0.5, dtype=t)
+    r, z = normal(g_, m, k, dtype=t), normal(g_, m, k, dtype=t)
+    want = dz.double() @ w.double() + r.double()
+    slack = (n + 4) * F32 * (dz.double().abs() @ w.double().abs() + r.double().abs())
+    dx, dp = (torch.empty(m, k, device="cuda", dtype=t) for _ in range(2))
+    for act in ("relu", "gelu", "silu"):
+        print(f"dgrad {m} {n} {k} {dtype} {act}", flush=True)
+        ddl.linear_dgrad(dz, w, dx, residual=r, act=act, z_prev=z, dz_prev=dp,
+                         workspace=workspace("dgrad", m, n, k))
+        near(dx, want, slack)
+        zz = z.double().requires_grad_()
+        slope, = torch.autograd.grad(act64(zz, act).sum(), zz)
+        if act == "relu":  # at 0, which the inputs hold here and there, the slope is 0
+            slope = (zz > 0).double()
+        near(dp, want * slope, slack * 1.13 + 16 * F32 * want.abs() * (1 + z.double().abs()))
+
+
+@pytest.mark.parametrize("dtype,out", [("f16", "f32"), ("bf16", "bf16")])
+@pytest.mark.parametrize("side,parts,n,k,m", LARGE, ids=LARGE_IDS)
+def test_weight_gradient_large_tiles(side, parts, n, k, m, dtype, out):
+    assert linear_tile(n, k, m) == (side, parts)
+    t, g_ = T[dtype], gen(m + n + k)
+    dz, x = normal(g_, m, n, dtype=t), normal(g_, m, k, dtype=t)
+    dw0, db0 = normal(g_, n, k, dtype=T[out]), normal(g_, n, dtype=T[out])
+    want = dz.double().t().contiguous() @ x.double()
+    slack = (m + 2) * F32 * (dz.double().abs().t().contiguous() @ x.double().abs())
+    bwant, bslack = dz.double().sum(0), (m + 2) * F32 * dz.double().abs().sum(0)
+    for add in (False, True):
+        print(f"wgrad {m} {n} {k} {dtype} {out} {add}", flush=True)
+        dw, db = dw0.clone(), db0.clone()
+        ddl.linear_wgrad(dz, x, dw, db=db, accumulate=add, workspace=workspace("wgrad", m, n, k))
+        old, bold = (dw0.double(), db0.double()) if add else (0 * dw0.double(), 0 * db0.double())
+        near(dw, want + old, slack + F32 * (want + old).abs() * 2)
+        near(db, bwant + bold, bslack + F32 * (bwant + bold).abs() * 2)
+
+
+# 128: sums in three parts; 256: whole sums, and sums of one long matrix in parts
+MUON_LARGE = [(128, [(2000, 2300)]), (128, [(2300, 2000)]),
+              (256, [(2100, 2300)] * 3 + [(2300, 2100)] * 3),
+              (256, [(40, 48)] * 128 + [(48, 40)] * 127 + [(40, 20000)]),
+              (256, [(48, 40)] * 255 + [(20000, 40)])]
+MUON_IDS = [f"{side}-{len(s)}x{s[-1][0]}x{s[-1][1]}" for side, s in MUON_LARGE]
+
+
+@pytest.mark.parametrize("side,shapes", MUON_LARGE, ids=MUON_IDS)
+def test_muon_large_tiles(side, shapes):
+    """A step, and orthogonalise in both 16-bit types.  The bound is four times
+    2^-20, the binary32 products' error that the entry point documents as 2e-6."""
+    assert muon_tile(shapes) == side
+    mats, size = pack(1, shapes)
+    h = ddl.Muon([(o, r, c, 0.5) for o, r, c in mats])
+    g_ = gen(size)
+    lr, mu = 0.5, 0.9
+    grad, mom = normal(g_, size, sigma=1e-2), normal(g_, size, sigma=3e-2)
+    w = normal(g_, size, sigma=0.02)
+    m64, w0 = mom.double(), w.double()
+    print(f"muon {side} {shapes[-1]}", flush=True)
+    h.step(grad, mom, [w], lr=lr, momentum_decay=mu, weight_decay=0.1)
+    outs = {}
+    for t in (torch.float16, torch.bfloat16):
+        outs[t] = (grad.to(t), torch.empty(size, device="cuda", dtype=t))
+        h.orthogonalise(*outs[t])
+    for i in {0, len(mats) // 2, len(mats) - 1}:
+        o, r, c = mats[i]
+        at = slice(o, o + r * c)
+        m = mu * m64[at] + grad[at].double()
+        x = orthogonal64((grad[at].double() + mu * m).view(r, c))
+        want = (1 - lr * 0.1) * w0[at] - lr * 0.5 * x.reshape(-1)
+        err = float((w[at].double() - want).norm())
+        assert err <= 4 * 2.0 ** -20 * lr * 0.5 * float(x.norm()) + 4 * F32 * float(want.norm())
+        for t, (g16, out) in outs.items():
+            want = orthogonal64(g16[at].view(r, c))
+            err = float((out[at].view(r, c).double() - want).norm() / want.norm())
+            assert err <= 4 * 2.0 ** -20 + u(t)

@@ -9,6 +9,7 @@ import pytest
 import torch
 
 import sgd_gradient_all_amd as ddl
+import test_gpu_operators as gpu_tests
 from sgd_gradient_all_amd import _operators as ops
 
 E_NULL, E_ARG, E_BUCKETS, E_ALIGN, E_SCRATCH = -1, -2, -3, -4, -10
@@ -281,22 +282,58 @@ def test_arrays_of_another_device_are_refused(index, current, monkeypatch):
             call()
 
 
-def test_handles_where_memory_runs_out(tmp_path):
-    """The optimizers' host code against a fake runtime that refuses every
-    allocation once (operators_host_driver.cpp)."""
+@pytest.fixture(scope="module")
+def host_driver(tmp_path_factory):
+    """The operators' host code on a fake runtime (operators_host_driver.cpp)."""
+    tmp = tmp_path_factory.mktemp("operators_host")
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
     csrc, objects = os.path.join(root, "sgd_gradient_all_amd", "csrc"), []
-    for name in ("adamw_kernels.hip", "muon_kernels.hip"):
-        objects.append(str(tmp_path / (name + ".o")))
+    for name in ("adamw_kernels.hip", "linear_kernels.hip", "muon_kernels.hip"):
+        objects.append(str(tmp / (name + ".o")))
         subprocess.run([hipcc, "--offload-arch=gfx950", "--offload-host-only", "-O1", "-std=c++17",
                         "-fPIC", "-c", os.path.join(csrc, name), "-o", objects[-1]], check=True)
-    exe = str(tmp_path / "operators_host")
+    exe = str(tmp / "operators_host")
     # the kernels' code, which is not built here, is the one name left open
     subprocess.run(["g++", "-std=c++17", "-O1", "-D__HIP_PLATFORM_AMD__", "-I/opt/rocm/include",
                     os.path.join(root, "tests", "operators_host_driver.cpp"),
                     os.path.join(csrc, "optimizer.cpp"), *objects, "-o", exe,
                     "-Wl,--unresolved-symbols=ignore-in-object-files"], check=True)
-    out = subprocess.run([exe], capture_output=True, text=True, timeout=60)
-    assert out.returncode == 0, out.stdout + out.stderr
-    assert re.fullmatch(r"ok \d\d+ refusals\n", out.stdout), out.stdout
+
+    def run(*args):
+        out = subprocess.run([exe, *map(str, args)], capture_output=True, text=True, timeout=60)
+        assert out.returncode == 0, out.stdout + out.stderr
+        return out.stdout
+    return run
+
+
+def test_handles_where_memory_runs_out(host_driver):
+    """Every allocation of the optimizers' host code is refused once."""
+    out = host_driver()
+    assert re.fullmatch(r"ok \d\d+ refusals\n", out), out
+
+
+def side_of(name):
+    """The side of a product kernel's tile, from its mangled name."""
+    return int(re.search(r"Core.*?Li(\d+)ELi(\d+)E", name).group(1))
+
+
+@pytest.mark.parametrize("op,order", [(0, "mnk"), (1, "mkn"), (2, "nkm")])
+def test_large_linear_cases_take_their_tiles(op, order, host_driver):
+    """The GPU tests' sizes reach the tiles and the parts of sums that they name."""
+    for side, parts, *sizes in gpu_tests.LARGE:
+        size = dict(zip(order, sizes))
+        names = host_driver("linear", op, size["m"], size["n"], size["k"]).split()
+        product, *rest = [x for x in names if "column" not in x]
+        assert "linear_kernel" in product and side_of(product) == side
+        assert len(rest) == (parts > 1) and all("linear_join" in x for x in rest)
+        # the last of the tile's flags: whether rows go through registers
+        staged = re.search(r"Lb\dELb\dELb(\d)E", product).group(1) == "1"
+        assert staged == (sizes[0] % 8 != 0)
+
+
+def test_large_muon_cases_take_their_tiles(host_driver):
+    for side, shapes in gpu_tests.MUON_LARGE:
+        names = host_driver("muon", *[n for s in shapes for n in s]).split()
+        products = [x for x in names if "product_kernel" in x]
+        assert len(products) == 15 and {side_of(x) for x in products} == {side}
