@@ -676,15 +676,35 @@ void lay_out(ddl_muon_s &h) {
     // The largest tile of which A's lower triangles give every compute unit
     // one (256) or every other (128): with fewer, too few workgroups hide each
     // other's waits, and the sums over k are cut into more parts to join
-    // (ResNet-50's matrices: 2.4 ms with 256, 1.3 ms with 128; one 4096 x 1024
-    // in bfloat16: 645 us with 128, 590 us with 64).
+    // (ResNet-50's matrices: 2.2 ms with 256, 1.3 ms with 128; one 4096 x 1024
+    // in bfloat16: 636 us with 128, 590 us with 64).  And of which the products
+    // that are issued, padding and halves above the diagonal included, are not
+    // more than what a larger tile's rate makes up for: 1.45 times those of 64
+    // (1.43 times, 100 of 400 x 1600: 4.09 ms with 64, 3.87 with 128; 1.54
+    // times, 100 of 300 x 900: 1.48 and 1.81 ms; 8 times, 300 of 64 x 64: 106
+    // and 242 us, with 256 1095 us), 1.03 times those of 128 (1.03 times, 8 of
+    // 2304 x 2304: 8.02 ms with 128, 7.53 with 256; 1.06 times, 26 of 1024 x
+    // 1024: 2.76 and 3.03 ms).
     auto triangles = [&](uint32_t T) {
         uint64_t n = 0;
         for (const Mat &m : h.mats)
             n += (uint64_t)(up(m.s, T) / T) * (up(m.s, T) / T + 1) / 2;
         return n;
     };
-    h.tile = triangles(256) >= 256 ? 256 : triangles(128) >= 128 ? 128 : 64;
+    auto issued = [&](uint32_t T) {
+        double n = 0;
+        for (const Mat &m : h.mats) {
+            const double s = up(m.s, T), l = up(m.l, T);
+            n += s * (s + T) / 2 * (l + s) + s * s * l;
+        }
+        return n;
+    };
+    h.tile = 64;
+    if (triangles(128) >= 128 && issued(128) <= 1.45 * issued(64)) {
+        h.tile = 128;
+        if (triangles(256) >= 256 && issued(256) <= 1.03 * issued(128))
+            h.tile = 256;
+    }
     for (uint32_t i = 0; i < h.mats.size(); ++i) {
         Mat &m = h.mats[i];
         m.sp = up(m.s, h.tile);

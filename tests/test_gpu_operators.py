@@ -688,9 +688,18 @@ def linear_tile(m, n, k):
 
 
 def muon_tile(shapes):
+    def up(n, t):
+        return -(-n // t) * t
+
     def lower(t):
-        return sum(-(-min(s) // t) * (-(-min(s) // t) + 1) // 2 for s in shapes)
-    return 256 if lower(256) >= 256 else 128 if lower(128) >= 128 else 64
+        return sum(up(min(s), t) // t * (up(min(s), t) // t + 1) // 2 for s in shapes)
+
+    def issued(t):
+        both = [(up(min(s), t), up(max(s), t)) for s in shapes]
+        return sum(s * (s + t) / 2 * (n + s) + s * s * n for s, n in both)
+    if lower(128) < 128 or issued(128) > 1.45 * issued(64):
+        return 64
+    return 256 if lower(256) >= 256 and issued(256) <= 1.03 * issued(128) else 128
 
 
 # (side, parts, rows and columns of the output, length of the sums)
@@ -766,9 +775,10 @@ def test_weight_gradient_large_tiles(side, parts, n, k, m, dtype, out):
 
 # 128: sums in three parts; 256: whole sums, and sums of one long matrix in parts
 MUON_LARGE = [(128, [(2000, 2300)]), (128, [(2300, 2000)]),
-              (256, [(2100, 2300)] * 3 + [(2300, 2100)] * 3),
-              (256, [(40, 48)] * 128 + [(48, 40)] * 127 + [(40, 20000)]),
-              (256, [(48, 40)] * 255 + [(20000, 40)])]
+              (128, [(2100, 2300)] * 3 + [(2300, 2100)] * 3),
+              (256, [(2300, 2304)] * 4 + [(2304, 2300)] * 4),
+              (256, [(2300, 2304)] * 8 + [(2290, 40000)]),
+              (256, [(2304, 2300)] * 8 + [(40000, 2290)])]
 MUON_IDS = [f"{side}-{len(s)}x{s[-1][0]}x{s[-1][1]}" for side, s in MUON_LARGE]
 
 

@@ -332,8 +332,13 @@ def test_large_linear_cases_take_their_tiles(op, order, host_driver):
         assert staged == (sizes[0] % 8 != 0)
 
 
-def test_large_muon_cases_take_their_tiles(host_driver):
-    for side, shapes in gpu_tests.MUON_LARGE:
-        names = host_driver("muon", *[n for s in shapes for n in s]).split()
-        products = [x for x in names if "product_kernel" in x]
-        assert len(products) == 15 and {side_of(x) for x in products} == {side}
+@pytest.mark.parametrize("side,shapes", gpu_tests.MUON_LARGE + [
+    (64, [(64, 64)] * 300), (64, [(16, 4096)] * 300), (64, [(300, 900)] * 100),
+    (64, [(4096, 16)] * 300), (64, [(4096, 1024)]), (128, [(400, 1600)] * 100),
+    (128, [(512, 512)] * 100), (128, [(1024, 1024)] * 26), (256, [(4096, 4096)] * 3)])
+def test_muon_takes_the_tile_that_its_matrices_fill(side, shapes, host_driver):
+    """Padding is not counted as work: many small matrices keep small tiles."""
+    assert gpu_tests.muon_tile(shapes) == side
+    names = host_driver("muon", *[n for s in shapes for n in s]).split()
+    products = [x for x in names if "product_kernel" in x]
+    assert len(products) == 15 and {side_of(x) for x in products} == {side}
