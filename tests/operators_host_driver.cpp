@@ -173,7 +173,7 @@ static int linear(int op, size_t m, size_t n, size_t k) {
     }
     ddl_wgrad_args a = {};
     a.m = m, a.n = n, a.k = k, a.dtype = DDL_F16, a.out_dtype = DDL_F32;
-    a.dz = a.x = a.dw = p;
+    a.dz = a.x = a.dw = a.db = p;
     a.lddz = n, a.ldx = a.lddw = k;
     return ddl_linear_wgrad(&a, p, all, nullptr);
 }

@@ -342,3 +342,13 @@ def test_muon_takes_the_tile_that_its_matrices_fill(side, shapes, host_driver):
     names = host_driver("muon", *[n for s in shapes for n in s]).split()
     products = [x for x in names if "product_kernel" in x]
     assert len(products) == 15 and {side_of(x) for x in products} == {side}
+
+
+@pytest.mark.parametrize("m,slices", [(0, 1), (1, 1), (1000, 1), (1024, 2), (2048, 4),
+                                      (1 << 20, 32)])
+def test_bias_gradients_of_many_rows_take_several_workgroups(m, slices, host_driver):
+    names = host_driver("linear", 2, m, 1000, 64).split()
+    assert sum("column_join" in x for x in names) == (slices > 1)
+    # workspace: the slices' sums, next to the parts of the product
+    alone = ddl.linear_workspace("dgrad", 1000, m, 64)  # the same product without db
+    assert ddl.linear_workspace("wgrad", m, 1000, 64) - alone == (slices > 1) * slices * 1000 * 4
