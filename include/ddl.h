@@ -560,8 +560,9 @@ int ddl_linear_wgrad(const ddl_wgrad_args *args, void *workspace, size_t workspa
  * before a capture into a HIP graph, otherwise DDL_E_UNBOUND); later calls
  * allocate nothing and run on that device (otherwise DDL_E_DEVICE).  Calls
  * are asynchronous on `stream`; two Muon calls of one handle that may run at
- * the same time on the device race on its workspace: order them.  Destroying
- * a handle waits for the device's work; a handle must outlive the graphs
+ * the same time on the device race on its workspace: order them.  On the
+ * host, calls on handles take turns, a first call's allocations included.
+ * Destroying a handle waits for the device's work; a handle must outlive the graphs
  * captured from it.
  * Errors: DDL_E_NULL, DDL_E_ARG (sizes, types, non-finite settings, or not a
  * live handle), DDL_E_BUCKETS (spans overlap or pass 2^40 elements),
@@ -594,13 +595,16 @@ typedef struct ddl_muon_s *ddl_muon;
  *     A = X X^T,  X <- 3.4445 X + (-4.7750 A + 2.0315 A A) X
  *   (on U^T where rows > cols), which takes every singular value that is not
  *   tiny to the neighbourhood of 1.
- * rows, cols <= 65536; extents of 0 are allowed. */
+ * rows, cols <= 65536; extents of 0 are allowed.
+ * The first call allocates 8 s (l + s) bytes for each matrix, s and l being
+ * its shorter and longer side rounded up to whole tiles (of 64, 128 or 256, one
+ * size for the handle), up to 128 MiB for sums in parts, and tables; the first
+ * orthogonalise in DDL_F32 16 s (l + s) bytes more. */
 int ddl_muon_create(ddl_muon *out, const ddl_muon_matrix *matrices, int nmatrices);
 /* out = orthogonal(grad) for every matrix, in grad's type.  DDL_F32 is
- * computed in binary64 (its workspace, four times the matrices' size and
- * more, is allocated by the first such call); the 16-bit types with products
- * of pairs of binary16 values (22 significant bits), as close as binary32
- * products, and rounded once.  out may be grad. */
+ * computed in binary64; the 16-bit types with products of pairs of binary16
+ * values (22 significant bits), as close as binary32 products, and rounded
+ * once.  out may be grad. */
 int ddl_muon_orthogonalise(ddl_muon handle, const void *grad, void *out, int dtype,
                            void *stream);
 /* momentum = momentum_decay momentum + g;

@@ -645,6 +645,8 @@ void deal(ddl_muon_s &h, int kind, std::vector<Work> &out) {
             steps += depth(m);
         });
     // parts of at most this many k tiles: the load of one of 512 equal shares
+    // (ResNet-50's matrices: 1.32 ms, uncut 1.84, of 1024 shares 1.46; one 4096
+    // x 1024 in 16 bits: 590 us, 886 and 649)
     const uint64_t share = std::max<uint64_t>((steps + 511) / 512, 16);
     uint64_t slots = 0;
     uint32_t tickets = 0;
