@@ -247,15 +247,8 @@ struct Core {
     __device__ __forceinline__ static void multiply(uint32_t la, uint32_t lb, f32x4 (&acc)[FM][FN]) {
         const uint32_t wave = threadIdx.x >> 6;
         const uint32_t ma = (wave / WC) * (FM * 16), nb = (wave % WC) * (FN * 16);
-        // Waves w and w + 4 share a SIMD and leave the barrier together: they
-        // take the tile's halves in opposite order, so that one reads while
-        // the other multiplies (256 x 256 tiles: 4096 x 4096 x 16384 from
-        // 1180 to 1280 TFLOP/s, both row by row from 1160 to 1215).
-        const uint32_t turn =
-            WR * WC > 4 ? __builtin_amdgcn_readfirstlane(wave >> 2) & 1u : 0u;
 #pragma unroll
-        for (uint32_t half = 0; half < BK / 32; ++half) {
-            const uint32_t kk = half ^ turn;
+        for (uint32_t kk = 0; kk < BK / 32; ++kk) {
             s16x8 b[FN];
 #pragma unroll
             for (int j = 0; j < FN; ++j)
@@ -360,8 +353,8 @@ struct Core {
     // What the epilogue reads comes from fetch, AHEAD pieces before the stores
     // of the first, so that a piece need not wait for memory by itself: four
     // with waves of 64 rows (128 x 128 tiles); with 128 rows the registers
-    // spill (8192 x 16384 x 4096 with GELU: 1036 us two ahead, 1000 us one), with 32
-    // there are two pieces.
+    // spill (8192 x 16384 x 4096 with GELU by tanh and z: 1036 us two ahead,
+    // 1007 us one), with 32 there are two pieces.
     template <bool TURNED = false, int AHEAD = (BM_ / WR_ == 64 ? 4 : 1), class G, class F>
     __device__ __forceinline__ static void each(const f32x4 (&acc)[FM][FN], uint8_t *lds,
                                                 G &&fetch, F &&then) {
