@@ -543,6 +543,67 @@ int ddl_linear_dgrad(const ddl_dgrad_args *args, void *workspace, size_t workspa
 int ddl_linear_wgrad(const ddl_wgrad_args *args, void *workspace, size_t workspace_bytes,
                      void *stream);
 
+/* ---- softmax cross entropy ----------------------------------------------- *
+ * The loss of a projection onto n classes and its gradient, without the m x n
+ * logits in memory: x m x k and weights w n x k, row-major, in DDL_F16 or
+ * DDL_BF16, as in the linear layer.
+ *
+ *   z = x w^T + bias,   lse_i = log sum_j exp z_ij
+ *   loss_i = lse_i - (1 - a) z_i,target(i) - a mean_j z_ij     (a: smoothing)
+ *   dz_ij = dloss_i scale (exp(z_ij - lse_i) - (1 - a) [j = target(i)] - a / n)
+ *   dx = dz w,   dw = dz^T x,   db = column sums of dz
+ *
+ * target: m classes; a negative one is none: the row's loss and lse are 0, and
+ * so is its gradient, whatever x holds there.  A target of n or more makes the
+ * row's loss, and every gradient that the row reaches, NaN.  bias may be -inf in
+ * classes that are never wanted; a row whose logits are all -inf has lse -inf and
+ * loss NaN.  Rows whose dloss scale is 0 count as rows without a target.
+ *
+ * Logits, sums and exponentials are binary32.  The gradient takes the classes
+ * in pieces: it computes their logits again and holds dz of one piece in 16 bits
+ * (scaled by a power of two, so that binary16 does not underflow), which
+ * dx and dw in 16 bits see as an error of up to their own rounding.  dw in
+ * DDL_F32 is computed from dz as a sum of two 16-bit values: 16 significant
+ * bits in DDL_BF16, 22 in DDL_F16.  db is summed before dz is rounded.
+ *
+ * ld*, alignment, workspace, stream, capture and errors as in the linear layer;
+ * m and n and k up to 2^22, n at least 1.  Results are the same from call to
+ * call. */
+enum { DDL_CE_FORWARD = 0, DDL_CE_GRAD = 1 };
+
+typedef struct {
+    size_t m, n, k;
+    int dtype;
+    double smoothing;        /* 0 .. 1 */
+    const void *x;           /* m x k */
+    size_t ldx;
+    const void *w;           /* n x k */
+    size_t ldw;
+    const void *bias;        /* NULL or n */
+    const long long *target; /* m */
+    float *loss;             /* m; not used by the gradient */
+    float *lse;              /* m: written by the loss, read by the gradient */
+} ddl_ce_args;
+
+typedef struct {
+    ddl_ce_args layer;
+    const float *dloss;      /* NULL (all 1) or m */
+    double scale;
+    void *dx;                /* NULL or m x k, of the layer's dtype */
+    size_t lddx;
+    void *dw;                /* NULL or n x k */
+    size_t lddw;
+    void *db;                /* NULL or n */
+    int dw_dtype;            /* of dw and db: DDL_F32 or the layer's dtype */
+    int accumulate;          /* 1: dw and db are added to */
+} ddl_ce_grad_args;
+
+int ddl_cross_entropy_workspace(int op, size_t m, size_t n, size_t k, size_t *bytes);
+int ddl_cross_entropy(const ddl_ce_args *args, void *workspace, size_t workspace_bytes,
+                      void *stream);
+int ddl_cross_entropy_grad(const ddl_ce_grad_args *args, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
 /* ---- optimizers ---------------------------------------------------------- *
  * The steps that follow the all-reduce where plain SGD and LARS do not: Muon
  * for the matrices of a flat parameter buffer, AdamW for the rest of it.

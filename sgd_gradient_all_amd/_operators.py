@@ -10,6 +10,7 @@ from ._ddl import DDL_F16, DDL_F32, _check, _ptr, lib
 DDL_BF16 = 2
 ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 _LINEAR_OPS = {"forward": 0, "dgrad": 1, "wgrad": 2}
+_CE_OPS = {"forward": 0, "grad": 1}
 _TYPES = {"torch.float32": DDL_F32, "torch.float16": DDL_F16, "torch.bfloat16": DDL_BF16}
 NORM_EPS = 1e-7  # added to the norm before Muon's first product
 
@@ -41,6 +42,21 @@ class ddl_wgrad_args(ctypes.Structure):
                    ("db", ctypes.c_void_p)])
 
 
+class ddl_ce_args(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_size_t) for n in "mnk"]
+                + [("dtype", ctypes.c_int), ("smoothing", ctypes.c_double),
+                   ("x", ctypes.c_void_p), ("ldx", ctypes.c_size_t), ("w", ctypes.c_void_p),
+                   ("ldw", ctypes.c_size_t)]
+                + [(n, ctypes.c_void_p) for n in ("bias", "target", "loss", "lse")])
+
+
+class ddl_ce_grad_args(ctypes.Structure):
+    _fields_ = [("layer", ddl_ce_args), ("dloss", ctypes.c_void_p), ("scale", ctypes.c_double),
+                ("dx", ctypes.c_void_p), ("lddx", ctypes.c_size_t), ("dw", ctypes.c_void_p),
+                ("lddw", ctypes.c_size_t), ("db", ctypes.c_void_p), ("dw_dtype", ctypes.c_int),
+                ("accumulate", ctypes.c_int)]
+
+
 class ddl_muon_matrix(ctypes.Structure):
     _fields_ = [("offset", ctypes.c_size_t), ("rows", ctypes.c_size_t),
                 ("cols", ctypes.c_size_t), ("scale", ctypes.c_double)]
@@ -60,6 +76,9 @@ def _lib():
             "ddl_linear": [P(ddl_linear_args), vp, sz, vp],
             "ddl_linear_dgrad": [P(ddl_dgrad_args), vp, sz, vp],
             "ddl_linear_wgrad": [P(ddl_wgrad_args), vp, sz, vp],
+            "ddl_cross_entropy_workspace": [i32, sz, sz, sz, P(sz)],
+            "ddl_cross_entropy": [P(ddl_ce_args), vp, sz, vp],
+            "ddl_cross_entropy_grad": [P(ddl_ce_grad_args), vp, sz, vp],
             "ddl_adamw_create": [P(vp), P(sz), P(sz), i32],
             "ddl_adamw_step": [vp, vp, i32, vp, vp, P(vp), i32, vp, i32, f64, f64, f64, f64, f64,
                                ctypes.c_longlong, vp],
@@ -244,6 +263,82 @@ def linear_wgrad(dz, x, dw, db=None, accumulate=False, workspace=None, stream=No
     rc = (_bound or _lib()).ddl_linear_wgrad(ctypes.byref(a), ws, size, _ptr(stream))
     if rc:
         _check(rc, "ddl_linear_wgrad")
+
+
+def cross_entropy_workspace(op, m, n, k):
+    """Bytes of workspace that `op` ("forward": cross_entropy, or "grad") takes
+    for x m x k and w n x k (ddl_cross_entropy_workspace)."""
+    if op not in _CE_OPS:
+        raise ValueError(f"unknown operation {op!r}: expected one of {', '.join(_CE_OPS)}")
+    if min(m, n, k) < 0:
+        raise ValueError(f"negative size in ({m}, {n}, {k})")
+    b = ctypes.c_size_t()
+    _check(_lib().ddl_cross_entropy_workspace(_CE_OPS[op], m, n, k, ctypes.byref(b)),
+           "ddl_cross_entropy_workspace")
+    return b.value
+
+
+def _targets(t, m, device):
+    if len(t.shape) != 1 or t.shape[0] != m or (m > 1 and t.stride(0) != 1):
+        raise ValueError(f"target has shape {tuple(t.shape)}, strides {tuple(t.stride())}: "
+                         f"expected {m} contiguous elements")
+    if t.get_device() != device or str(t.dtype) != "torch.int64":
+        raise ValueError(f"target is {t.dtype} on {t.device}: expected int64 on device {device}")
+    return t.data_ptr()
+
+
+def _floats(t, n, device, what):
+    """The pointer of n contiguous float32 elements."""
+    if t is not None and _type(t, what) != DDL_F32:
+        raise ValueError(f"{what} has type {t.dtype}: expected float32")
+    return _vector(t, n, device, t.dtype if t is not None else None, what)
+
+
+def _ce_layer(x, w, target, bias, smoothing):
+    m, k = _two(x, "x")
+    n = _two(w, "w")[0]
+    code = _type(x, "x")
+    d, t = _device(x, "x"), x.dtype
+    px, ldx = _matrix(x, m, k, d, t, "x")
+    pw, ldw = _matrix(w, n, k, d, t, "w")
+    a = ddl_ce_args(m, n, k, code, smoothing, px, ldx, pw, ldw, _vector(bias, n, d, t, "bias"),
+                    _targets(target, m, d))
+    return a, d
+
+
+def cross_entropy(x, w, target, loss, lse, bias=None, smoothing=0.0, workspace=None, stream=None):
+    """loss = the softmax cross entropy of the classes' logits x w^T + bias, and
+    their log-sum-exp into lse, without the logits in memory (ddl_cross_entropy).
+    x (m, k), w (n, k) and bias (n), all float16 or all bfloat16; target (m) int64,
+    negative: no target, loss and lse 0; loss and lse (m) float32."""
+    a, d = _ce_layer(x, w, target, bias, smoothing)
+    a.loss, a.lse = _floats(loss, a.m, d, "loss"), _floats(lse, a.m, d, "lse")
+    ws, size = _workspace(workspace, d)
+    rc = (_bound or _lib()).ddl_cross_entropy(ctypes.byref(a), ws, size, _ptr(stream))
+    if rc:
+        _check(rc, "ddl_cross_entropy")
+
+
+def cross_entropy_grad(x, w, target, lse, dloss=None, scale=1.0, dx=None, dw=None, db=None,
+                       bias=None, smoothing=0.0, accumulate=False, workspace=None, stream=None):
+    """The gradient of sum(dloss * scale * loss) (ddl_cross_entropy_grad), from
+    cross_entropy's lse: into dx (m, k) in x's type; into, or with accumulate
+    added to, dw (n, k) and db (n) in float32 or in x's type.  dloss (m) float32,
+    or None for ones.  Outputs that are None are not computed."""
+    a, d = _ce_layer(x, w, target, bias, smoothing)
+    m, n, k, t = a.m, a.n, a.k, x.dtype
+    a.lse = _floats(lse, m, d, "lse")
+    like = dw if dw is not None else db
+    out = t if like is None else like.dtype
+    px, ldx = _matrix(dx, m, k, d, t, "dx")
+    pw, ldw = _matrix(dw, n, k, d, out, "dw")
+    g = ddl_ce_grad_args(a, _floats(dloss, m, d, "dloss"), scale, px, ldx, pw, ldw,
+                         _vector(db, n, d, out, "db"),
+                         a.dtype if like is None else _type(like, "dw"), int(bool(accumulate)))
+    ws, size = _workspace(workspace, d)
+    rc = (_bound or _lib()).ddl_cross_entropy_grad(ctypes.byref(g), ws, size, _ptr(stream))
+    if rc:
+        _check(rc, "ddl_cross_entropy_grad")
 
 
 def _flat(t, need, what, codes=None, device=None):

@@ -1,0 +1,627 @@
+// cross_entropy_grad.hip -- the cross entropy's gradient (gfx950), from the
+// forward pass's lse:
+//
+//     dz_ij = dloss_i scale (exp(z_ij - lse_i) - (1 - a) [j = target(i)] - a / n)
+//     dx = dz w,   dw = dz^T x,   db = the column sums of dz
+//
+// The classes go through in pieces: a piece's logits are computed again, dz
+// leaves the matrix instruction's registers in 16 bits, and two products take it
+// from there.  So the memory held is a piece's dz, whatever the number of
+// classes, and the price is one product more than with all logits kept.
+//
+// dz's rounding is the one that results see besides their own: 16-bit outputs
+// are up to sqrt(2) of their own rounding off.  Binary32 dw would lose half of
+// its digits that way, so for it dz is held as a sum of two 16-bit values (16
+// significant bits in bfloat16, 22 in binary16) and its product takes two
+// passes.  db is summed from dz before it is rounded.
+#include <hip/hip_runtime.h>
+#include <math.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "cross_entropy_internal.h"
+
+namespace ddl {
+namespace {
+
+using gemm::Bfloat;
+using gemm::f32x4;
+using gemm::Half;
+
+// ---------------------------------------------------------------------------
+// dz of a piece
+// ---------------------------------------------------------------------------
+
+struct DzArgs {
+    Rows rows;
+    Operand x, w;           // w: the piece's rows
+    const void *bias;       // T, the piece's, or null
+    uint32_t tn, n;         // the piece's tiles and columns
+    uint32_t first;         // its first class
+    float smooth, wanted;   // a / n, 1 - a
+    uint16_t *dz[2];        // [count][ld]; the low parts: or null
+    uint64_t ld;            // n rounded up to 64; columns past n are 0
+    float *db;              // [row tile][ld]: column sums, or null
+};
+
+struct RowOf {
+    float lse, g;
+    uint32_t want;  // target - the piece's first class
+    u32x4 bias[1];
+};
+
+template <class T, class Core>
+__global__ __launch_bounds__(Core::THREADS) void dz_kernel(DzArgs a) {
+    using E = typename T::E;
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    constexpr uint32_t BM = Core::BM, BN = Core::BN;
+    const uint32_t count = a.rows.head->count, tm = (count + BM - 1) / BM;
+    if (blockIdx.x >= tm * a.tn)
+        return;
+    uint32_t ti, tj;
+    tile_of(blockIdx.x, tm, a.tn, ti, tj);
+    a.x.row0 = ti * BM;
+    a.x.rows = count;
+    a.w.row0 = tj * BN;
+    const float factor = a.rows.head->factor;
+    f32x4 acc[Core::FM][Core::FN] = {};
+    if (a.x.k)
+        Core::run(a.x, a.w, 0, (uint32_t)((a.x.k + Core::BK - 1) / Core::BK), 0, lds, acc);
+    const uint32_t m0 = ti * BM, n0 = tj * BN;
+    float sums[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    Core::template each<false, 1>(
+        acc, lds,
+        [&](uint32_t mi, uint32_t ni) {
+            RowOf f;
+            const uint32_t m = m0 + mi, n = n0 + ni;
+            if (m >= count || n >= a.ld)
+                return f;
+            f.lse = a.rows.lse[m];
+            f.g = a.rows.g[m];
+            f.want = (uint32_t)a.rows.target[m] - a.first;
+            if (a.bias)
+                load8<false>((const E *)a.bias + n, n < a.n ? a.n - n : 0, f.bias);
+            return f;
+        },
+        [&](uint32_t mi, uint32_t ni, float (&v)[8], const RowOf &f) {
+            const uint32_t m = m0 + mi, n = n0 + ni;
+            if (m >= count || n >= a.ld)
+                return;
+            if (a.bias) {
+                float b[8];
+                widen8<E>(f.bias, b);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[e] += b[e];
+            }
+            float low[8];
+            const float g = f.g * factor;
+#pragma unroll
+            for (uint32_t e = 0; e < 8; ++e) {
+                float p = __builtin_amdgcn_exp2f((v[e] - f.lse) * kLog2e) - a.smooth;
+                if (n + e == f.want)
+                    p -= a.wanted;
+                p = n + e < a.n ? p * g : 0.0f;
+                sums[e] += p;
+                v[e] = p;
+                low[e] = p - (float)(E)p;
+            }
+            store8<true>((E *)a.dz[0] + m * a.ld + n, 8, v);
+            if (a.dz[1])
+                store8<true>((E *)a.dz[1] + m * a.ld + n, 8, low);
+        });
+    if (!a.db)
+        return;
+    // a lane holds the sums of 8 columns over its rows; the wave's other rows
+    // of the same columns are in the lanes LANES apart
+    constexpr uint32_t LANES = Core::FN * 2;
+    const uint32_t wave = threadIdx.x >> 6, l = threadIdx.x & 63u;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+#pragma unroll
+        for (uint32_t d = LANES; d < 64; d *= 2)
+            sums[e] += __shfl_xor(sums[e], d);
+    __syncthreads();  // every wave is done with its part of LDS
+    float *columns = (float *)lds;  // [WR][BN]
+    if (l < LANES)
+#pragma unroll
+        for (uint32_t e = 0; e < 8; ++e)
+            columns[wave / Core::WC * BN + wave % Core::WC * (Core::FN * 16) + l * 8 + e] =
+                sums[e];
+    __syncthreads();
+    if (threadIdx.x < BN && n0 + threadIdx.x < a.ld) {
+        float s = 0.0f;
+#pragma unroll
+        for (uint32_t w = 0; w < Core::WR; ++w)
+            s += columns[w * BN + threadIdx.x];
+        a.db[ti * a.ld + n0 + threadIdx.x] = s;
+    }
+}
+
+// db of a piece from its row tiles' sums.
+template <class O>
+__global__ __launch_bounds__(256) void db_kernel(const RowsHead *head, const float *sums,
+                                                 uint64_t ld, uint32_t side, uint32_t n, O *db,
+                                                 int add) {
+    const uint32_t c = blockIdx.x * 256 + threadIdx.x;
+    if (c >= n)
+        return;
+    const uint32_t tm = (head->count + side - 1) / side;
+    float v = 0.0f;
+#pragma unroll 8
+    for (uint32_t t = 0; t < tm; ++t)
+        v += sums[t * ld + c];
+    v *= head->inverse;
+    db[c] = (O)(add ? (float)db[c] + v : v);
+}
+
+// ---------------------------------------------------------------------------
+// the products that take dz
+// ---------------------------------------------------------------------------
+
+// C of a product: dx (of the packed rows; sums of the pieces so far are in
+// `sum`) or dw (of the piece's classes).
+struct Out {
+    uint32_t m;       // rows: dw; dx: the rows with a target
+    uint32_t n;       // columns
+    void *c;          // dx: T, by the caller's rows; dw: T or binary32
+    uint64_t ld;
+    float *sum;       // dx: [count][sum_ld] of the pieces before, or null
+    uint64_t sum_ld;
+    const uint32_t *row;  // dx: the caller's
+    int read, write;  // dx: whether sum is read, and written in c's place
+    int f32, add;     // dw
+    int vec;          // c's rows start on 16-byte boundaries, n is a multiple of 8
+};
+
+struct GradArgs {
+    const RowsHead *head;
+    Operand a, b;
+    uint32_t tn, splits;
+    uint64_t tile_rows;  // dx: 0 (they go by the count); dw: tiles of m
+    float *partial;      // splits > 1: [splits][m][part_ld]
+    uint64_t part_ld;    // n rounded up to 8
+    Out o;
+};
+
+struct Old {
+    u32x4 v[2];
+};
+
+template <class E, bool DX, bool VEC>
+__device__ __forceinline__ Old old8(const Out &o, uint32_t m, uint32_t n) {
+    Old f;
+    if (m >= o.m || n >= o.n)
+        return f;
+    if (DX) {
+        if (o.read)
+            load8<true>(o.sum + m * o.sum_ld + n, 8, f.v);
+    } else if (o.add) {
+        const uint32_t have = o.n - n < 8 ? o.n - n : 8;
+        if (o.f32) {
+            load8<VEC>((const float *)o.c + m * o.ld + n, have, f.v);
+        } else {
+            u32x4 t[1];
+            load8<VEC>((const E *)o.c + m * o.ld + n, have, t);
+            f.v[0] = t[0];
+        }
+    }
+    return f;
+}
+
+template <class E, bool DX, bool VEC>
+__device__ __forceinline__ void out8(const Out &o, float inverse, uint32_t m, uint32_t n,
+                                     float (&v)[8], const Old &f) {
+    if (m >= o.m || n >= o.n)
+        return;
+    const uint32_t have = o.n - n < 8 ? o.n - n : 8;
+    float t[8];
+    if (DX) {
+        if (o.read) {
+            widen8<float>(f.v, t);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] += t[i];
+        }
+        if (o.write) {
+            store8<true>(o.sum + m * o.sum_ld + n, 8, v);
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] *= inverse;
+        store8<VEC>((E *)o.c + o.row[m] * o.ld + n, have, v);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] *= inverse;
+    if (o.add) {
+        if (o.f32) {
+            widen8<float>(f.v, t);
+        } else {
+            u32x4 h[1] = {f.v[0]};
+            widen8<E>(h, t);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] += t[i];
+    }
+    if (o.f32)
+        store8<VEC>((float *)o.c + m * o.ld + n, have, v);
+    else
+        store8<VEC>((E *)o.c + m * o.ld + n, have, v);
+}
+
+// DX: C = dz w over the piece's classes.  Otherwise C = dz^T x over the packed
+// rows, PAIR: with dz in two parts, the low ones first.
+template <class T, class Core, bool DX, bool PAIR>
+__global__ __launch_bounds__(Core::THREADS) void grad_kernel(GradArgs g) {
+    using E = typename T::E;
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    const uint32_t count = g.head->count;
+    if (DX) {
+        g.a.rows = g.o.m = count;
+    } else {
+        g.a.k = g.b.k = count;
+    }
+    const uint32_t tm = DX ? (count + Core::BM - 1) / Core::BM : (uint32_t)g.tile_rows;
+    if (blockIdx.x >= tm * g.tn)
+        return;
+    uint32_t ti, tj;
+    tile_of(blockIdx.x, tm, g.tn, ti, tj);
+    g.a.row0 = ti * Core::BM;
+    g.b.row0 = tj * Core::BN;
+    const float inverse = g.head->inverse;
+    const uint32_t s = blockIdx.y;
+    const uint32_t kt = (uint32_t)((g.a.k + Core::BK - 1) / Core::BK);
+    const uint32_t all = PAIR ? 2 * kt : kt;
+    const uint32_t t0 = (uint32_t)((uint64_t)all * s / g.splits);
+    const uint32_t t1 = (uint32_t)((uint64_t)all * (s + 1) / g.splits);
+    f32x4 acc[Core::FM][Core::FN] = {};
+    // of the three passes over pairs, the two that take b's one part
+    if (t0 < t1)
+        Core::run(g.a, g.b, (PAIR ? kt : 0) + t0, (PAIR ? kt : 0) + t1, PAIR ? kt : 0, lds, acc);
+    const uint32_t m0 = g.a.row0, n0 = g.b.row0;
+    if (g.splits > 1) {
+        float *part = g.partial + (uint64_t)s * g.o.m * g.part_ld;
+        Core::each(
+            acc, lds, [](uint32_t, uint32_t) { return 0; },
+            [&](uint32_t mi, uint32_t ni, float (&v)[8], int) {
+                if (m0 + mi < g.o.m && n0 + ni < g.o.n)
+                    store8<true>(part + (m0 + mi) * g.part_ld + n0 + ni, 8, v);
+            });
+    } else if (g.o.vec) {
+        Core::each(
+            acc, lds,
+            [&](uint32_t mi, uint32_t ni) { return old8<E, DX, true>(g.o, m0 + mi, n0 + ni); },
+            [&](uint32_t mi, uint32_t ni, float (&v)[8], const Old &f) {
+                out8<E, DX, true>(g.o, inverse, m0 + mi, n0 + ni, v, f);
+            });
+    } else {
+        Core::template each<false, 1>(
+            acc, lds,
+            [&](uint32_t mi, uint32_t ni) { return old8<E, DX, false>(g.o, m0 + mi, n0 + ni); },
+            [&](uint32_t mi, uint32_t ni, float (&v)[8], const Old &f) {
+                out8<E, DX, false>(g.o, inverse, m0 + mi, n0 + ni, v, f);
+            });
+    }
+}
+
+// The sums of the parts, in their order; 8 columns a lane.
+template <class T, bool DX>
+__global__ __launch_bounds__(256) void grad_join(GradArgs g) {
+    using E = typename T::E;
+    if (DX)
+        g.o.m = g.head->count;
+    const uint32_t groups = (g.o.n + 7) / 8;
+    const uint64_t id = (uint64_t)blockIdx.x * 256 + threadIdx.x;
+    if (id >= (uint64_t)groups * g.o.m)
+        return;
+    const uint32_t m = (uint32_t)(id / groups), n = (uint32_t)(id % groups) * 8;
+    const float inverse = g.head->inverse;
+    const Old f = g.o.vec ? old8<E, DX, true>(g.o, m, n) : old8<E, DX, false>(g.o, m, n);
+    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 4
+    for (uint32_t s = 0; s < g.splits; ++s) {
+        const float *p = g.partial + ((uint64_t)s * g.o.m + m) * g.part_ld + n;
+        const f32x4 x = *(const f32x4 *)p, y = *(const f32x4 *)(p + 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] += x[i];
+            v[4 + i] += y[i];
+        }
+    }
+    if (g.o.vec)
+        out8<E, DX, true>(g.o, inverse, m, n, v, f);
+    else
+        out8<E, DX, false>(g.o, inverse, m, n, v, f);
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+
+// dz's memory: a piece of classes for which it stays within this many bytes
+// (of one part), but at least 256 classes.
+constexpr size_t kPieceBytes = 256u << 20;
+
+size_t piece_columns(size_t m, size_t n) {
+    const size_t fit = std::max<size_t>(kPieceBytes / (2 * m) / 256 * 256, 256);
+    return std::min(fit, (n + 63) / 64 * 64);
+}
+
+struct Buffers {
+    Rows rows;
+    uint16_t *dz[2];
+    float *sum;      // dx's over the pieces: [m][ld]
+    float *db;
+    float *partial;
+};
+
+// The largest of the products' parts, over whole pieces and the last one.
+size_t partial_floats(size_t m, size_t n, size_t k, size_t piece) {
+    const size_t kp = (k + 7) / 8 * 8, last = n - (n - 1) / piece * piece;
+    size_t most = 0;
+    for (const size_t have : {std::min(piece, n), last}) {
+        const Cut x = cut(m, k, have), w = cut(have, k, m);
+        most = std::max(most, x.splits > 1 ? x.splits * m * kp : 0);
+        most = std::max(most, w.splits > 1 ? w.splits * have * kp : 0);
+    }
+    return most;
+}
+
+Buffers carve_grad(Carve &c, size_t m, size_t n, size_t k) {
+    Buffers b;
+    b.rows = carve_rows(c, m, k);
+    const size_t piece = piece_columns(m, n);
+    b.dz[0] = c.take<uint16_t>(m * piece);
+    b.dz[1] = c.take<uint16_t>(m * piece);
+    b.sum = c.take<float>(piece < n ? m * b.rows.ld : 0);
+    b.db = c.take<float>((m + 63) / 64 * piece);
+    b.partial = c.take<float>(partial_floats(m, n, k, piece));
+    return b;
+}
+
+template <class T, bool STAGED>
+int launch_dz(DzArgs &a, int tile, uint64_t m, hipStream_t s) {
+    auto go = [&](auto core) {
+        using Core = decltype(core);
+        a.tn = (a.n + Core::BN - 1) / Core::BN;
+        const int rc = allow_lds(dz_kernel<T, Core>, Core::LDS);
+        return rc ? rc
+                  : launch(dz_kernel<T, Core>,
+                           dim3((uint32_t)((m + Core::BM - 1) / Core::BM) * a.tn),
+                           dim3(Core::THREADS), Core::LDS, s, a);
+    };
+    if (tile == 0)
+        return go(gemm::Core<T, 256, 256, 2, 4, 64, 2, false, false, STAGED>());
+    if (tile == 1)
+        return go(gemm::Core<T, 128, 128, 2, 2, 64, 2, false, false, STAGED>());
+    return go(gemm::Core<T, 64, 64, 2, 2, 64, 3, false, false, STAGED>());
+}
+
+template <class T, bool DX, bool PAIR, bool STAGED>
+int launch_grad(GradArgs &g, const Cut &c, uint64_t m, hipStream_t s) {
+    auto go = [&](auto core) {
+        using Core = decltype(core);
+        constexpr auto kernel = grad_kernel<T, Core, DX, PAIR>;
+        const uint32_t tm = (uint32_t)((m + Core::BM - 1) / Core::BM);
+        g.tn = (g.o.n + Core::BN - 1) / Core::BN;
+        g.tile_rows = tm;
+        g.splits = c.splits;
+        int rc = allow_lds(kernel, Core::LDS);
+        rc = rc ? rc
+                : launch(kernel, dim3(tm * g.tn, g.splits), dim3(Core::THREADS), Core::LDS, s, g);
+        if (rc || g.splits == 1)
+            return rc;
+        const uint64_t lanes = (uint64_t)(g.o.n + 7) / 8 * m;
+        return launch(grad_join<T, DX>, dim3((uint32_t)((lanes + 255) / 256)), dim3(256), 0, s, g);
+    };
+    if (c.tile == 0)
+        return go(gemm::Core<T, 256, 256, 2, 4, 64, 2, !DX, true, STAGED>());
+    if (c.tile == 1)
+        return go(gemm::Core<T, 128, 128, 2, 2, 64, 2, !DX, true, STAGED>());
+    return go(gemm::Core<T, 64, 64, 2, 2, 64, 3, !DX, true, STAGED>());
+}
+
+template <class T>
+int gradient(const ddl_ce_grad_args *c, void *ws, hipStream_t s) {
+    using E = typename T::E;
+    const ddl_ce_args &l = c->layer;
+    const size_t m = l.m, n = l.n, k = l.k;
+    const bool f32 = c->dw_dtype == DDL_F32;
+    Carve carve{(uint8_t *)ws};
+    const Buffers b = carve_grad(carve, m, n, k);
+    RowsArgs r = {};
+    r.m = (uint32_t)m;
+    r.n = n;
+    r.k = k;
+    r.x = l.x;
+    r.ldx = l.ldx;
+    r.target = l.target;
+    r.lse = l.lse;
+    r.dloss = c->dloss;
+    r.scale = (float)c->scale;
+    r.dx = (uint16_t *)c->dx;
+    r.lddx = c->lddx;
+    int rc = pack_rows(r, b.rows, s);
+    const size_t piece = piece_columns(m, n);
+    // straight to LDS where w's rows start on 16 bytes
+    const bool direct = k % 8 == 0 && aligned16(l.w, l.ldw, 2);
+    for (size_t first = 0; first < n && !rc; first += piece) {
+        const size_t have = std::min(piece, n - first);
+        const uint16_t *w = (const uint16_t *)l.w + first * l.ldw;
+        DzArgs d = {};
+        d.rows = b.rows;
+        d.x = operand(b.rows.x, b.rows.ld, m, k);
+        d.w = operand(w, l.ldw, have, k);
+        d.bias = l.bias ? (const uint16_t *)l.bias + first : nullptr;
+        d.n = (uint32_t)have;
+        d.first = (uint32_t)first;
+        d.smooth = (float)(l.smoothing / (double)n);
+        d.wanted = (float)(1.0 - l.smoothing);
+        d.dz[0] = b.dz[0];
+        d.dz[1] = c->dw && f32 ? b.dz[1] : nullptr;
+        d.ld = (have + 63) / 64 * 64;
+        d.db = c->db ? b.db : nullptr;
+        const int tile = cut(m, have, k).tile;
+        rc = direct ? launch_dz<T, false>(d, tile, m, s) : launch_dz<T, true>(d, tile, m, s);
+        if (!rc && c->db) {
+            const dim3 grid((uint32_t)((have + 255) / 256));
+            rc = f32 ? launch(db_kernel<float>, grid, dim3(256), 0, s, b.rows.head, b.db, d.ld,
+                              kTile[tile], d.n, (float *)c->db + first, c->accumulate)
+                     : launch(db_kernel<E>, grid, dim3(256), 0, s, b.rows.head, b.db, d.ld,
+                              kTile[tile], d.n, (E *)c->db + first, c->accumulate);
+        }
+        if (!rc && c->dx && k) {
+            GradArgs g = {};
+            g.head = b.rows.head;
+            g.a = operand(b.dz[0], d.ld, m, have);
+            g.b = operand(w, l.ldw, k, have);
+            g.partial = b.partial;
+            g.part_ld = b.rows.ld;
+            g.o.n = (uint32_t)k;
+            g.o.c = c->dx;
+            g.o.ld = c->lddx;
+            g.o.sum = b.sum;
+            g.o.sum_ld = b.rows.ld;
+            g.o.row = b.rows.row;
+            g.o.read = first > 0;
+            g.o.write = first + have < n;
+            g.o.vec = k % 8 == 0 && aligned16(c->dx, c->lddx, 2);
+            const Cut t = cut(m, k, have);
+            rc = direct ? launch_grad<T, true, false, false>(g, t, m, s)
+                        : launch_grad<T, true, false, true>(g, t, m, s);
+        }
+        if (!rc && c->dw && k) {
+            GradArgs g = {};
+            const size_t esz = f32 ? 4 : 2;
+            g.head = b.rows.head;
+            g.a = operand(b.dz[0], d.ld, d.ld, 0);
+            g.a.plane[1] = b.dz[1];
+            g.b = operand(b.rows.x, b.rows.ld, b.rows.ld, 0);
+            g.partial = b.partial;
+            g.part_ld = b.rows.ld;
+            g.o.m = (uint32_t)have;
+            g.o.n = (uint32_t)k;
+            g.o.c = (uint8_t *)c->dw + first * c->lddw * esz;
+            g.o.ld = c->lddw;
+            g.o.f32 = f32;
+            g.o.add = c->accumulate;
+            g.o.vec = k % 8 == 0 && aligned16(g.o.c, c->lddw, esz);
+            const Cut t = cut(have, k, m);
+            rc = f32 ? launch_grad<T, false, true, false>(g, t, have, s)
+                     : launch_grad<T, false, false, false>(g, t, have, s);
+        }
+    }
+    return rc;
+}
+
+// The gradients of no rows.
+template <class V>
+__global__ __launch_bounds__(256) void clear_kernel(V *p, uint64_t rows, uint64_t cols,
+                                                    uint64_t ld) {
+    for (uint64_t r = blockIdx.x; r < rows; r += gridDim.x)
+        for (uint64_t c = threadIdx.x; c < cols; c += 256)
+            p[r * ld + c] = 0;
+}
+
+template <class V>
+int clear(const ddl_ce_grad_args *a, hipStream_t s) {
+    const size_t n = a->layer.n, k = a->layer.k;
+    const dim3 rows((uint32_t)std::min<size_t>(n, 65536));
+    int rc = DDL_OK;
+    if (a->dw && k)
+        rc = launch(clear_kernel<V>, rows, dim3(256), 0, s, (V *)a->dw, n, k, a->lddw);
+    if (a->db && !rc)
+        rc = launch(clear_kernel<V>, dim3(1), dim3(256), 0, s, (V *)a->db, 1, n, n);
+    return rc;
+}
+
+bool row_ok(const void *p, size_t ld, size_t cols, size_t rows) {
+    return !p || (ld <= kMaxExtent && (ld >= cols || rows <= 1));
+}
+
+}  // namespace
+
+size_t grad_workspace(size_t m, size_t n, size_t k) {
+    if (!m)
+        return 0;
+    Carve c{nullptr};
+    carve_grad(c, m, n, k);
+    return c.used;
+}
+
+static bool sizes_ok(size_t m, size_t n, size_t k) {
+    return m <= kMaxTargets && n >= 1 && n <= kMaxExtent && k <= kMaxExtent;
+}
+
+int check_cross_entropy(const ddl_ce_args *a, int op, const void *ws, size_t bytes) {
+    const size_t m = a->m, n = a->n, k = a->k;
+    if ((a->dtype != DDL_F16 && a->dtype != DDL_BF16) || !sizes_ok(m, n, k)
+        || !(a->smoothing >= 0 && a->smoothing <= 1))
+        return DDL_E_ARG;
+    if (!m)
+        return DDL_OK;
+    if (!a->target || (k && (!a->x || !a->w)))
+        return DDL_E_NULL;
+    if (!row_ok(a->x, a->ldx, k, m) || !row_ok(a->w, a->ldw, k, n))
+        return DDL_E_ARG;
+    if (!element_ok(a->x, 2) || !element_ok(a->w, 2) || !element_ok(a->bias, 2)
+        || !element_ok(a->target, 8) || !element_ok(a->lse, 4))
+        return DDL_E_ALIGN;
+    if (!ws)
+        return DDL_E_NULL;
+    if ((uintptr_t)ws % 16)
+        return DDL_E_ALIGN;
+    const size_t need =
+        op == DDL_CE_FORWARD ? loss_workspace(m, n, k) : grad_workspace(m, n, k);
+    return bytes < need ? DDL_E_SCRATCH : DDL_OK;
+}
+
+}  // namespace ddl
+
+using namespace ddl;
+
+extern "C" {
+
+int ddl_cross_entropy_workspace(int op, size_t m, size_t n, size_t k, size_t *bytes) {
+    if (!bytes)
+        return DDL_E_NULL;
+    if ((op != DDL_CE_FORWARD && op != DDL_CE_GRAD) || !sizes_ok(m, n, k))
+        return DDL_E_ARG;
+    *bytes = !m ? 0 : op == DDL_CE_FORWARD ? loss_workspace(m, n, k) : grad_workspace(m, n, k);
+    return DDL_OK;
+}
+
+int ddl_cross_entropy_grad(const ddl_ce_grad_args *a, void *workspace, size_t workspace_bytes,
+                           void *stream) {
+    if (!a)
+        return DDL_E_NULL;
+    const ddl_ce_args &l = a->layer;
+    int rc = check_cross_entropy(&l, DDL_CE_GRAD, workspace, workspace_bytes);
+    if (rc)
+        return rc;
+    if ((a->dw_dtype != DDL_F32 && a->dw_dtype != l.dtype)
+        || (a->accumulate != 0 && a->accumulate != 1) || !std::isfinite(a->scale)
+        || !row_ok(a->dx, a->lddx, l.k, l.m) || !row_ok(a->dw, a->lddw, l.k, l.n))
+        return DDL_E_ARG;
+    if (l.k && !a->dx && !a->dw && !a->db)
+        return DDL_E_NULL;
+    const size_t esz = a->dw_dtype == DDL_F32 ? 4 : 2;
+    if (!element_ok(a->dx, 2) || !element_ok(a->dw, esz) || !element_ok(a->db, esz)
+        || !element_ok(a->dloss, 4))
+        return DDL_E_ALIGN;
+    if (!l.m)
+        return a->accumulate ? DDL_OK
+               : esz == 4    ? clear<uint32_t>(a, (hipStream_t)stream)
+                             : clear<uint16_t>(a, (hipStream_t)stream);
+    if (!l.lse)
+        return DDL_E_NULL;
+    return l.dtype == DDL_F16 ? gradient<Half>(a, workspace, (hipStream_t)stream)
+                              : gradient<Bfloat>(a, workspace, (hipStream_t)stream);
+}
+
+}  // extern "C"

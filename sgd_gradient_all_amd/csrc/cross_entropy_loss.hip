@@ -1,0 +1,545 @@
+// cross_entropy_loss.hip -- softmax cross entropy of a projection (gfx950):
+//
+//     z = x w^T + bias,   lse_i = log sum_j exp z_ij
+//     loss_i = lse_i - (1 - a) z_i,target(i) - a mean_j z_ij
+//
+// The logits stay in the matrix instruction's registers: every tile of the
+// product leaves, for each of its rows, the largest logit and the sum of the
+// exponentials under it (and the sum of the logits where a > 0), 8 bytes for 256
+// logits, and a second kernel joins a row's tiles.  The product bounds it.
+#include <hip/hip_runtime.h>
+#include <math.h>
+
+#include <algorithm>
+
+#include "cross_entropy_internal.h"
+
+namespace ddl {
+namespace {
+
+using gemm::Bfloat;
+using gemm::f32x4;
+using gemm::Half;
+
+constexpr float kNone = -__builtin_huge_valf();  // the largest of no logits
+
+// exp(v - top), and 0 where all logits so far are -inf
+__device__ __forceinline__ float part_of(float v, float top) {
+    return __builtin_amdgcn_exp2f((v - (top == kNone ? 0.0f : top)) * kLog2e);
+}
+
+// ---------------------------------------------------------------------------
+// rows
+// ---------------------------------------------------------------------------
+
+// The factor of row i's dz.
+__device__ __forceinline__ float factor_of(const RowsArgs &a, uint64_t i) {
+    return a.dloss ? a.dloss[i] * a.scale : a.scale;
+}
+
+// Packs the indices of the rows with a target, in their order: one workgroup,
+// 4096 targets at a time (their counts by wave are then one wave's scan).
+// Gradient: factor is the power of two that takes the largest |dloss scale| to
+// [2^14, 2^15).  dz = factor dloss scale (p - wanted) is held in 16 bits, and
+// |p - wanted| <= 1: so binary16 keeps 11 bits of every p down to 2^-29 of the
+// largest row's, whatever the loss is scaled by.
+__global__ __launch_bounds__(1024) void rows_kernel(RowsArgs a, Rows r) {
+    constexpr uint32_t U = 4, WAVES = 16;
+    __shared__ uint32_t counts[U * WAVES], before[U * WAVES + 1];
+    __shared__ float tops[WAVES];
+    const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
+    uint32_t base = 0;
+    float top = 0.0f;
+    for (uint32_t i0 = 0; i0 < a.m; i0 += U * 1024) {
+        long long t[U];
+        float g[U];
+        uint64_t have[U];
+#pragma unroll
+        for (uint32_t j = 0; j < U; ++j) {
+            const uint32_t i = i0 + j * 1024 + threadIdx.x;
+            t[j] = i < a.m ? a.target[i] : -1;
+            g[j] = i < a.m && a.lse ? factor_of(a, i) : 1.0f;
+        }
+#pragma unroll
+        for (uint32_t j = 0; j < U; ++j) {
+            t[j] = g[j] == 0.0f ? -1 : t[j];
+            have[j] = __ballot(t[j] >= 0);
+            if (lane == 0)
+                counts[j * WAVES + wave] = (uint32_t)__popcll(have[j]);
+        }
+        __syncthreads();
+        if (wave == 0) {
+            uint32_t sum = counts[lane];
+#pragma unroll
+            for (uint32_t d = 1; d < 64; d *= 2) {
+                const uint32_t left = __shfl_up(sum, d);
+                sum += lane >= d ? left : 0;
+            }
+            before[lane + 1] = sum;
+            if (lane == 0)
+                before[0] = 0;
+        }
+        __syncthreads();
+#pragma unroll
+        for (uint32_t j = 0; j < U; ++j) {
+            const uint32_t i = i0 + j * 1024 + threadIdx.x;
+            if (t[j] >= 0) {
+                const uint32_t at = base + before[j * WAVES + wave]
+                                    + (uint32_t)__popcll(have[j] & ((1ull << lane) - 1));
+                const bool bad = (uint64_t)t[j] >= a.n;
+                r.row[at] = i;
+                r.target[at] = bad ? kBadTarget : (int32_t)t[j];
+                if (a.lse) {
+                    r.lse[at] = a.lse[i];
+                    r.g[at] = bad ? __builtin_nanf("") : g[j];
+                    top = fmaxf(top, fabsf(g[j]));
+                }
+            } else if (i < a.m && a.loss) {
+                a.loss[i] = 0.0f;
+                a.lse_out[i] = 0.0f;
+            }
+        }
+        base += before[U * WAVES];
+        __syncthreads();
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2)
+        top = fmaxf(top, __shfl_xor(top, d));
+    if (lane == 0)
+        tops[wave] = top;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (uint32_t w = 1; w < WAVES; ++w)
+            top = fmaxf(top, tops[w]);
+        int e = 0;
+        if (top > 0.0f) {
+            e = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127;  // infinity: 128
+            e = 14 - (e < -86 ? -86 : e > 114 ? 114 : e);
+        }
+        r.head->count = base;
+        r.head->factor = ldexpf(1.0f, e);
+        r.head->inverse = ldexpf(1.0f, -e);
+    }
+}
+
+// Row blockIdx.x of the packed x, zeros up to its ld, and of dx, where the
+// caller's row of that index is not packed.
+template <bool VEC>
+__global__ __launch_bounds__(256) void pack_kernel(RowsArgs a, Rows r) {
+    const uint64_t i = blockIdx.x;
+    if (i < r.head->count) {
+        const uint16_t *from = (const uint16_t *)a.x + (uint64_t)r.row[i] * a.ldx;
+        uint16_t *to = r.x + i * r.ld;
+        for (uint64_t c = threadIdx.x * 8; c < r.ld; c += 256 * 8) {
+            if (VEC) {
+                *(u32x4 *)(to + c) = *(const u32x4 *)(from + c);
+            } else {
+                uint16_t v[8];
+#pragma unroll
+                for (uint32_t e = 0; e < 8; ++e)
+                    v[e] = c + e < a.k ? from[c + e] : (uint16_t)0;
+                __builtin_memcpy(to + c, v, 16);
+            }
+        }
+    }
+    if (a.dx && (a.target[i] < 0 || factor_of(a, i) == 0.0f))
+        for (uint64_t c = threadIdx.x; c < a.k; c += 256)
+            a.dx[i * a.lddx + c] = 0;
+}
+
+}  // namespace
+
+int pack_rows(const RowsArgs &a, const Rows &r, hipStream_t s) {
+    const int rc = launch(rows_kernel, dim3(1), dim3(1024), 0, s, a, r);
+    const bool vec = a.k % 8 == 0 && aligned16(a.x, a.ldx, 2);
+    return rc ? rc
+              : launch(vec ? pack_kernel<true> : pack_kernel<false>, dim3(a.m), dim3(256), 0, s, a,
+                       r);
+}
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// the product
+// ---------------------------------------------------------------------------
+
+struct LossArgs {
+    Rows rows;
+    Operand x, w;
+    const void *bias;       // T or null
+    uint64_t m, n;
+    uint32_t first, tn;     // columns' tiles of this launch
+    float *top, *sum, *all; // [part][m]; all: or null
+};
+
+// A tile's rows: largest logit and sum of exponentials.  A lane holds, of row
+// l % 16 of each of its FM fragments, 4 columns of each of the FN fragments;
+// the row's other columns of the wave are in the lanes 16, 32 and 48 on, and
+// the waves' parts are joined through LDS.
+template <class T, class Core>
+__global__ __launch_bounds__(Core::THREADS) void loss_kernel(LossArgs a) {
+    using E = typename T::E;
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    constexpr uint32_t BM = Core::BM, BN = Core::BN;
+    const uint32_t count = a.rows.head->count, tm = (count + BM - 1) / BM;
+    if (blockIdx.x >= tm * a.tn)
+        return;
+    uint32_t ti, tj;
+    tile_of(blockIdx.x, tm, a.tn, ti, tj);
+    tj += a.first;
+    a.x.row0 = ti * BM;
+    a.x.rows = count;
+    a.w.row0 = tj * BN;
+    f32x4 acc[Core::FM][Core::FN] = {};
+    if (a.x.k)
+        Core::run(a.x, a.w, 0, (uint32_t)((a.x.k + Core::BK - 1) / Core::BK), 0, lds, acc);
+    const uint32_t wave = threadIdx.x >> 6, l = threadIdx.x & 63u;
+    const uint32_t m0 = (wave / Core::WC) * (Core::FM * 16) + (l & 15u);
+    const uint32_t n0 = (wave % Core::WC) * (Core::FN * 16) + (l >> 4) * 4;
+    const uint64_t col = (uint64_t)tj * BN + n0;
+    float bias[Core::FN][4];
+#pragma unroll
+    for (int j = 0; j < Core::FN; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint64_t c = col + j * 16 + e;
+            bias[j][e] = a.bias && c < a.n ? (float)((const E *)a.bias)[c] : 0.0f;
+        }
+    const bool whole = (uint64_t)(tj + 1) * BN <= a.n;
+    gemm::wait_and_meet<0>();  // every wave is done with the tiles
+    float *tops = (float *)lds, *sums = tops + Core::WC * BM, *alls = sums + Core::WC * BM;
+    static_assert(3 * Core::WC * BM * 4 <= Core::LDS, "the rows' part of LDS");
+#pragma unroll
+    for (int i = 0; i < Core::FM; ++i) {
+        const uint32_t row = ti * BM + m0 + i * 16;
+        const uint32_t want =
+            row < count ? (uint32_t)a.rows.target[row] - (uint32_t)col : ~0u;
+        float top = kNone, all = 0.0f;
+#pragma unroll
+        for (int j = 0; j < Core::FN; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float v = acc[i][j][e] + bias[j][e];
+                if (want == (uint32_t)(j * 16 + e) && col + j * 16 + e < a.n)
+                    a.rows.at[row] = v;
+                if (!whole && col + j * 16 + e >= a.n)
+                    v = kNone;
+                else
+                    all += v;
+                acc[i][j][e] = v;
+                top = fmaxf(top, v);
+            }
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < Core::FN; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                sum += part_of(acc[i][j][e], top);
+        sum += __shfl_xor(sum, 16);
+        sum += __shfl_xor(sum, 32);
+        all += __shfl_xor(all, 16);
+        all += __shfl_xor(all, 32);
+        if (l < 16) {
+            const uint32_t at = (wave % Core::WC) * BM + m0 + i * 16;
+            tops[at] = top;
+            sums[at] = sum;
+            alls[at] = all;
+        }
+    }
+    __syncthreads();
+    const uint32_t row = ti * BM + threadIdx.x;
+    if (threadIdx.x >= BM || row >= count)
+        return;
+    float top = kNone, sum = 0.0f, all = 0.0f;
+#pragma unroll
+    for (uint32_t w = 0; w < Core::WC; ++w)
+        top = fmaxf(top, tops[w * BM + threadIdx.x]);
+#pragma unroll
+    for (uint32_t w = 0; w < Core::WC; ++w) {
+        sum += sums[w * BM + threadIdx.x] * part_of(tops[w * BM + threadIdx.x], top);
+        all += alls[w * BM + threadIdx.x];
+    }
+    const uint64_t at = (uint64_t)tj * a.m + row;
+    a.top[at] = top;
+    a.sum[at] = sum;
+    if (a.all)
+        a.all[at] = all;
+}
+
+// Up to 16 rows: the weights are read once and bound the time.  A workgroup
+// takes a run of groups of 16 columns; for each, its 8 waves take an eighth of
+// k, straight into the matrix instruction's registers, and 256 lanes add the
+// parts up and keep the rows' largest logit and sum as they go.
+constexpr int kFewWaves = 8;
+constexpr uint64_t kFewRows = 16;
+
+template <class T>
+__global__ __launch_bounds__(kFewWaves * 64) void few_kernel(LossArgs a, uint32_t groups) {
+    using E = typename T::E;
+    __shared__ f32x4 parts[2][kFewWaves][16][5];  // [wave][m][n / 4], a chunk of padding
+    const uint32_t count = a.rows.head->count;
+    const uint32_t l = threadIdx.x & 63u, wave = threadIdx.x >> 6, r = l & 15u, g = l >> 4;
+    if (!count)
+        return;
+    const uint32_t g0 = (uint32_t)((uint64_t)groups * blockIdx.x / gridDim.x);
+    const uint32_t g1 = (uint32_t)((uint64_t)groups * (blockIdx.x + 1) / gridDim.x);
+    const uint32_t steps = (uint32_t)((a.x.k + 31) / 32);
+    const uint32_t s0 = steps * wave / kFewWaves, s1 = steps * (wave + 1) / kFewWaves;
+    const uint32_t rx = r < count ? r : count - 1;
+    const uint16_t *px = a.x.plane[0] + (uint64_t)rx * a.x.ld + g * 8;
+    // the lane's row and column where parts are added up
+    const uint32_t m = threadIdx.x >> 4, c = threadIdx.x & 15u;
+    const bool mine = threadIdx.x < 256 && m < count;
+    const uint32_t want = mine ? (uint32_t)a.rows.target[m] : ~0u;
+    float top = kNone, sum = 0.0f, all = 0.0f;
+    for (uint32_t q = g0; q < g1; ++q) {
+        const uint64_t n0 = (uint64_t)q * 16;
+        const uint64_t rw = n0 + r < a.n ? n0 + r : a.n - 1;
+        const uint16_t *pw = a.w.plane[0] + rw * a.w.ld + g * 8;
+        f32x4 acc = {0, 0, 0, 0};
+        constexpr uint32_t U = 8;
+        uint32_t s = s0;
+        for (; s + U <= s1 && (uint64_t)(s + U) * 32 <= a.x.k; s += U) {
+            gemm::s16x8 x[U], w[U];
+#pragma unroll
+            for (uint32_t i = 0; i < U; ++i) {
+                w[i] = *(const gemm::s16x8 *)(pw + (uint64_t)(s + i) * 32);
+                x[i] = *(const gemm::s16x8 *)(px + (uint64_t)(s + i) * 32);
+            }
+#pragma unroll
+            for (uint32_t i = 0; i < U; ++i)
+                acc = T::mfma(w[i], x[i], acc);
+        }
+        for (; s < s1; ++s) {
+            gemm::s16x8 x = {}, w = {};
+            if ((uint64_t)s * 32 + g * 8 < a.x.k) {  // k is a multiple of 8
+                w = *(const gemm::s16x8 *)(pw + (uint64_t)s * 32);
+                x = *(const gemm::s16x8 *)(px + (uint64_t)s * 32);
+            }
+            acc = T::mfma(w, x, acc);
+        }
+        // two buffers: a wave that is a group ahead does not overwrite what
+        // the last one's sums are read from
+        parts[q & 1][wave][r][g] = acc;
+        __syncthreads();
+        if (mine) {
+            float v = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kFewWaves; ++w)
+                v += parts[q & 1][w][m][c / 4][c % 4];
+            if (n0 + c < a.n) {
+                if (a.bias)
+                    v += (float)((const E *)a.bias)[n0 + c];
+                if (want == (uint32_t)(n0 + c))
+                    a.rows.at[m] = v;
+                all += v;
+                // each lane its own columns; -inf and NaN as elsewhere
+                const float old = top;
+                top = fmaxf(top, v);
+                sum = sum * part_of(old, top) + part_of(v, top);
+            }
+        }
+    }
+    if (!mine)
+        return;
+    const float own = top;
+#pragma unroll
+    for (int d = 1; d < 16; d *= 2)
+        top = fmaxf(top, __shfl_xor(top, d));
+    sum *= part_of(own, top);
+#pragma unroll
+    for (int d = 1; d < 16; d *= 2) {
+        sum += __shfl_xor(sum, d);
+        all += __shfl_xor(all, d);
+    }
+    if (c == 0) {
+        const uint64_t at = (uint64_t)blockIdx.x * a.m + m;
+        a.top[at] = top;
+        a.sum[at] = sum;
+        if (a.all)
+            a.all[at] = all;
+    }
+}
+
+// A row's parts, joined: R rows by 256 / R lanes a workgroup.
+template <int R>
+__global__ __launch_bounds__(256) void join_kernel(LossArgs a, uint32_t parts, float smoothing,
+                                                   float *loss, float *lse) {
+    constexpr uint32_t LANES = 256 / R;
+    __shared__ float tops[256], sums[256], alls[256];
+    const uint32_t lane = threadIdx.x / R, in = threadIdx.x % R;
+    const uint64_t row = (uint64_t)blockIdx.x * R + in;
+    const uint32_t count = a.rows.head->count;
+    if ((uint64_t)blockIdx.x * R >= count)
+        return;
+    float top = kNone, sum = 0.0f, all = 0.0f;
+    if (row < count) {
+#pragma unroll 8
+        for (uint32_t p = lane; p < parts; p += LANES) {
+            const uint64_t at = (uint64_t)p * a.m + row;
+            const float t = a.top[at], s = a.sum[at], old = top;
+            top = fmaxf(top, t);
+            sum = sum * part_of(old, top) + s * part_of(t, top);
+            if (a.all)
+                all += a.all[at];
+        }
+    }
+    tops[threadIdx.x] = top;
+    sums[threadIdx.x] = sum;
+    alls[threadIdx.x] = all;
+    for (uint32_t half = LANES / 2; half; half /= 2) {
+        __syncthreads();
+        if (lane < half) {
+            const uint32_t o = threadIdx.x + half * R;
+            const float t = tops[o], old = top;
+            top = fmaxf(top, t);
+            sum = sum * part_of(old, top) + sums[o] * part_of(t, top);
+            all += alls[o];
+            tops[threadIdx.x] = top;
+            sums[threadIdx.x] = sum;
+            alls[threadIdx.x] = all;
+        }
+    }
+    if (lane || row >= count)
+        return;
+    const uint32_t to = a.rows.row[row];
+    const float l = top + logf(sum);
+    float v = __builtin_nanf("");
+    if (a.rows.target[row] != kBadTarget) {
+        v = l - (1.0f - smoothing) * a.rows.at[row];
+        if (a.all)
+            v -= smoothing * (all / (float)a.n);
+    }
+    loss[to] = v;
+    lse[to] = l;
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+
+// As many workgroups as run at the same time for few rows.
+constexpr uint32_t kFewGroups = 1024;
+
+bool few(uint64_t m, uint64_t n, uint64_t k) { return m <= kFewRows && n >= 2048 && k >= 256; }
+
+// Tiles as the linear layer cuts them, but never parts of k.
+struct LossCut {
+    int tile;
+    uint32_t tn, parts;
+};
+
+LossCut loss_cut(uint64_t m, uint64_t n, uint64_t k) {
+    LossCut c;
+    c.tile = cut(m, n, k).tile;
+    c.tn = (uint32_t)((n + kTile[c.tile] - 1) / kTile[c.tile]);
+    c.parts = few(m, n, k) ? std::max(c.tn, kFewGroups) : c.tn;
+    return c;
+}
+
+LossArgs carve_loss(Carve &c, size_t m, size_t n, size_t k) {
+    LossArgs a = {};
+    a.rows = carve_rows(c, m, k);
+    const LossCut t = loss_cut(m, n, k);
+    a.top = c.take<float>((size_t)t.parts * m);
+    a.sum = c.take<float>((size_t)t.parts * m);
+    a.all = c.take<float>((size_t)t.parts * m);
+    return a;
+}
+
+template <class T, bool STAGED>
+int launch_loss(LossArgs &a, int tile, uint32_t tn, hipStream_t s) {
+    auto go = [&](auto core) {
+        using Core = decltype(core);
+        const uint64_t tm = (a.m + Core::BM - 1) / Core::BM;
+        int rc = allow_lds(loss_kernel<T, Core>, Core::LDS);
+        // a launch takes fewer than 2^32 lanes
+        const uint32_t most = (uint32_t)((1ull << 31) / Core::THREADS / tm);
+        for (a.first = 0; !rc && a.first < tn; a.first += a.tn) {
+            a.tn = std::min(most, tn - a.first);
+            rc = launch(loss_kernel<T, Core>, dim3((uint32_t)tm * a.tn), dim3(Core::THREADS),
+                        Core::LDS, s, a);
+        }
+        return rc;
+    };
+    if (tile == 0)
+        return go(gemm::Core<T, 256, 256, 2, 4, 64, 2, false, false, STAGED>());
+    if (tile == 1)
+        return go(gemm::Core<T, 128, 128, 2, 2, 64, 2, false, false, STAGED>());
+    return go(gemm::Core<T, 64, 64, 2, 2, 64, 3, false, false, STAGED>());
+}
+
+template <class T>
+int loss(const ddl_ce_args *c, void *ws, hipStream_t s) {
+    Carve carve{(uint8_t *)ws};
+    LossArgs a = carve_loss(carve, c->m, c->n, c->k);
+    RowsArgs r = {};
+    r.m = (uint32_t)c->m;
+    r.n = c->n;
+    r.k = c->k;
+    r.x = c->x;
+    r.ldx = c->ldx;
+    r.target = c->target;
+    r.loss = c->loss;
+    r.lse_out = c->lse;
+    int rc = pack_rows(r, a.rows, s);
+    if (rc)
+        return rc;
+    a.x = operand(a.rows.x, a.rows.ld, c->m, c->k);
+    a.w = operand(c->w, c->ldw, c->n, c->k);
+    a.bias = c->bias;
+    a.m = c->m;
+    a.n = c->n;
+    if (c->smoothing == 0.0)
+        a.all = nullptr;
+    const LossCut t = loss_cut(c->m, c->n, c->k);
+    uint32_t parts = t.tn;
+    // straight to LDS or registers where every row starts on 16 bytes
+    const bool direct = c->k % 8 == 0 && aligned16(c->w, c->ldw, 2);
+    if (direct && few(c->m, c->n, c->k)) {
+        const uint32_t groups = (uint32_t)((c->n + 15) / 16);
+        parts = std::min(kFewGroups, groups);
+        rc = launch(few_kernel<T>, dim3(parts), dim3(kFewWaves * 64), 0, s, a, groups);
+    } else {
+        rc = direct ? launch_loss<T, false>(a, t.tile, t.tn, s)
+                    : launch_loss<T, true>(a, t.tile, t.tn, s);
+    }
+    if (rc)
+        return rc;
+    const float smoothing = (float)c->smoothing;
+    // few rows: a workgroup for each, so that a row's parts are read by many
+    return c->m <= 256
+               ? launch(join_kernel<1>, dim3((uint32_t)c->m), dim3(256), 0, s, a, parts, smoothing,
+                        c->loss, c->lse)
+               : launch(join_kernel<32>, dim3((uint32_t)((c->m + 31) / 32)), dim3(256), 0, s, a,
+                        parts, smoothing, c->loss, c->lse);
+}
+
+}  // namespace
+
+size_t loss_workspace(size_t m, size_t n, size_t k) {
+    Carve c{nullptr};
+    carve_loss(c, m, n, k);
+    return c.used;
+}
+
+}  // namespace ddl
+
+using namespace ddl;
+
+extern "C" int ddl_cross_entropy(const ddl_ce_args *a, void *workspace, size_t workspace_bytes,
+                                 void *stream) {
+    if (!a)
+        return DDL_E_NULL;
+    const int rc = check_cross_entropy(a, DDL_CE_FORWARD, workspace, workspace_bytes);
+    if (rc || !a->m)
+        return rc;
+    if (!a->loss || !a->lse)
+        return DDL_E_NULL;
+    if (!element_ok(a->loss, 4) || !element_ok(a->lse, 4))
+        return DDL_E_ALIGN;
+    return a->dtype == DDL_F16 ? loss<Half>(a, workspace, (hipStream_t)stream)
+                               : loss<Bfloat>(a, workspace, (hipStream_t)stream);
+}
