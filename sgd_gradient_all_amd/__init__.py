@@ -13,6 +13,6 @@ from ._ddl import (  # noqa: F401
     ddl_plan_create, ddl_strerror, get_tuning, lib, set_tuning, topo,
 )
 from ._operators import (  # noqa: F401
-    ACTS, DDL_BF16, AdamW, Muon, cross_entropy, cross_entropy_grad, cross_entropy_workspace,
-    linear, linear_dgrad, linear_wgrad, linear_workspace,
+    ACTS, DDL_BF16, AdamW, AdamW8, Muon, cross_entropy, cross_entropy_grad,
+    cross_entropy_workspace, linear, linear_dgrad, linear_wgrad, linear_workspace,
 )

@@ -15,7 +15,7 @@ SOURCES = [os.path.join(HERE, "csrc", f)
            for f in ("schedule.cpp", "plan.cpp", "step_kernels.hip", "fused_kernel.hip",
                      "lars_kernels.hip", "linear_kernels.hip",
                      "adamw_kernels.hip", "muon_kernels.hip", "optimizer.cpp",
-                     "cross_entropy_loss.hip", "cross_entropy_grad.hip")]
+                     "cross_entropy_loss.hip", "cross_entropy_grad.hip", "adamw8_kernels.hip")]
 
 HIP_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
              "-Wall", "-ffp-contract=off", "-fno-gpu-flush-denormals-to-zero",

@@ -83,6 +83,12 @@ def _lib():
             "ddl_adamw_step": [vp, vp, i32, vp, vp, P(vp), i32, vp, i32, f64, f64, f64, f64, f64,
                                ctypes.c_longlong, vp],
             "ddl_adamw_destroy": [vp],
+            "ddl_adamw8_create": [P(vp), P(sz), P(sz), i32],
+            "ddl_adamw8_blocks": [vp, P(sz)],
+            "ddl_adamw8_step": [vp, vp, i32, vp, vp, vp, vp, P(vp), i32, vp, i32, f64, f64, f64,
+                                f64, f64, ctypes.c_longlong, vp],
+            "ddl_adamw8_values": [vp, vp, vp, vp, vp, vp, vp, vp],
+            "ddl_adamw8_destroy": [vp],
             "ddl_muon_create": [P(vp), P(ddl_muon_matrix), i32],
             "ddl_muon_orthogonalise": [vp, vp, vp, i32, vp],
             "ddl_muon_step": [vp, vp, i32, vp, P(vp), i32, vp, i32, f64, f64, i32, f64, vp],
@@ -384,9 +390,9 @@ class _Optimizer:
             pass
 
 
-class AdamW(_Optimizer):
-    """AdamW over spans [(offset, count)] of flat buffers (ddl_adamw_*)."""
-    _destroy = "ddl_adamw_destroy"
+class _Spans(_Optimizer):
+    """A handle over spans [(offset, count)] of flat buffers."""
+    _create = None
 
     def __init__(self, spans):
         spans = [(int(o), int(c)) for o, c in spans]
@@ -397,8 +403,13 @@ class AdamW(_Optimizer):
         cnts = (ctypes.c_size_t * max(1, n))(*[c for _, c in spans])
         self.need = max([o + c for o, c in spans if c], default=0)
         h = ctypes.c_void_p()
-        _check(_lib().ddl_adamw_create(ctypes.byref(h), offs, cnts, n), "ddl_adamw_create")
+        _check(getattr(_lib(), self._create)(ctypes.byref(h), offs, cnts, n), self._create)
         self.handle = h
+
+
+class AdamW(_Spans):
+    """AdamW over spans [(offset, count)] of flat buffers (ddl_adamw_*)."""
+    _create, _destroy = "ddl_adamw_create", "ddl_adamw_destroy"
 
     def step(self, grad, m, v, weights, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0,
              step=1, copy=None, stream=None):
@@ -413,6 +424,50 @@ class AdamW(_Optimizer):
             step, _ptr(stream))
         if rc:
             _check(rc, "ddl_adamw_step")
+
+
+class AdamW8(_Spans):
+    """AdamW with both states in 8 bits over spans [(offset, count)] of flat
+    buffers (ddl_adamw8_*).  The states are m (int8) and v (uint8), flat like the
+    other buffers, and m_scale and v_scale (float32, `blocks` elements each);
+    zeros before the first step."""
+    _create, _destroy = "ddl_adamw8_create", "ddl_adamw8_destroy"
+
+    def __init__(self, spans):
+        super().__init__(spans)
+        b = ctypes.c_size_t()
+        _check(_lib().ddl_adamw8_blocks(self.handle, ctypes.byref(b)), "ddl_adamw8_blocks")
+        self.blocks = b.value
+
+    def _states(self, m, v, m_scale, v_scale, device):
+        for t, name, dtype in ((m, "m", "torch.int8"), (v, "v", "torch.uint8")):
+            if str(t.dtype) != dtype:
+                raise ValueError(f"{name} has type {t.dtype}: expected {dtype}")
+        return (_flat(m, self.need, "m", None, device), _flat(v, self.need, "v", None, device),
+                _flat(m_scale, self.blocks, "m_scale", _F32, device),
+                _flat(v_scale, self.blocks, "v_scale", _F32, device))
+
+    def step(self, grad, m, v, m_scale, v_scale, weights, lr, beta1=0.9, beta2=0.999, eps=1e-8,
+             weight_decay=0.0, step=1, copy=None, stream=None):
+        """One step on every replica in `weights`; `step` counts from 1; copy: a
+        16-bit buffer that receives the new weights, or None."""
+        n, d = self.need, _device(grad, "grad")
+        rc = _lib().ddl_adamw8_step(
+            self.handle, _flat(grad, n, "grad", None, d), _type(grad, "grad"),
+            *self._states(m, v, m_scale, v_scale, d), _weights(weights, n, d), len(weights),
+            _flat(copy, n, "copy", _F16S, d), _type(copy, "copy") if copy is not None else 0, lr,
+            beta1, beta2, eps, weight_decay, step, _ptr(stream))
+        if rc:
+            _check(rc, "ddl_adamw8_step")
+
+    def values(self, m, v, m_scale, v_scale, m_out, v_out, stream=None):
+        """The states' values into the flat float32 buffers m_out and v_out."""
+        n, d = self.need, _device(m, "m")
+        rc = _lib().ddl_adamw8_values(
+            self.handle, *self._states(m, v, m_scale, v_scale, d),
+            _flat(m_out, n, "m_out", _F32, d), _flat(v_out, n, "v_out", _F32, d), _ptr(stream))
+        if rc:
+            _check(rc, "ddl_adamw8_values")
 
 
 class Muon(_Optimizer):
