@@ -19,13 +19,19 @@
 // everywhere.  A v over 0 keeps at least k = 1: rounded to 0 it would leave eps
 // alone under an m that is not 0.
 //
-// 16 bytes an element with binary16 gradients and copies, against 28 with
-// binary32 states: bound by memory.
+// Bound by memory: 16 bytes an element with binary16 gradients and copies, against
+// 28 with binary32 states.  300M elements with binary32 gradients and bfloat16
+// copies take 950 us (5.7 TB/s of 18 bytes), with binary32 states 1735 us.  A wave
+// takes two blocks, so that one row of exchanges finds both largest values and
+// enough waves fit to hide memory (four blocks, a block's maxima one after the
+// other: 1530 us); elements that binary64 has to decide are done one at a time
+// (both blocks whole: 1190 us).
 #include <hip/hip_runtime.h>
 #include <math.h>
 
 #include <algorithm>
 #include <new>
+#include <type_traits>
 
 #include "../../include/ddl.h"
 #include "optimizer_internal.h"
@@ -34,10 +40,10 @@ namespace ddl {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr uint32_t kBlock = DDL_ADAMW8_BLOCK;  // a wave's: 4 elements a lane
-constexpr uint32_t kEach = 4;                  // blocks of a wave
-constexpr uint32_t kChunk = kBlock * kEach * (kThreads / 64);
-static_assert(kBlock == 256, "4 elements a lane");
+constexpr uint32_t kBlock = DDL_ADAMW8_BLOCK;  // 4 elements of each lane
+constexpr uint32_t kWave = 2 * kBlock;         // two blocks a wave
+constexpr uint32_t kChunk = kWave * (kThreads / 64);
+static_assert(kBlock == 256, "4 elements of each lane");
 
 // A workgroup's part of a span, and the index of its first block.
 struct Part {
@@ -61,195 +67,276 @@ struct Adam8Args {
     double b1, b2, c1, c2;  // c = 1 - b; b1 / 127^2 and b2 / 255^4
     float step, root, eps;  // lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
     float keep;             // 1 - lr decay
-    int vec;
+    int vec, subnormal;     // subnormal: eps does not cover roots of subnormal v
 };
 
-// The largest of a wave's values (bits of numbers without a sign, so that NaN
-// is over all others), NaN if it is not finite.
-__device__ __forceinline__ float wave_max(uint32_t x) {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2)
-        x = max(x, (uint32_t)__shfl_xor((int)x, d));
+// The largest of x over the wave in its lower half's lanes, and that of y in the
+// upper half's: bits of numbers without a sign, so that NaN is over all others;
+// NaN where it is not finite.
+template <int TURN>
+__device__ __forceinline__ uint32_t turn_max(uint32_t x) {
+    return max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x120 + TURN, 0xf, 0xf, false));
+}
+__device__ __forceinline__ float both_max(uint32_t x, uint32_t y) {
+    const auto h = __builtin_amdgcn_permlane32_swap(x, y, false, false);  // halves
+    x = turn_max<1>(turn_max<2>(turn_max<4>(turn_max<8>(max(h[0], h[1])))));  // rows of 16
+    const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);  // the half's two rows
+    x = max(r[0], r[1]);
     return __builtin_bit_cast(float, x >= 0x7f800000u ? 0x7fc00000u : x);
 }
-
-// k of y = 127^2 |m| / s: the nearest to y's root, at most 127.  The root in
-// binary32 is at most one off.
-__device__ __forceinline__ float code_m(double y) {
-    float k = __builtin_rintf(__builtin_amdgcn_sqrtf((float)y));
-    const float hi = k + 0.5f, lo = k - 0.5f;
-    if (y >= (double)(hi * hi))
-        k += 1.0f;
-    else if (k > 0.0f && y < (double)(lo * lo))
-        k -= 1.0f;
-    return fminf(k, 127.0f);
-}
-// k of y = 255^4 v / s, at most 255.
-__device__ __forceinline__ float code_v(double y) {
-    float k = __builtin_rintf(__builtin_amdgcn_sqrtf(__builtin_amdgcn_sqrtf((float)y)));
-    const float h = k + 0.5f, l = k - 0.5f;
-    const double hi = (double)(h * h), lo = (double)(l * l);  // exact
-    if (y >= hi * hi)
-        k += 1.0f;
-    else if (k > 0.0f && y < lo * lo)
-        k -= 1.0f;
-    return fminf(k, 255.0f);
+__device__ __forceinline__ float of_lane(float x, int lane) {
+    return __builtin_bit_cast(
+        float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
 }
 
 constexpr double kM = 127.0 * 127.0, kV = 255.0 * 255.0 * 255.0 * 255.0;
 
-// Elements of a lane: 4 neighbours (VEC), or every 64th of the block.
+// k of y = 127^2 |m| / s: the nearest to y's root, at most 127.  The root in
+// binary32 is at most one off.
+__device__ __forceinline__ float code_m(double y) {
+    const float k = __builtin_rintf(sqrtf((float)y));
+    const float h = k + 0.5f, l = fmaxf(k - 0.5f, 0.0f);
+    return fminf(k + (y >= (double)(h * h) ? 1.0f : 0.0f) - (y < (double)(l * l) ? 1.0f : 0.0f),
+                 127.0f);
+}
+// k of y = 255^4 v / s, at most 255.
+__device__ __forceinline__ float code_v(double y) {
+    const float k = __builtin_rintf(sqrtf(sqrtf((float)y)));
+    const float h = k + 0.5f, l = fmaxf(k - 0.5f, 0.0f);
+    const double hi = (double)(h * h), lo = (double)(l * l);  // exact
+    return fminf(k + (y >= hi * hi ? 1.0f : 0.0f) - (y < lo * lo ? 1.0f : 0.0f), 255.0f);
+}
+
+// The element e of a lane, within its block: 4 neighbours (VEC), or every 64th.
 template <bool VEC>
 __device__ __forceinline__ uint32_t place(uint32_t lane, int e) {
     return VEC ? lane * 4 + e : lane + 64 * e;
 }
 
-template <bool VEC, class X, class F>
-__device__ __forceinline__ void load4(const X *p, uint32_t lane, uint32_t count, F (&out)[4]) {
+// Every byte is read and written once: all accesses are non-temporal (300M
+// elements without the arithmetic: 930 us, otherwise 1020).
+// VEC: a lane's elements are all there or none.
+template <bool VEC, class X>
+__device__ __forceinline__ void load4(const X *p, uint32_t lane, uint32_t count, X (&out)[4]) {
     typedef X X4 __attribute__((ext_vector_type(4)));
-    if (VEC && lane * 4 + 4 <= count) {
-        const X4 v = *(const X4 *)(p + lane * 4);
+    if constexpr (VEC) {
+        X4 v = {};
+        if (lane * 4 < count)
+            v = __builtin_nontemporal_load((const X4 *)(p + lane * 4));
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            out[e] = (F)v[e];
-        return;
-    }
+            out[e] = v[e];
+    } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-        out[e] = place<VEC>(lane, e) < count ? (F)p[place<VEC>(lane, e)] : (F)0;
+        for (int e = 0; e < 4; ++e)
+            out[e] = place<VEC>(lane, e) < count ? p[place<VEC>(lane, e)] : (X)0;
+    }
 }
-template <bool VEC, class X, class F>
-__device__ __forceinline__ void store4(X *p, uint32_t lane, uint32_t count, const F (&in)[4]) {
+template <bool VEC, class X>
+__device__ __forceinline__ void store4(X *p, uint32_t lane, uint32_t count, const X (&in)[4]) {
     typedef X X4 __attribute__((ext_vector_type(4)));
-    if (VEC && lane * 4 + 4 <= count) {
+    if constexpr (VEC) {
         X4 v;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            v[e] = (X)in[e];
-        *(X4 *)(p + lane * 4) = v;
-        return;
-    }
+            v[e] = in[e];
+        if (lane * 4 < count)
+            __builtin_nontemporal_store(v, (X4 *)(p + lane * 4));
+    } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-        if (place<VEC>(lane, e) < count)
-            p[place<VEC>(lane, e)] = (X)in[e];
+        for (int e = 0; e < 4; ++e)
+            if (place<VEC>(lane, e) < count)
+                p[place<VEC>(lane, e)] = in[e];
+    }
 }
 
-// kEach blocks of a wave, from element `at` on, `count` elements; all are
-// loaded before the first is computed.
-template <class G, class C, bool VEC, bool MANY>
-__device__ __forceinline__ void step_blocks(const Adam8Args &a, const Replicas &r, uint64_t at,
-                                            uint32_t count, uint32_t block, uint32_t lane) {
-    float g[kEach][4], w[kEach][4];
-    int km[kEach][4], kv[kEach][4];
-    float sm[kEach], sv[kEach];
+struct Moments {
+    double m, v;
+};
+__device__ __forceinline__ Moments moments(const Adam8Args &a, double dm, double dv, int8_t km,
+                                           uint8_t kv, float g) {
+    const double ge = (double)g;
+    const float k = (float)km, h = (float)kv;
+    const double h2 = (double)(h * h);
+    return {__builtin_fma(dm, (double)(k * fabsf(k)), a.c1 * ge),
+            __builtin_fma(dv, h2 * h2, a.c2 * ge * ge)};
+}
+
+// A wave's two blocks from element `at` on, `count` elements of them.
+template <class G, class C, bool VEC, class R>
+__device__ __forceinline__ void step_wave(const Adam8Args &a, const R &r, uint64_t at,
+                                          uint32_t count, uint32_t block, uint32_t lane) {
+    const uint32_t have[2] = {count, count > kBlock ? count - kBlock : 0};
+    G gh[2][4];
+    float w[2][4];
+    int8_t km[2][4];
+    uint8_t kv[2][4];
+    double dm[2], dv[2];
 #pragma unroll
-    for (uint32_t b = 0; b < kEach; ++b) {
+    for (int b = 0; b < 2; ++b) {
         const uint64_t i = at + b * kBlock;
-        const uint32_t have = count > b * kBlock ? count - b * kBlock : 0;
-        load4<VEC>((const G *)a.grad + i, lane, have, g[b]);
-        load4<VEC>(a.w + i, lane, have, w[b]);
-        load4<VEC>(a.s.m + i, lane, have, km[b]);
-        load4<VEC>(a.s.v + i, lane, have, kv[b]);
-        sm[b] = have ? a.s.m_scale[block + b] : 0.0f;
-        sv[b] = have ? a.s.v_scale[block + b] : 0.0f;
+        load4<VEC>((const G *)a.grad + i, lane, have[b], gh[b]);
+        load4<VEC>((const float *)a.w + i, lane, have[b], w[b]);
+        load4<VEC>((const int8_t *)a.s.m + i, lane, have[b], km[b]);
+        load4<VEC>((const uint8_t *)a.s.v + i, lane, have[b], kv[b]);
+        dm[b] = have[b] ? a.b1 * (double)a.s.m_scale[block + b] : 0.0;
+        dv[b] = have[b] ? a.b2 * (double)a.s.v_scale[block + b] : 0.0;
     }
+    double m[2][4], v[2][4];
+    float root[2][4];
+    uint32_t top_m[2] = {0, 0}, top_v[2] = {0, 0};
 #pragma unroll
-    for (uint32_t b = 0; b < kEach; ++b) {
-        if (count <= b * kBlock)
-            break;
+    for (int b = 0; b < 2; ++b) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const Moments x = moments(a, dm[b], dv[b], km[b][e], kv[b][e], (float)gh[b][e]);
+            m[b][e] = x.m;
+            v[b][e] = x.v;
+            const float mf = (float)x.m, vf = (float)x.v;
+            top_m[b] = max(top_m[b], __builtin_bit_cast(uint32_t, mf) & 0x7fffffffu);
+            top_v[b] = max(top_v[b], __builtin_bit_cast(uint32_t, vf));
+            // the hardware's root, 1 ulp off, takes subnormal numbers for 0
+            root[b][e] = __builtin_amdgcn_sqrtf(vf);
+            float d = root[b][e];
+            if (a.subnormal && vf < 0x1p-96f)
+                d = __builtin_amdgcn_sqrtf(vf * 0x1p64f) * 0x1p-32f;
+            // so is its reciprocal; a root of binary32 and eps are never subnormal
+            w[b][e] = __builtin_fmaf(-a.step,
+                                     mf * __builtin_amdgcn_rcpf(__builtin_fmaf(d, a.root, a.eps)),
+                                     a.keep * w[b][e]);
+        }
         const uint64_t i = at + b * kBlock;
-        const uint32_t have = count - b * kBlock;
-        const double dm = a.b1 * (double)sm[b], dv = a.b2 * (double)sv[b];
-        double m[4], v[4];
-        uint32_t top_m = 0, top_v = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const double ge = (double)g[b][e];
-            const double v2 = (double)(kv[b][e] * kv[b][e]);
-            const int k2 = km[b][e] * km[b][e];
-            m[e] = dm * (double)(km[b][e] < 0 ? -k2 : k2) + a.c1 * ge;
-            v[e] = dv * (v2 * v2) + a.c2 * (ge * ge);
-            const float mf = (float)m[e], vf = (float)v[e];
-            w[b][e] = a.keep * w[b][e] - a.step * (mf / (sqrtf(vf) * a.root + a.eps));
-            top_m = max(top_m, __builtin_bit_cast(uint32_t, mf) & 0x7fffffffu);
-            top_v = max(top_v, __builtin_bit_cast(uint32_t, vf));
-        }
-        const float tm = wave_max(top_m), tv = wave_max(top_v);
-        const double im = tm > 0.0f ? kM / (double)tm : 0.0, iv = tv > 0.0f ? kV / (double)tv : 0.0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int p = (int)code_m(fabs(m[e]) * im), q = (int)code_v(v[e] * iv);
-            km[b][e] = m[e] < 0.0 ? -p : p;
-            kv[b][e] = q == 0 && v[e] * iv > 0.0 ? 1 : q;
-        }
-        store4<VEC>(a.s.m + i, lane, have, km[b]);
-        store4<VEC>(a.s.v + i, lane, have, kv[b]);
-        store4<VEC>(a.w + i, lane, have, w[b]);
-        if (MANY)
+        store4<VEC>(a.w + i, lane, have[b], w[b]);
+        if constexpr (std::is_same<R, Replicas>::value)
             for (int k = 1; k < r.count; ++k)
-                store4<VEC>(r.w[k] + i, lane, have, w[b]);
-        if (a.copy)
-            store4<VEC>((C *)a.copy + i, lane, have, w[b]);
-        if (lane == 0) {
-            a.s.m_scale[block + b] = tm;
-            a.s.v_scale[block + b] = tv;
+                store4<VEC>(r.w[k] + i, lane, have[b], w[b]);
+        if (a.copy) {
+            C c[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                c[e] = (C)w[b][e];
+            store4<VEC>((C *)a.copy + i, lane, have[b], c);
         }
+    }
+    const float tm = both_max(top_m[0], top_m[1]), tv = both_max(top_v[0], top_v[1]);
+    // The codes by binary32 roots: the hardware's, reciprocals and roots of
+    // reciprocals are 1 ulp off, so that 255 times the root is 8.8e-5 off at
+    // most.  Where one is closer to a border than 1e-4 (a block in ten), or scales
+    // are so small or large that shares lose digits, binary64 decides.
+    auto plain = [](float t) { return t == 0.0f || (t >= 0x1p-80f && t <= 0x1p80f); };
+    const float im = tm > 0.0f ? __builtin_amdgcn_rcpf(tm) : 0.0f;
+    const float iv = tv > 0.0f ? __builtin_amdgcn_rsqf(tv) : 0.0f;
+    const bool far = !plain(tm) || !plain(tv);
+    float off = far ? 1.0f : 0.0f;
+    float x[2][4], y[2][4];
+    int8_t cm[2][4];
+    uint8_t cv[2][4];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        const float jm = of_lane(im, b * 32), jv = of_lane(iv, b * 32);
+        const float least = jv > 0.0f ? 1.0f : 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float mf = (float)m[b][e];
+            x[b][e] = 127.0f * __builtin_amdgcn_sqrtf(fabsf(mf) * jm);
+            y[b][e] = 255.0f * __builtin_amdgcn_sqrtf(root[b][e] * jv);
+            const float k = __builtin_rintf(x[b][e]), h = __builtin_rintf(y[b][e]);
+            x[b][e] -= k;
+            y[b][e] -= h;
+            off = fmaxf(off, fmaxf(fabsf(x[b][e]), fabsf(y[b][e])));
+            cm[b][e] = (int8_t)(int)__builtin_copysignf(k, mf);
+            cv[b][e] = (uint8_t)(int)(v[b][e] > 0.0 ? fmaxf(h, least) : h);
+        }
+    }
+    if (__any(!(off < 0.4999f))) {
+        const bool far_any = __any(far);
+        const double em = tm > 0.0f ? kM / (double)tm : 0.0, ev = tv > 0.0f ? kV / (double)tv : 0.0;
+        auto of = [](double x, int lane) {
+            const uint64_t u = __builtin_bit_cast(uint64_t, x);
+            const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, lane);
+            const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), lane);
+            return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+        };
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const double jm = of(em, b * 32), jv = of(ev, b * 32);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (!far_any && fmaxf(fabsf(x[b][e]), fabsf(y[b][e])) < 0.4999f)
+                    continue;
+                const int k = (int)code_m(fabs(m[b][e]) * jm), h = (int)code_v(v[b][e] * jv);
+                cm[b][e] = (int8_t)(m[b][e] < 0.0 ? -k : k);
+                cv[b][e] = (uint8_t)(v[b][e] > 0.0 && jv > 0.0 ? max(h, 1) : h);
+            }
+        }
+    }
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        store4<VEC>(a.s.m + at + b * kBlock, lane, have[b], cm[b]);
+        store4<VEC>(a.s.v + at + b * kBlock, lane, have[b], cv[b]);
+    }
+    if (lane % 32 == 0 && lane / 32 * kBlock < count) {
+        a.s.m_scale[block + lane / 32] = tm;
+        a.s.v_scale[block + lane / 32] = tv;
     }
 }
 
-template <class G, class C, bool MANY>
-__global__ __launch_bounds__(kThreads) void adamw8_kernel(Adam8Args a, Replicas r) {
-    const Part p = a.parts[blockIdx.x];
-    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63u;
-    const uint32_t first = wave * kEach * kBlock;
+// A wave's part of workgroup blockIdx.x's part, to f(VEC, element, elements, block).
+template <class F>
+__device__ __forceinline__ void with_wave(const Part *parts, int vec, F &&f) {
+    const Part p = parts[blockIdx.x];
+    const uint32_t first = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * kWave;
     if (first >= p.count)
         return;
-    const uint64_t at = p.at + first;
-    const uint32_t count = p.count - first, block = p.block + wave * kEach;
-    if (a.vec && p.at % 4 == 0)
-        step_blocks<G, C, true, MANY>(a, r, at, count, block, lane);
+    const uint32_t count = p.count - first, block = p.block + first / kBlock;
+    if (vec && p.at % 4 == 0 && (count % 4 == 0 || count >= kWave))
+        f(std::true_type(), p.at + first, count, block);
     else
-        step_blocks<G, C, false, MANY>(a, r, at, count, block, lane);
+        f(std::false_type(), p.at + first, count, block);
+}
+
+// R: Replicas; or int for one, whose launch then carries 1 KB of arguments less.
+template <class G, class C, class R>
+__global__ __launch_bounds__(kThreads) void adamw8_kernel(Adam8Args a, R r) {
+    with_wave(a.parts, a.vec, [&](auto vec, uint64_t at, uint32_t count, uint32_t block) {
+        step_wave<G, C, decltype(vec)::value>(a, r, at, count, block, threadIdx.x & 63u);
+    });
 }
 
 template <bool VEC>
-__device__ __forceinline__ void values_blocks(const States &s, float *m, float *v, uint64_t at,
-                                              uint32_t count, uint32_t block, uint32_t lane) {
+__device__ __forceinline__ void values_wave(const States &s, float *m, float *v, uint64_t at,
+                                            uint32_t count, uint32_t block, uint32_t lane) {
+    const uint32_t have[2] = {count, count > kBlock ? count - kBlock : 0};
+    int8_t km[2][4];
+    uint8_t kv[2][4];
+    double dm[2], dv[2];
 #pragma unroll
-    for (uint32_t b = 0; b < kEach; ++b) {
-        if (count <= b * kBlock)
-            break;
-        const uint64_t i = at + b * kBlock;
-        const uint32_t have = count - b * kBlock;
-        int km[4], kv[4];
-        load4<VEC>(s.m + i, lane, have, km);
-        load4<VEC>(s.v + i, lane, have, kv);
-        const double dm = (double)s.m_scale[block + b] / kM, dv = (double)s.v_scale[block + b] / kV;
+    for (int b = 0; b < 2; ++b) {
+        load4<VEC>((const int8_t *)s.m + at + b * kBlock, lane, have[b], km[b]);
+        load4<VEC>((const uint8_t *)s.v + at + b * kBlock, lane, have[b], kv[b]);
+        dm[b] = have[b] ? (double)s.m_scale[block + b] * (1 / kM) : 0.0;
+        dv[b] = have[b] ? (double)s.v_scale[block + b] * (1 / kV) : 0.0;
+    }
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
         float x[4], y[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const double v2 = (double)(kv[e] * kv[e]);
-            const int k2 = km[e] * km[e];
-            x[e] = (float)(dm * (double)(km[e] < 0 ? -k2 : k2));
-            y[e] = (float)(dv * (v2 * v2));
+            const float k = (float)km[b][e], h = (float)kv[b][e];
+            const double h2 = (double)(h * h);
+            x[e] = (float)(dm[b] * (double)(k * fabsf(k)));
+            y[e] = (float)(dv[b] * (h2 * h2));
         }
-        store4<VEC>(m + i, lane, have, x);
-        store4<VEC>(v + i, lane, have, y);
+        store4<VEC>(m + at + b * kBlock, lane, have[b], x);
+        store4<VEC>(v + at + b * kBlock, lane, have[b], y);
     }
 }
 
 __global__ __launch_bounds__(kThreads) void values8_kernel(const Part *parts, States s, float *m,
                                                            float *v, int vec) {
-    const Part p = parts[blockIdx.x];
-    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63u;
-    const uint32_t first = wave * kEach * kBlock;
-    if (first >= p.count)
-        return;
-    if (vec && p.at % 4 == 0)
-        values_blocks<true>(s, m, v, p.at + first, p.count - first, p.block + wave * kEach, lane);
-    else
-        values_blocks<false>(s, m, v, p.at + first, p.count - first, p.block + wave * kEach, lane);
+    with_wave(parts, vec, [&](auto vec_, uint64_t at, uint32_t count, uint32_t block) {
+        values_wave<decltype(vec_)::value>(s, m, v, at, count, block, threadIdx.x & 63u);
+    });
 }
 
 }  // namespace
@@ -366,20 +453,23 @@ int ddl_adamw8_step(ddl_adamw8 h, const void *grad, int grad_dtype, signed char 
     a.root = (float)(1 / std::sqrt(1 - std::pow(beta2, (double)step)));
     a.eps = (float)eps;
     a.keep = (float)(1 - lr * weight_decay);
-    uintptr_t all = (uintptr_t)grad | (uintptr_t)copy;
+    // under it, roots of subnormal v are below a rounding of eps
+    a.subnormal = eps < 1e-11;
+    uintptr_t all = (uintptr_t)grad | (uintptr_t)copy | (uintptr_t)m | (uintptr_t)v;
     for (int i = 0; i < r.count; ++i)
         all |= (uintptr_t)r.w[i];
-    a.vec = all % 16 == 0 && ((uintptr_t)m | (uintptr_t)v) % 4 == 0;
+    a.vec = all % 16 == 0;
     const dim3 grid((uint32_t)h->parts.size()), block(kThreads);
     hipStream_t s = (hipStream_t)stream;
     auto go = [&](auto g) {
         using G = decltype(g);
         const bool half = !copy || copy_dtype == DDL_F16;
-        return launch(r.count > 1 ? half ? adamw8_kernel<G, _Float16, true>
-                                         : adamw8_kernel<G, __bf16, true>
-                      : half      ? adamw8_kernel<G, _Float16, false>
-                                  : adamw8_kernel<G, __bf16, false>,
-                      grid, block, 0, s, a, r);
+        if (r.count > 1)
+            return launch(half ? adamw8_kernel<G, _Float16, Replicas>
+                               : adamw8_kernel<G, __bf16, Replicas>,
+                          grid, block, 0, s, a, r);
+        return launch(half ? adamw8_kernel<G, _Float16, int> : adamw8_kernel<G, __bf16, int>, grid,
+                      block, 0, s, a, 0);
     };
     return grad_dtype == DDL_F32   ? go(float())
            : grad_dtype == DDL_F16 ? go(_Float16())
@@ -404,8 +494,8 @@ int ddl_adamw8_values(ddl_adamw8 h, const signed char *m, const unsigned char *v
     const int rc = h->bind((hipStream_t)stream);
     if (rc)
         return rc;
-    const int vec = ((uintptr_t)m_out | (uintptr_t)v_out) % 16 == 0
-                    && ((uintptr_t)m | (uintptr_t)v) % 4 == 0;
+    const int vec =
+        ((uintptr_t)m_out | (uintptr_t)v_out | (uintptr_t)m | (uintptr_t)v) % 16 == 0;
     const States st = {(int8_t *)m, (uint8_t *)v, (float *)m_scale, (float *)v_scale};
     return launch(values8_kernel, dim3((uint32_t)h->parts.size()), dim3(kThreads), 0,
                   (hipStream_t)stream, h->d_parts, st, m_out, v_out, vec);
