@@ -40,8 +40,8 @@ struct DzArgs {
     uint32_t tn, n;         // the piece's tiles and columns
     uint32_t first;         // its first class
     float smooth, wanted;   // a / n, 1 - a
-    uint16_t *dz[2];        // [count][ld]; the low parts: or null
-    uint64_t ld;            // n rounded up to 64; columns past n are 0
+    uint16_t *dz[2];        // [up64(count)][ld]; the low parts: or null
+    uint64_t ld;            // n rounded up to 64; rows past count and columns past n are 0
     float *db;              // [row tile][ld]: column sums, or null
 };
 
@@ -68,7 +68,7 @@ __global__ __launch_bounds__(Core::THREADS) void dz_kernel(DzArgs a) {
     f32x4 acc[Core::FM][Core::FN] = {};
     if (a.x.k)
         Core::run(a.x, a.w, 0, (uint32_t)((a.x.k + Core::BK - 1) / Core::BK), 0, lds, acc);
-    const uint32_t m0 = ti * BM, n0 = tj * BN;
+    const uint32_t m0 = ti * BM, n0 = tj * BN, rows = (uint32_t)up64(count);
     float sums[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     Core::template each<false, 1>(
         acc, lds,
@@ -86,7 +86,7 @@ __global__ __launch_bounds__(Core::THREADS) void dz_kernel(DzArgs a) {
         },
         [&](uint32_t mi, uint32_t ni, float (&v)[8], const RowOf &f) {
             const uint32_t m = m0 + mi, n = n0 + ni;
-            if (m >= count || n >= a.ld)
+            if (m >= rows || n >= a.ld)
                 return;
             if (a.bias) {
                 float b[8];
@@ -102,7 +102,7 @@ __global__ __launch_bounds__(Core::THREADS) void dz_kernel(DzArgs a) {
                 float p = __builtin_amdgcn_exp2f((v[e] - f.lse) * kLog2e) - a.smooth;
                 if (n + e == f.want)
                     p -= a.wanted;
-                p = n + e < a.n ? p * g : 0.0f;
+                p = n + e < a.n && m < count ? p * g : 0.0f;
                 sums[e] += p;
                 v[e] = p;
                 low[e] = p - (float)(E)p;
@@ -264,7 +264,7 @@ __global__ __launch_bounds__(Core::THREADS) void grad_kernel(GradArgs g) {
     if (DX) {
         g.a.rows = g.o.m = count;
     } else {
-        g.a.k = g.b.k = count;
+        g.a.k = g.b.k = up64(count);
     }
     const uint32_t tm = DX ? (count + Core::BM - 1) / Core::BM : (uint32_t)g.tile_rows;
     if (blockIdx.x >= tm * g.tn)
@@ -376,8 +376,8 @@ Buffers carve_grad(Carve &c, size_t m, size_t n, size_t k) {
     Buffers b;
     b.rows = carve_rows(c, m, k);
     const size_t piece = piece_columns(m, n);
-    b.dz[0] = c.take<uint16_t>(m * piece);
-    b.dz[1] = c.take<uint16_t>(m * piece);
+    b.dz[0] = c.take<uint16_t>(up64(m) * piece);
+    b.dz[1] = c.take<uint16_t>(up64(m) * piece);
     b.sum = c.take<float>(piece < n ? m * b.rows.ld : 0);
     b.db = c.take<float>((m + 63) / 64 * piece);
     b.partial = c.take<float>(partial_floats(m, n, k, piece));
@@ -396,7 +396,7 @@ int launch_dz(DzArgs &a, int tile, uint64_t m, hipStream_t s) {
                            dim3(Core::THREADS), Core::LDS, s, a);
     };
     if (tile == 0)
-        return go(gemm::Core<T, 256, 256, 2, 4, 64, 2, false, false, STAGED>());
+        return go(gemm::Core<T, 256, 256, 2, 4, 64, 2, false, false, STAGED, !STAGED>());
     if (tile == 1)
         return go(gemm::Core<T, 128, 128, 2, 2, 64, 2, false, false, STAGED>());
     return go(gemm::Core<T, 64, 64, 2, 2, 64, 3, false, false, STAGED>());
@@ -420,7 +420,7 @@ int launch_grad(GradArgs &g, const Cut &c, uint64_t m, hipStream_t s) {
         return launch(grad_join<T, DX>, dim3((uint32_t)((lanes + 255) / 256)), dim3(256), 0, s, g);
     };
     if (c.tile == 0)
-        return go(gemm::Core<T, 256, 256, 2, 4, 64, 2, !DX, true, STAGED>());
+        return go(gemm::Core<T, 256, 256, 2, 4, 64, 2, !DX, true, STAGED, !STAGED>());
     if (c.tile == 1)
         return go(gemm::Core<T, 128, 128, 2, 2, 64, 2, !DX, true, STAGED>());
     return go(gemm::Core<T, 64, 64, 2, 2, 64, 3, !DX, true, STAGED>());

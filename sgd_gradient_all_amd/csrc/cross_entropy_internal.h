@@ -37,10 +37,12 @@ struct Rows {
     float *lse;       // gradient: the caller's
     float *g;         // gradient: the factor of the row's dz
     float *at;        // loss: the target's logit
-    uint16_t *x;      // [m][ld], zeros behind the k-th element
+    uint16_t *x;      // [up64(count)][ld], zeros behind the k-th element and the last row
     uint64_t ld;      // k rounded up to 8
 };
 
+// Sums over the packed rows run over whole k tiles: rows of zeros fill the last.
+__host__ __device__ inline uint64_t up64(uint64_t n) { return (n + 63) / 64 * 64; }
 inline size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 // Parts of one workspace, one after another on 256-byte boundaries.
@@ -64,7 +66,7 @@ inline Rows carve_rows(Carve &c, size_t m, size_t k) {
     r.g = c.take<float>(m);
     r.at = c.take<float>(m);
     r.ld = (k + 7) / 8 * 8;
-    r.x = c.take<uint16_t>(m * r.ld);
+    r.x = c.take<uint16_t>(up64(m) * r.ld);
     return r;
 }
 

@@ -126,8 +126,11 @@ __global__ __launch_bounds__(1024) void rows_kernel(RowsArgs a, Rows r) {
 // caller's row of that index is not packed.
 template <bool VEC>
 __global__ __launch_bounds__(256) void pack_kernel(RowsArgs a, Rows r) {
-    const uint64_t i = blockIdx.x;
-    if (i < r.head->count) {
+    const uint64_t i = blockIdx.x, count = r.head->count;
+    if (i >= count && i < up64(count))
+        for (uint64_t c = threadIdx.x * 8; c < r.ld; c += 256 * 8)
+            *(u32x4 *)(r.x + i * r.ld + c) = u32x4{0, 0, 0, 0};
+    if (i < count) {
         const uint16_t *from = (const uint16_t *)a.x + (uint64_t)r.row[i] * a.ldx;
         uint16_t *to = r.x + i * r.ld;
         for (uint64_t c = threadIdx.x * 8; c < r.ld; c += 256 * 8) {
@@ -142,7 +145,7 @@ __global__ __launch_bounds__(256) void pack_kernel(RowsArgs a, Rows r) {
             }
         }
     }
-    if (a.dx && (a.target[i] < 0 || factor_of(a, i) == 0.0f))
+    if (a.dx && i < a.m && (a.target[i] < 0 || factor_of(a, i) == 0.0f))
         for (uint64_t c = threadIdx.x; c < a.k; c += 256)
             a.dx[i * a.lddx + c] = 0;
 }
@@ -153,8 +156,8 @@ int pack_rows(const RowsArgs &a, const Rows &r, hipStream_t s) {
     const int rc = launch(rows_kernel, dim3(1), dim3(1024), 0, s, a, r);
     const bool vec = a.k % 8 == 0 && aligned16(a.x, a.ldx, 2);
     return rc ? rc
-              : launch(vec ? pack_kernel<true> : pack_kernel<false>, dim3(a.m), dim3(256), 0, s, a,
-                       r);
+              : launch(vec ? pack_kernel<true> : pack_kernel<false>, dim3((uint32_t)up64(a.m)),
+                       dim3(256), 0, s, a, r);
 }
 
 namespace {
@@ -194,7 +197,6 @@ __global__ __launch_bounds__(Core::THREADS) void loss_kernel(LossArgs a) {
     if (a.x.k)
         Core::run(a.x, a.w, 0, (uint32_t)((a.x.k + Core::BK - 1) / Core::BK), 0, lds, acc);
     const uint32_t wave = threadIdx.x >> 6, l = threadIdx.x & 63u;
-    const uint32_t m0 = (wave / Core::WC) * (Core::FM * 16) + (l & 15u);
     const uint32_t n0 = (wave % Core::WC) * (Core::FN * 16) + (l >> 4) * 4;
     const uint64_t col = (uint64_t)tj * BN + n0;
     float bias[Core::FN][4];
@@ -211,7 +213,8 @@ __global__ __launch_bounds__(Core::THREADS) void loss_kernel(LossArgs a) {
     static_assert(3 * Core::WC * BM * 4 <= Core::LDS, "the rows' part of LDS");
 #pragma unroll
     for (int i = 0; i < Core::FM; ++i) {
-        const uint32_t row = ti * BM + m0 + i * 16;
+        const uint32_t in = (wave / Core::WC) * (Core::FM * 16) + i * 16 + (l & 15u);
+        const uint32_t row = ti * BM + in;
         const uint32_t want =
             row < count ? (uint32_t)a.rows.target[row] - (uint32_t)col : ~0u;
         float top = kNone, all = 0.0f;
@@ -242,7 +245,7 @@ __global__ __launch_bounds__(Core::THREADS) void loss_kernel(LossArgs a) {
         all += __shfl_xor(all, 16);
         all += __shfl_xor(all, 32);
         if (l < 16) {
-            const uint32_t at = (wave % Core::WC) * BM + m0 + i * 16;
+            const uint32_t at = (wave % Core::WC) * BM + in;
             tops[at] = top;
             sums[at] = sum;
             alls[at] = all;
@@ -465,7 +468,7 @@ int launch_loss(LossArgs &a, int tile, uint32_t tn, hipStream_t s) {
         return rc;
     };
     if (tile == 0)
-        return go(gemm::Core<T, 256, 256, 2, 4, 64, 2, false, false, STAGED>());
+        return go(gemm::Core<T, 256, 256, 2, 4, 64, 2, false, false, STAGED, !STAGED>());
     if (tile == 1)
         return go(gemm::Core<T, 128, 128, 2, 2, 64, 2, false, false, STAGED>());
     return go(gemm::Core<T, 64, 64, 2, 2, 64, 3, false, false, STAGED>());

@@ -99,8 +99,10 @@ __device__ __forceinline__ uint32_t chunk_key(uint32_t row) {
 // 16 bytes of every lane to LDS at `lds` + 16 lane, without registers between.
 // Written in assembly because the compiler, which cannot tell the two buffers
 // apart, would make every LDS read wait for the copy into the other one; the
-// wait is wait_and_meet, before the barrier that opens the buffer.  The wait
-// state between the write of m0 and its use is the s_nop.
+// wait is wait_and_meet, before the barrier that opens the buffer, and no copy
+// passes one: what lies between two of them may be reordered around the copies,
+// since they go to a buffer that is not read there.  The wait state between the
+// write of m0 and its use is the s_nop.
 // m0 is declared, since the compiler merges its own writes of it; that it is a
 // reserved register, which the compiler warns of, is no harm: nothing of its
 // own lives there.
@@ -110,13 +112,13 @@ __device__ __forceinline__ void load16_to_lds(const uint8_t *base, uint32_t off,
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                  :
                  : "s"(lds), "v"(off), "s"(base)
-                 : "m0", "memory");
+                 : "m0");
 }
 __device__ __forceinline__ void load16_to_lds(const uint8_t *p, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
                  :
                  : "s"(lds), "v"(p)
-                 : "m0", "memory");
+                 : "m0");
 }
 #pragma clang diagnostic pop
 // Waits until at most N of the wave's copies to LDS are in flight and its own
@@ -126,8 +128,10 @@ __device__ __forceinline__ void wait_and_meet() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
+// SPREAD: copies are sent one by one between the products, from further ahead: see
+// run_spread.
 template <class T, int BM_, int BN_, int WR_, int WC_, int BK_, int STAGES, bool TRA, bool TRB,
-          bool STAGED>
+          bool STAGED, bool SPREAD = false>
 struct Core {
     static constexpr int BM = BM_, BN = BN_, WR = WR_, WC = WC_, BK = BK_;
     static constexpr int S = STAGED ? 2 : STAGES;  // tiles in LDS
@@ -136,8 +140,9 @@ struct Core {
     static constexpr int CH = BK / 8;  // 16-byte chunks of a row with k contiguous
     static constexpr int LA = BM * CH / THREADS, LB = BN * CH / THREADS;  // loads a lane
     static constexpr int BYTES_A = BM * BK * 2, BYTES_B = BN * BK * 2;
-    static constexpr int LDS = S * (BYTES_A + BYTES_B);
+    static constexpr int LDS = S * (BYTES_A + BYTES_B) + (SPREAD ? BYTES_B : 0);
     static_assert(LA >= 1 && LB >= 1 && FN >= 2 && BK == 64 && S >= 2, "tile");
+    static_assert(!SPREAD || (!STAGED && S == 2 && LDS <= 163840), "spread");
 
     // One side's loads of a tile: lane offsets from the tile's uniform base.
     template <bool TR, int R, int L>
@@ -190,6 +195,12 @@ struct Core {
                        : ((q % CH) ^ chunk_key<TR, R>(q / CH)) * 8;
                 load16_to_lds(k < left ? b + off[i] : (const uint8_t *)zero_page, lds);
             }
+        }
+        // WHOLE: left >= BK
+        template <bool WHOLE>
+        __device__ __forceinline__ void send(int i, const uint8_t *b, uint64_t left,
+                                             uint32_t lds) const {
+            issue(i, b, WHOLE ? (uint64_t)BK : left, lds);
         }
         __device__ __forceinline__ void fetch(const uint8_t *b, uint64_t left,
                                               u32x4 (&reg)[L]) const {
@@ -263,6 +274,114 @@ struct Core {
         }
     }
 
+    // Two tiles of A and three of B in LDS.  A wave's copies are accepted at the rate
+    // that the memory system serves all of the compute unit's, and a wave that
+    // sends a whole tile of them at once stands still for it: so they go out one
+    // at a time, every other fragment's products.  A's next tile first, which then
+    // has half a tile's time to arrive, then B's next but one, which the wait
+    // leaves in flight.  Fragments of A are read three steps before their products,
+    // B's for the second half of k during the first.  8192 x 16384 x 4096: 1390
+    // TFLOP/s, all of a tile's copies sent before its products 1180; with B by
+    // rows 1360 and 1170, both by rows 1330 and 1120.
+    __device__ __forceinline__ static void run_spread(const Operand &a, const Operand &b,
+                                                      uint32_t t0, uint32_t t1, uint32_t pairs,
+                                                      uint32_t lds0, f32x4 (&acc)[FM][FN]) {
+        Side<TRA, BM, LA> sa;
+        Side<TRB, BN, LB> sb;
+        sa.init(a);
+        sb.init(b);
+        const uint32_t wave = threadIdx.x >> 6;
+        const uint32_t ma = (wave / WC) * (FM * 16), nb = (wave % WC) * (FN * 16);
+        struct Base {
+            const uint8_t *p;
+            uint64_t left;
+        };
+        auto base = [&](bool is_a, uint32_t t) {
+            const uint32_t pass = !pairs || t >= 2 * pairs ? 2 : t < pairs ? 0 : 1;
+            const uint64_t k0 = (uint64_t)(t - pass * pairs) * BK;
+            return Base{is_a ? sa.base(a, pass == 1, k0) : sb.base(b, pass == 0, k0), a.k - k0};
+        };
+        uint32_t a_now = lds0, a_next = lds0 + BYTES_A;
+        uint32_t b_now = lds0 + 2 * BYTES_A, b_next = b_now + BYTES_B, b_third = b_next + BYTES_B;
+        auto send = [&](bool is_a, uint32_t t, uint32_t to) {
+            const Base p = base(is_a, t);
+            if (is_a) {
+#pragma unroll
+                for (int x = 0; x < LA; ++x)
+                    sa.issue(x, p.p, p.left, to);
+            } else {
+#pragma unroll
+                for (int x = 0; x < LB; ++x)
+                    sb.issue(x, p.p, p.left, to);
+            }
+        };
+        send(true, t0, a_now);
+        send(false, t0, b_now);
+        if (t0 + 1 < t1)
+            send(false, t0 + 1, b_next);
+        // PLAIN: both copies are there to send, of whole k tiles
+        auto tile = [&](auto plain, uint32_t t) {
+            constexpr bool PLAIN = decltype(plain)::value;
+            constexpr int STEPS = BK / 32 * FM, AHEAD = 3;
+            static_assert(2 * (LA + LB) <= STEPS && FM > FN, "a copy every other step");
+            const bool more_a = PLAIN || t + 1 < t1, more_b = PLAIN || t + 2 < t1;
+            Base p = {}, q = {};
+            if (more_a)
+                p = base(true, t + 1);
+            if (more_b)
+                q = base(false, t + 2);
+            s16x8 fb[BK / 32][FN], fa[AHEAD + 1];
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                fb[0][j] = fragment<TRB, BN>(b_now, nb, j, 0);
+#pragma unroll
+            for (int d = 0; d < AHEAD; ++d)
+                fa[d] = fragment<TRA, BM>(a_now, ma, d, 0);
+#pragma unroll
+            for (int step = 0; step < STEPS; ++step) {
+                const int kk = step / FM, i = step % FM, ahead = step + AHEAD;
+                if (ahead < STEPS)
+                    fa[ahead % (AHEAD + 1)] =
+                        fragment<TRA, BM>(a_now, ma, ahead % FM, ahead / FM);
+                const int j1 = step - (FM - FN - 1);
+                if (j1 >= 0 && j1 < FN)
+                    fb[1][j1] = fragment<TRB, BN>(b_now, nb, j1, 1);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int j = 0; j < FN; ++j)
+                    acc[i][j] = T::mfma(fb[kk][j], fa[step % (AHEAD + 1)], acc[i][j]);
+                const int x = step / 2;
+                if (step % 2 == 0 && x < LA && more_a)
+                    sa.template send<PLAIN>(x, p.p, p.left, a_next);
+                if (step % 2 == 0 && x >= LA && x < LA + LB && more_b)
+                    sb.template send<PLAIN>(x - LA, q.p, q.left, b_third);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            const uint32_t x = a_now, y = b_now;
+            a_now = a_next;
+            a_next = x;
+            b_now = b_next;
+            b_next = b_third;
+            b_third = y;
+        };
+        // whole tiles first: a check at every copy costs what their order gains
+        const uint32_t whole =
+            a.k % BK == 0 ? t1 : pairs ? t0 : (uint32_t)(a.k / BK) < t1 ? (uint32_t)(a.k / BK) : t1;
+        uint32_t t = t0;
+        for (; t + 2 < whole; ++t) {
+            // tile t has landed, and every wave is done with the one before
+            wait_and_meet<LB>();
+            tile(std::true_type(), t);
+        }
+        for (; t < t1; ++t) {
+            if (t + 1 < t1)
+                wait_and_meet<LB>();
+            else
+                wait_and_meet<0>();
+            tile(std::false_type(), t);
+        }
+    }
+
     // acc += the k tiles [t0, t1), t0 < t1.  Plain operands: pairs = 0.  Pairs
     // of high and low parts: pairs = the tiles of one pass over k; tiles go
     // through high * low, low * high, and high * high last, so that the sums
@@ -312,6 +431,8 @@ struct Core {
                 now = next;
                 next = x;
             }
+        } else if constexpr (SPREAD) {
+            run_spread(a, b, t0, t1, pairs, lds0, acc);
         } else {
             // S - 1 tiles are in flight ahead of the one multiplied, so that a
             // copy has that many tiles' time to arrive
