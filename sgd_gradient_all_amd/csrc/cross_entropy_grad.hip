@@ -343,18 +343,20 @@ __global__ __launch_bounds__(256) void grad_join(GradArgs g) {
 // host
 // ---------------------------------------------------------------------------
 
-// dz's memory: a piece of classes for which it stays within this many bytes
-// (of one part), but at least 256 classes.
-constexpr size_t kPieceBytes = 256u << 20;
+bool packs(uint64_t m, uint64_t k) { return k % 8 && m >= kPackGrad; }
 
-size_t piece_columns(size_t m, size_t n) {
-    const size_t fit = std::max<size_t>(kPieceBytes / (2 * m) / 256 * 256, 256);
-    return std::min(fit, (n + 63) / 64 * 64);
+// Classes of a piece: as many as dz and a packed w have room for, whole tiles, but
+// all of them where they fit.
+size_t piece_columns(size_t m, size_t n, size_t k) {
+    const size_t most = packs(m, k) ? std::max(m, k) : m;
+    const size_t fit = std::max<size_t>(kPieceElements / most / 256, 1) * 256;
+    return std::min<size_t>(fit, up64(n));
 }
 
 struct Buffers {
     Rows rows;
     uint16_t *dz[2];
+    uint16_t *w;
     float *sum;      // dx's over the pieces: [m][ld]
     float *db;
     float *partial;
@@ -365,7 +367,7 @@ size_t partial_floats(size_t m, size_t n, size_t k, size_t piece) {
     const size_t kp = (k + 7) / 8 * 8, last = n - (n - 1) / piece * piece;
     size_t most = 0;
     for (const size_t have : {std::min(piece, n), last}) {
-        const Cut x = cut(m, k, have), w = cut(have, k, m);
+        const Plan x = plan_product(m, k, have, true), w = plan_product(have, k, m, true);
         most = std::max(most, x.splits > 1 ? x.splits * m * kp : 0);
         most = std::max(most, w.splits > 1 ? w.splits * have * kp : 0);
     }
@@ -375,9 +377,10 @@ size_t partial_floats(size_t m, size_t n, size_t k, size_t piece) {
 Buffers carve_grad(Carve &c, size_t m, size_t n, size_t k) {
     Buffers b;
     b.rows = carve_rows(c, m, k);
-    const size_t piece = piece_columns(m, n);
+    const size_t piece = piece_columns(m, n, k);
     b.dz[0] = c.take<uint16_t>(up64(m) * piece);
     b.dz[1] = c.take<uint16_t>(up64(m) * piece);
+    b.w = c.take<uint16_t>(packs(m, k) ? piece * b.rows.ld : 0);
     b.sum = c.take<float>(piece < n ? m * b.rows.ld : 0);
     b.db = c.take<float>((m + 63) / 64 * piece);
     b.partial = c.take<float>(partial_floats(m, n, k, piece));
@@ -385,7 +388,7 @@ Buffers carve_grad(Carve &c, size_t m, size_t n, size_t k) {
 }
 
 template <class T, bool STAGED>
-int launch_dz(DzArgs &a, int tile, uint64_t m, hipStream_t s) {
+int launch_dz(DzArgs &a, const Plan &p, uint64_t m, hipStream_t s) {
     auto go = [&](auto core) {
         using Core = decltype(core);
         a.tn = (a.n + Core::BN - 1) / Core::BN;
@@ -395,15 +398,17 @@ int launch_dz(DzArgs &a, int tile, uint64_t m, hipStream_t s) {
                            dim3((uint32_t)((m + Core::BM - 1) / Core::BM) * a.tn),
                            dim3(Core::THREADS), Core::LDS, s, a);
     };
-    if (tile == 0)
+    if (p.tile == 0)
         return go(gemm::Core<T, 256, 256, 2, 4, 64, 2, false, false, STAGED, !STAGED>());
-    if (tile == 1)
+    if (p.tile == 1)
         return go(gemm::Core<T, 128, 128, 2, 2, 64, 2, false, false, STAGED>());
+    if (p.deep && !STAGED)
+        return go(gemm::Core<T, 64, 64, 2, 2, 64, kDeep, false, false, STAGED>());
     return go(gemm::Core<T, 64, 64, 2, 2, 64, 3, false, false, STAGED>());
 }
 
 template <class T, bool DX, bool PAIR, bool STAGED>
-int launch_grad(GradArgs &g, const Cut &c, uint64_t m, hipStream_t s) {
+int launch_grad(GradArgs &g, const Plan &c, uint64_t m, hipStream_t s) {
     auto go = [&](auto core) {
         using Core = decltype(core);
         constexpr auto kernel = grad_kernel<T, Core, DX, PAIR>;
@@ -423,6 +428,8 @@ int launch_grad(GradArgs &g, const Cut &c, uint64_t m, hipStream_t s) {
         return go(gemm::Core<T, 256, 256, 2, 4, 64, 2, !DX, true, STAGED, !STAGED>());
     if (c.tile == 1)
         return go(gemm::Core<T, 128, 128, 2, 2, 64, 2, !DX, true, STAGED>());
+    if (c.deep && !STAGED)
+        return go(gemm::Core<T, 64, 64, 2, 2, 64, kDeep, !DX, true, STAGED>());
     return go(gemm::Core<T, 64, 64, 2, 2, 64, 3, !DX, true, STAGED>());
 }
 
@@ -447,16 +454,23 @@ int gradient(const ddl_ce_grad_args *c, void *ws, hipStream_t s) {
     r.dx = (uint16_t *)c->dx;
     r.lddx = c->lddx;
     int rc = pack_rows(r, b.rows, s);
-    const size_t piece = piece_columns(m, n);
-    // straight to LDS where w's rows start on 16 bytes
-    const bool direct = k % 8 == 0 && aligned16(l.w, l.ldw, 2);
+    const size_t piece = piece_columns(m, n, k);
+    // straight to LDS where w's rows start on 16 bytes, or a packed piece's do
+    const bool pack = packs(m, k), direct = pack || (k % 8 == 0 && aligned16(l.w, l.ldw, 2));
+    const size_t ldw = pack ? b.rows.ld : l.ldw;
     for (size_t first = 0; first < n && !rc; first += piece) {
         const size_t have = std::min(piece, n - first);
         const uint16_t *w = (const uint16_t *)l.w + first * l.ldw;
+        if (pack) {
+            rc = pack_matrix(w, l.ldw, have, k, b.w, s);
+            if (rc)
+                break;
+            w = b.w;
+        }
         DzArgs d = {};
         d.rows = b.rows;
         d.x = operand(b.rows.x, b.rows.ld, m, k);
-        d.w = operand(w, l.ldw, have, k);
+        d.w = operand(w, ldw, have, k);
         d.bias = l.bias ? (const uint16_t *)l.bias + first : nullptr;
         d.n = (uint32_t)have;
         d.first = (uint32_t)first;
@@ -466,20 +480,21 @@ int gradient(const ddl_ce_grad_args *c, void *ws, hipStream_t s) {
         d.dz[1] = c->dw && f32 ? b.dz[1] : nullptr;
         d.ld = (have + 63) / 64 * 64;
         d.db = c->db ? b.db : nullptr;
-        const int tile = cut(m, have, k).tile;
-        rc = direct ? launch_dz<T, false>(d, tile, m, s) : launch_dz<T, true>(d, tile, m, s);
+        const Plan p = plan_product(m, have, k, false);
+        rc = direct ? launch_dz<T, false>(d, p, m, s) : launch_dz<T, true>(d, p, m, s);
         if (!rc && c->db) {
             const dim3 grid((uint32_t)((have + 255) / 256));
             rc = f32 ? launch(db_kernel<float>, grid, dim3(256), 0, s, b.rows.head, b.db, d.ld,
-                              kTile[tile], d.n, (float *)c->db + first, c->accumulate)
+                              kTile[p.tile], d.n, (float *)c->db + first, c->accumulate)
                      : launch(db_kernel<E>, grid, dim3(256), 0, s, b.rows.head, b.db, d.ld,
-                              kTile[tile], d.n, (E *)c->db + first, c->accumulate);
+                              kTile[p.tile], d.n, (E *)c->db + first, c->accumulate);
         }
         if (!rc && c->dx && k) {
             GradArgs g = {};
             g.head = b.rows.head;
             g.a = operand(b.dz[0], d.ld, m, have);
-            g.b = operand(w, l.ldw, k, have);
+            // a packed w's columns past k are zeros
+            g.b = operand(w, ldw, pack ? ldw : k, have);
             g.partial = b.partial;
             g.part_ld = b.rows.ld;
             g.o.n = (uint32_t)k;
@@ -491,7 +506,7 @@ int gradient(const ddl_ce_grad_args *c, void *ws, hipStream_t s) {
             g.o.read = first > 0;
             g.o.write = first + have < n;
             g.o.vec = k % 8 == 0 && aligned16(c->dx, c->lddx, 2);
-            const Cut t = cut(m, k, have);
+            const Plan t = plan_product(m, k, have, true);
             rc = direct ? launch_grad<T, true, false, false>(g, t, m, s)
                         : launch_grad<T, true, false, true>(g, t, m, s);
         }
@@ -511,7 +526,7 @@ int gradient(const ddl_ce_grad_args *c, void *ws, hipStream_t s) {
             g.o.f32 = f32;
             g.o.add = c->accumulate;
             g.o.vec = k % 8 == 0 && aligned16(g.o.c, c->lddw, esz);
-            const Cut t = cut(have, k, m);
+            const Plan t = plan_product(have, k, m, true);
             rc = f32 ? launch_grad<T, false, true, false>(g, t, have, s)
                      : launch_grad<T, false, false, false>(g, t, have, s);
         }

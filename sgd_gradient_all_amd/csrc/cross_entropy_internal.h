@@ -88,6 +88,49 @@ struct RowsArgs {
 // Packs the rows (cross_entropy_loss.hip).
 int pack_rows(const RowsArgs &a, const Rows &r, hipStream_t s);
 
+// Rows of k elements that do not start on 16 bytes go through registers on their
+// way to LDS; from this many rows of x on, a piece of w is packed first.  A row of
+// w costs 4 k bytes then, each product with it loses its third more.
+constexpr size_t kPackLoss = 768, kPackGrad = 384;
+// Elements of a piece of w, and of dz, that a call holds at a time.
+constexpr size_t kPieceElements = 128u << 20;
+// to: rows of up8(k) elements, zeros behind the k-th.
+int pack_matrix(const void *from, size_t ld, size_t rows, size_t k, uint16_t *to, hipStream_t s);
+
+// How a product is cut, by the time that it should take: rounds of workgroups over
+// the chip, each of k tiles of 64 at what a tile was measured to take (us, with
+// the chip full of its kind: 1.3, 1.0 and 0.65 PFLOP/s), and where k is cut the
+// parts' way through memory.
+constexpr int kDeep = 8;  // tiles in LDS
+struct Plan {
+    int tile;         // 0: 256 x 256, 1: 128 x 128, 2: 64 x 64
+    uint32_t splits;
+    bool deep;        // 64 x 64, one workgroup a compute unit: more tiles ahead
+};
+
+inline Plan plan_product(uint64_t m, uint64_t n, uint64_t k, bool parts) {
+    constexpr double kStep[3] = {1.65, 1.07, 0.62}, kStart[3] = {6, 4, 3};
+    constexpr uint64_t kSlots[3] = {256, 512, 768};
+    const uint64_t kt = std::max<uint64_t>((k + 63) / 64, 1);
+    Plan best = {2, 1, false};
+    double least = 1e300;
+    for (int t = 0; t < 3; ++t)
+        for (const uint64_t p : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64}) {
+            if (p > 1 && (!parts || kt / p < 4))
+                break;
+            const uint64_t groups = tiles(m, n, t) * p, steps = (kt + p - 1) / p;
+            double us = (double)((groups + kSlots[t] - 1) / kSlots[t])
+                        * (kStart[t] + (double)steps * kStep[t]);
+            if (p > 1)
+                us += 5 + (double)(p * m * n) * 8e-6 / 4;
+            if (us < least) {
+                least = us;
+                best = {t, (uint32_t)p, t == 2 && groups <= 256 && steps >= 8};
+            }
+        }
+    return best;
+}
+
 // What both calls refuse (cross_entropy_grad.hip), and their workspaces.
 int check_cross_entropy(const ddl_ce_args *a, int op, const void *ws, size_t bytes);
 size_t loss_workspace(size_t m, size_t n, size_t k);

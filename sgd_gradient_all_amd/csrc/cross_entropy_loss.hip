@@ -122,9 +122,31 @@ __global__ __launch_bounds__(1024) void rows_kernel(RowsArgs a, Rows r) {
     }
 }
 
+// One row of k elements by a workgroup, zeros up to ld.
+__device__ __forceinline__ void copy_row(const uint16_t *from, uint64_t k, uint16_t *to,
+                                         uint64_t ld) {
+    for (uint64_t c = threadIdx.x * 8; c < ld; c += 256 * 8) {
+        u32x4 v;
+        if (c + 8 <= k) {
+            __builtin_memcpy(&v, from + c, 16);
+        } else {
+            uint16_t e[8];
+#pragma unroll
+            for (uint32_t i = 0; i < 8; ++i)
+                e[i] = c + i < k ? from[c + i] : (uint16_t)0;
+            __builtin_memcpy(&v, e, 16);
+        }
+        *(u32x4 *)(to + c) = v;
+    }
+}
+
+__global__ __launch_bounds__(256) void matrix_kernel(const uint16_t *from, uint64_t ld, uint64_t k,
+                                                     uint16_t *to, uint64_t ld_to) {
+    copy_row(from + blockIdx.x * ld, k, to + blockIdx.x * ld_to, ld_to);
+}
+
 // Row blockIdx.x of the packed x, zeros up to its ld, and of dx, where the
 // caller's row of that index is not packed.
-template <bool VEC>
 __global__ __launch_bounds__(256) void pack_kernel(RowsArgs a, Rows r) {
     const uint64_t i = blockIdx.x, count = r.head->count;
     if (i >= count && i < up64(count))
@@ -133,17 +155,7 @@ __global__ __launch_bounds__(256) void pack_kernel(RowsArgs a, Rows r) {
     if (i < count) {
         const uint16_t *from = (const uint16_t *)a.x + (uint64_t)r.row[i] * a.ldx;
         uint16_t *to = r.x + i * r.ld;
-        for (uint64_t c = threadIdx.x * 8; c < r.ld; c += 256 * 8) {
-            if (VEC) {
-                *(u32x4 *)(to + c) = *(const u32x4 *)(from + c);
-            } else {
-                uint16_t v[8];
-#pragma unroll
-                for (uint32_t e = 0; e < 8; ++e)
-                    v[e] = c + e < a.k ? from[c + e] : (uint16_t)0;
-                __builtin_memcpy(to + c, v, 16);
-            }
-        }
+        copy_row(from, a.k, to, r.ld);
     }
     if (a.dx && i < a.m && (a.target[i] < 0 || factor_of(a, i) == 0.0f))
         for (uint64_t c = threadIdx.x; c < a.k; c += 256)
@@ -154,10 +166,12 @@ __global__ __launch_bounds__(256) void pack_kernel(RowsArgs a, Rows r) {
 
 int pack_rows(const RowsArgs &a, const Rows &r, hipStream_t s) {
     const int rc = launch(rows_kernel, dim3(1), dim3(1024), 0, s, a, r);
-    const bool vec = a.k % 8 == 0 && aligned16(a.x, a.ldx, 2);
-    return rc ? rc
-              : launch(vec ? pack_kernel<true> : pack_kernel<false>, dim3((uint32_t)up64(a.m)),
-                       dim3(256), 0, s, a, r);
+    return rc ? rc : launch(pack_kernel, dim3((uint32_t)up64(a.m)), dim3(256), 0, s, a, r);
+}
+
+int pack_matrix(const void *from, size_t ld, size_t rows, size_t k, uint16_t *to, hipStream_t s) {
+    return launch(matrix_kernel, dim3((uint32_t)rows), dim3(256), 0, s, (const uint16_t *)from,
+                  (uint64_t)ld, (uint64_t)k, to, (uint64_t)((k + 7) / 8 * 8));
 }
 
 namespace {
@@ -271,17 +285,19 @@ __global__ __launch_bounds__(Core::THREADS) void loss_kernel(LossArgs a) {
         a.all[at] = all;
 }
 
-// Up to 16 rows: the weights are read once and bound the time.  A workgroup
-// takes a run of groups of 16 columns; for each, its 8 waves take an eighth of
-// k, straight into the matrix instruction's registers, and 256 lanes add the
-// parts up and keep the rows' largest logit and sum as they go.
+// Up to 64 rows: the weights are read once and bound the time, or the few steps of
+// each sum do.  A workgroup takes a run of groups of 16 columns; for each, its 8
+// waves take an eighth of k, straight into the matrix instruction's registers,
+// for R groups of 16 rows; then the lanes add the parts up, a row and column each,
+// and keep the rows' largest logit and sum as they go.
 constexpr int kFewWaves = 8;
-constexpr uint64_t kFewRows = 16;
+constexpr uint64_t kFewRows = 64;
 
-template <class T>
+template <class T, int R>
 __global__ __launch_bounds__(kFewWaves * 64) void few_kernel(LossArgs a, uint32_t groups) {
     using E = typename T::E;
-    __shared__ f32x4 parts[2][kFewWaves][16][5];  // [wave][m][n / 4], a chunk of padding
+    constexpr uint32_t TURNS = R < 4 ? 2 : 1;  // as many as 64 KB of LDS hold
+    __shared__ f32x4 parts[TURNS][kFewWaves][R * 16][5];  // [wave][m][n / 4], a chunk of padding
     const uint32_t count = a.rows.head->count;
     const uint32_t l = threadIdx.x & 63u, wave = threadIdx.x >> 6, r = l & 15u, g = l >> 4;
     if (!count)
@@ -290,79 +306,111 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_kernel(LossArgs a, uint32_
     const uint32_t g1 = (uint32_t)((uint64_t)groups * (blockIdx.x + 1) / gridDim.x);
     const uint32_t steps = (uint32_t)((a.x.k + 31) / 32);
     const uint32_t s0 = steps * wave / kFewWaves, s1 = steps * (wave + 1) / kFewWaves;
-    const uint32_t rx = r < count ? r : count - 1;
-    const uint16_t *px = a.x.plane[0] + (uint64_t)rx * a.x.ld + g * 8;
-    // the lane's row and column where parts are added up
-    const uint32_t m = threadIdx.x >> 4, c = threadIdx.x & 15u;
-    const bool mine = threadIdx.x < 256 && m < count;
-    const uint32_t want = mine ? (uint32_t)a.rows.target[m] : ~0u;
-    float top = kNone, sum = 0.0f, all = 0.0f;
+    const uint16_t *px[R];
+#pragma unroll
+    for (uint32_t i = 0; i < R; ++i) {
+        const uint32_t row = i * 16 + r;
+        px[i] = a.x.plane[0] + (uint64_t)(row < count ? row : count - 1) * a.x.ld + g * 8;
+    }
+    // the lane's rows and column where parts are added up
+    constexpr uint32_t EACH = R < 2 ? 1 : R / 2;  // rows, 32 apart
+    const uint32_t m0 = threadIdx.x >> 4, c = threadIdx.x & 15u;
+    uint32_t want[EACH];
+    float top[EACH], sum[EACH], all[EACH];
+#pragma unroll
+    for (uint32_t i = 0; i < EACH; ++i) {
+        const uint32_t m = m0 + i * 32;
+        want[i] = m < count ? (uint32_t)a.rows.target[m] : ~0u;
+        top[i] = kNone;
+        sum[i] = all[i] = 0.0f;
+    }
     for (uint32_t q = g0; q < g1; ++q) {
         const uint64_t n0 = (uint64_t)q * 16;
         const uint64_t rw = n0 + r < a.n ? n0 + r : a.n - 1;
         const uint16_t *pw = a.w.plane[0] + rw * a.w.ld + g * 8;
-        f32x4 acc = {0, 0, 0, 0};
+        f32x4 acc[R] = {};
         constexpr uint32_t U = 8;
         uint32_t s = s0;
         for (; s + U <= s1 && (uint64_t)(s + U) * 32 <= a.x.k; s += U) {
-            gemm::s16x8 x[U], w[U];
-#pragma unroll
-            for (uint32_t i = 0; i < U; ++i) {
-                w[i] = *(const gemm::s16x8 *)(pw + (uint64_t)(s + i) * 32);
-                x[i] = *(const gemm::s16x8 *)(px + (uint64_t)(s + i) * 32);
-            }
+            gemm::s16x8 w[U];
 #pragma unroll
             for (uint32_t i = 0; i < U; ++i)
-                acc = T::mfma(w[i], x[i], acc);
+                w[i] = __builtin_nontemporal_load(
+                    (const gemm::s16x8 *)(pw + (uint64_t)(s + i) * 32));
+#pragma unroll
+            for (int j = 0; j < R; ++j) {
+                gemm::s16x8 x[U];
+#pragma unroll
+                for (uint32_t i = 0; i < U; ++i)
+                    x[i] = *(const gemm::s16x8 *)(px[j] + (uint64_t)(s + i) * 32);
+#pragma unroll
+                for (uint32_t i = 0; i < U; ++i)
+                    acc[j] = T::mfma(w[i], x[i], acc[j]);
+            }
         }
         for (; s < s1; ++s) {
-            gemm::s16x8 x = {}, w = {};
-            if ((uint64_t)s * 32 + g * 8 < a.x.k) {  // k is a multiple of 8
+            const bool in = (uint64_t)s * 32 + g * 8 < a.x.k;  // k is a multiple of 8
+            gemm::s16x8 w = {};
+            if (in)
                 w = *(const gemm::s16x8 *)(pw + (uint64_t)s * 32);
-                x = *(const gemm::s16x8 *)(px + (uint64_t)s * 32);
+#pragma unroll
+            for (int j = 0; j < R; ++j) {
+                gemm::s16x8 x = {};
+                if (in)
+                    x = *(const gemm::s16x8 *)(px[j] + (uint64_t)s * 32);
+                acc[j] = T::mfma(w, x, acc[j]);
             }
-            acc = T::mfma(w, x, acc);
         }
-        // two buffers: a wave that is a group ahead does not overwrite what
-        // the last one's sums are read from
-        parts[q & 1][wave][r][g] = acc;
+        // a wave that is a group ahead does not overwrite what the last one's
+        // sums are read from
+        if (TURNS == 1)
+            __syncthreads();
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+            parts[q % TURNS][wave][j * 16 + r][g] = acc[j];
         __syncthreads();
-        if (mine) {
+        float b = 0.0f;
+        if (a.bias && n0 + c < a.n)
+            b = (float)((const E *)a.bias)[n0 + c];
+#pragma unroll
+        for (uint32_t i = 0; i < EACH; ++i) {
+            const uint32_t m = m0 + i * 32;
+            if (m >= count || n0 + c >= a.n)
+                continue;
             float v = 0.0f;
 #pragma unroll
             for (int w = 0; w < kFewWaves; ++w)
-                v += parts[q & 1][w][m][c / 4][c % 4];
-            if (n0 + c < a.n) {
-                if (a.bias)
-                    v += (float)((const E *)a.bias)[n0 + c];
-                if (want == (uint32_t)(n0 + c))
-                    a.rows.at[m] = v;
-                all += v;
-                // each lane its own columns; -inf and NaN as elsewhere
-                const float old = top;
-                top = fmaxf(top, v);
-                sum = sum * part_of(old, top) + part_of(v, top);
-            }
+                v += parts[q % TURNS][w][m][c / 4][c % 4];
+            v += b;
+            if (want[i] == (uint32_t)(n0 + c))
+                a.rows.at[m] = v;
+            all[i] += v;
+            // each lane its own columns; -inf and NaN as elsewhere
+            const float old = top[i];
+            top[i] = fmaxf(old, v);
+            sum[i] = sum[i] * part_of(old, top[i]) + part_of(v, top[i]);
         }
     }
-    if (!mine)
-        return;
-    const float own = top;
 #pragma unroll
-    for (int d = 1; d < 16; d *= 2)
-        top = fmaxf(top, __shfl_xor(top, d));
-    sum *= part_of(own, top);
+    for (uint32_t i = 0; i < EACH; ++i) {
+        const uint32_t m = m0 + i * 32;
+        const float own = top[i];
 #pragma unroll
-    for (int d = 1; d < 16; d *= 2) {
-        sum += __shfl_xor(sum, d);
-        all += __shfl_xor(all, d);
-    }
-    if (c == 0) {
-        const uint64_t at = (uint64_t)blockIdx.x * a.m + m;
-        a.top[at] = top;
-        a.sum[at] = sum;
-        if (a.all)
-            a.all[at] = all;
+        for (int d = 1; d < 16; d *= 2)
+            top[i] = fmaxf(top[i], __shfl_xor(top[i], d));
+        sum[i] *= part_of(own, top[i]);
+#pragma unroll
+        for (int d = 1; d < 16; d *= 2) {
+            sum[i] += __shfl_xor(sum[i], d);
+            all[i] += __shfl_xor(all[i], d);
+        }
+        if (c == 0 && m < count) {
+            const uint64_t at = (uint64_t)blockIdx.x * a.m + m;
+            a.top[at] = top[i];
+            a.sum[at] = sum[i];
+            if (a.all)
+                a.all[at] = all[i];
+        }
     }
 }
 
@@ -423,61 +471,77 @@ __global__ __launch_bounds__(256) void join_kernel(LossArgs a, uint32_t parts, f
 // host
 // ---------------------------------------------------------------------------
 
-// As many workgroups as run at the same time for few rows.
+// Workgroups for few rows: as many as are there at the same time.
 constexpr uint32_t kFewGroups = 1024;
 
-bool few(uint64_t m, uint64_t n, uint64_t k) { return m <= kFewRows && n >= 2048 && k >= 256; }
+bool few(uint64_t m) { return m <= kFewRows; }
+bool packs(uint64_t m, uint64_t k) { return k % 8 && m >= kPackLoss; }
 
-// Tiles as the linear layer cuts them, but never parts of k.
 struct LossCut {
-    int tile;
-    uint32_t tn, parts;
+    Plan plan;
+    uint32_t parts;  // of a row
+    size_t piece;    // columns whose w is packed at a time; 0: none are
 };
 
 LossCut loss_cut(uint64_t m, uint64_t n, uint64_t k) {
     LossCut c;
-    c.tile = cut(m, n, k).tile;
-    c.tn = (uint32_t)((n + kTile[c.tile] - 1) / kTile[c.tile]);
-    c.parts = few(m, n, k) ? std::max(c.tn, kFewGroups) : c.tn;
+    c.plan = plan_product(m, n, k, false);
+    c.parts = (uint32_t)((n + kTile[c.plan.tile] - 1) / kTile[c.plan.tile]);
+    if (few(m))
+        c.parts = std::max(c.parts, kFewGroups);
+    // whole tiles
+    c.piece = packs(m, k) ? std::min<size_t>(std::max<size_t>(kPieceElements / k / 256, 1) * 256,
+                                             (n + 255) / 256 * 256)
+                          : 0;
     return c;
 }
 
-LossArgs carve_loss(Carve &c, size_t m, size_t n, size_t k) {
+struct LossBuffers {
     LossArgs a = {};
-    a.rows = carve_rows(c, m, k);
+    uint16_t *w;
+};
+
+LossBuffers carve_loss(Carve &c, size_t m, size_t n, size_t k) {
+    LossBuffers b;
+    b.a.rows = carve_rows(c, m, k);
     const LossCut t = loss_cut(m, n, k);
-    a.top = c.take<float>((size_t)t.parts * m);
-    a.sum = c.take<float>((size_t)t.parts * m);
-    a.all = c.take<float>((size_t)t.parts * m);
-    return a;
+    b.a.top = c.take<float>((size_t)t.parts * m);
+    b.a.sum = c.take<float>((size_t)t.parts * m);
+    b.a.all = c.take<float>((size_t)t.parts * m);
+    b.w = c.take<uint16_t>(t.piece * b.a.rows.ld);
+    return b;
 }
 
+// The tiles [first, last) of the columns.
 template <class T, bool STAGED>
-int launch_loss(LossArgs &a, int tile, uint32_t tn, hipStream_t s) {
+int launch_loss(LossArgs a, const Plan &p, uint32_t first, uint32_t last, hipStream_t s) {
     auto go = [&](auto core) {
         using Core = decltype(core);
         const uint64_t tm = (a.m + Core::BM - 1) / Core::BM;
         int rc = allow_lds(loss_kernel<T, Core>, Core::LDS);
         // a launch takes fewer than 2^32 lanes
         const uint32_t most = (uint32_t)((1ull << 31) / Core::THREADS / tm);
-        for (a.first = 0; !rc && a.first < tn; a.first += a.tn) {
-            a.tn = std::min(most, tn - a.first);
+        for (a.first = first; !rc && a.first < last; a.first += a.tn) {
+            a.tn = std::min(most, last - a.first);
             rc = launch(loss_kernel<T, Core>, dim3((uint32_t)tm * a.tn), dim3(Core::THREADS),
                         Core::LDS, s, a);
         }
         return rc;
     };
-    if (tile == 0)
+    if (p.tile == 0)
         return go(gemm::Core<T, 256, 256, 2, 4, 64, 2, false, false, STAGED, !STAGED>());
-    if (tile == 1)
+    if (p.tile == 1)
         return go(gemm::Core<T, 128, 128, 2, 2, 64, 2, false, false, STAGED>());
+    if (p.deep && !STAGED)
+        return go(gemm::Core<T, 64, 64, 2, 2, 64, kDeep, false, false, STAGED>());
     return go(gemm::Core<T, 64, 64, 2, 2, 64, 3, false, false, STAGED>());
 }
 
 template <class T>
 int loss(const ddl_ce_args *c, void *ws, hipStream_t s) {
     Carve carve{(uint8_t *)ws};
-    LossArgs a = carve_loss(carve, c->m, c->n, c->k);
+    LossBuffers buf = carve_loss(carve, c->m, c->n, c->k);
+    LossArgs &a = buf.a;
     RowsArgs r = {};
     r.m = (uint32_t)c->m;
     r.n = c->n;
@@ -498,16 +562,30 @@ int loss(const ddl_ce_args *c, void *ws, hipStream_t s) {
     if (c->smoothing == 0.0)
         a.all = nullptr;
     const LossCut t = loss_cut(c->m, c->n, c->k);
-    uint32_t parts = t.tn;
+    const uint32_t side = kTile[t.plan.tile];
+    uint32_t parts = (uint32_t)((c->n + side - 1) / side);
     // straight to LDS or registers where every row starts on 16 bytes
     const bool direct = c->k % 8 == 0 && aligned16(c->w, c->ldw, 2);
-    if (direct && few(c->m, c->n, c->k)) {
+    if (direct && few(c->m)) {
         const uint32_t groups = (uint32_t)((c->n + 15) / 16);
         parts = std::min(kFewGroups, groups);
-        rc = launch(few_kernel<T>, dim3(parts), dim3(kFewWaves * 64), 0, s, a, groups);
+        rc = launch(c->m <= 16   ? few_kernel<T, 1>
+                    : c->m <= 32 ? few_kernel<T, 2>
+                                 : few_kernel<T, 4>,
+                    dim3(parts), dim3(kFewWaves * 64), 0, s, a, groups);
+    } else if (t.piece) {
+        for (size_t first = 0; first < c->n && !rc; first += t.piece) {
+            const size_t have = std::min(t.piece, c->n - first);
+            rc = pack_matrix((const uint16_t *)c->w + first * c->ldw, c->ldw, have, c->k, buf.w, s);
+            // tiles go by their columns' places in the whole of w
+            a.w = operand(buf.w - first * a.rows.ld, a.rows.ld, c->n, c->k);
+            if (!rc)
+                rc = launch_loss<T, false>(a, t.plan, (uint32_t)(first / side),
+                                           (uint32_t)((first + have + side - 1) / side), s);
+        }
     } else {
-        rc = direct ? launch_loss<T, false>(a, t.tile, t.tn, s)
-                    : launch_loss<T, true>(a, t.tile, t.tn, s);
+        rc = direct ? launch_loss<T, false>(a, t.plan, 0, parts, s)
+                    : launch_loss<T, true>(a, t.plan, 0, parts, s);
     }
     if (rc)
         return rc;
