@@ -45,12 +45,6 @@ struct DzArgs {
     float *db;              // [row tile][ld]: column sums, or null
 };
 
-struct RowOf {
-    float lse, g;
-    uint32_t want;  // target - the piece's first class
-    u32x4 bias[1];
-};
-
 template <class T, class Core>
 __global__ __launch_bounds__(Core::THREADS) void dz_kernel(DzArgs a) {
     using E = typename T::E;
@@ -68,55 +62,84 @@ __global__ __launch_bounds__(Core::THREADS) void dz_kernel(DzArgs a) {
     f32x4 acc[Core::FM][Core::FN] = {};
     if (a.x.k)
         Core::run(a.x, a.w, 0, (uint32_t)((a.x.k + Core::BK - 1) / Core::BK), 0, lds, acc);
+    // dz in place of the logits.  A lane holds, of row l % 16 of each of its FM
+    // fragments, 4 columns of each of the FN fragments.
     const uint32_t m0 = ti * BM, n0 = tj * BN, rows = (uint32_t)up64(count);
+    const uint32_t wave = threadIdx.x >> 6, l = threadIdx.x & 63u;
+    const uint32_t col = n0 + wave % Core::WC * (Core::FN * 16) + (l >> 4) * 4;
+    const uint32_t row0 = m0 + wave / Core::WC * (Core::FM * 16) + (l & 15u);
+    float lse[Core::FM], g[Core::FM];
+    uint32_t want[Core::FM];
+#pragma unroll
+    for (int i = 0; i < Core::FM; ++i) {
+        const uint32_t row = row0 + i * 16;
+        const bool in = row < count;
+        lse[i] = in ? a.rows.lse[row] : 0.0f;
+        g[i] = in ? a.rows.g[row] * factor : 0.0f;
+        want[i] = (in ? (uint32_t)a.rows.target[row] : ~0u) - a.first - col;
+    }
+    if (a.bias)
+#pragma unroll
+        for (int j = 0; j < Core::FN; ++j) {
+            const uint32_t c = col + j * 16;
+            float b[4];
+            load4((const E *)a.bias + c, c < a.n ? a.n - c : 0, b);
+#pragma unroll
+            for (int i = 0; i < Core::FM; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[i][j][e] += b[e];
+        }
+#pragma unroll
+    for (int i = 0; i < Core::FM; ++i) {
+#pragma unroll
+        for (int j = 0; j < Core::FN; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                acc[i][j][e] =
+                    (__builtin_amdgcn_exp2f((acc[i][j][e] - lse[i]) * kLog2e) - a.smooth) * g[i];
+        // few rows have their target among the wave's columns
+        if (__any(want[i] < Core::FN * 16))
+#pragma unroll
+            for (int j = 0; j < Core::FN; ++j)
+#pragma unroll
+                for (uint32_t e = 0; e < 4; ++e)
+                    if (want[i] == j * 16 + e)
+                        acc[i][j][e] -= a.wanted * g[i];
+    }
+    if (m0 + BM > count || n0 + BN > a.n)
+#pragma unroll
+        for (int i = 0; i < Core::FM; ++i)
+#pragma unroll
+            for (int j = 0; j < Core::FN; ++j)
+#pragma unroll
+                for (uint32_t e = 0; e < 4; ++e)
+                    if (row0 + i * 16 >= count || col + j * 16 + e >= a.n)
+                        acc[i][j][e] = 0.0f;
     float sums[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     Core::template each<false, 1>(
-        acc, lds,
-        [&](uint32_t mi, uint32_t ni) {
-            RowOf f;
-            const uint32_t m = m0 + mi, n = n0 + ni;
-            if (m >= count || n >= a.ld)
-                return f;
-            f.lse = a.rows.lse[m];
-            f.g = a.rows.g[m];
-            f.want = (uint32_t)a.rows.target[m] - a.first;
-            if (a.bias)
-                load8<false>((const E *)a.bias + n, n < a.n ? a.n - n : 0, f.bias);
-            return f;
-        },
-        [&](uint32_t mi, uint32_t ni, float (&v)[8], const RowOf &f) {
+        acc, lds, [](uint32_t, uint32_t) { return 0; },
+        [&](uint32_t mi, uint32_t ni, float (&v)[8], int) {
             const uint32_t m = m0 + mi, n = n0 + ni;
             if (m >= rows || n >= a.ld)
                 return;
-            if (a.bias) {
-                float b[8];
-                widen8<E>(f.bias, b);
+            store8<true>((E *)a.dz[0] + m * a.ld + n, 8, v);
+            if (a.db)
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    v[e] += b[e];
-            }
-            float low[8];
-            const float g = f.g * factor;
+                    sums[e] += v[e];
+            if (a.dz[1]) {
 #pragma unroll
-            for (uint32_t e = 0; e < 8; ++e) {
-                float p = __builtin_amdgcn_exp2f((v[e] - f.lse) * kLog2e) - a.smooth;
-                if (n + e == f.want)
-                    p -= a.wanted;
-                p = n + e < a.n && m < count ? p * g : 0.0f;
-                sums[e] += p;
-                v[e] = p;
-                low[e] = p - (float)(E)p;
+                for (int e = 0; e < 8; ++e)
+                    v[e] -= (float)(E)v[e];
+                store8<true>((E *)a.dz[1] + m * a.ld + n, 8, v);
             }
-            store8<true>((E *)a.dz[0] + m * a.ld + n, 8, v);
-            if (a.dz[1])
-                store8<true>((E *)a.dz[1] + m * a.ld + n, 8, low);
         });
     if (!a.db)
         return;
     // a lane holds the sums of 8 columns over its rows; the wave's other rows
     // of the same columns are in the lanes LANES apart
     constexpr uint32_t LANES = Core::FN * 2;
-    const uint32_t wave = threadIdx.x >> 6, l = threadIdx.x & 63u;
 #pragma unroll
     for (int e = 0; e < 8; ++e)
 #pragma unroll
@@ -179,7 +202,7 @@ struct GradArgs {
     const RowsHead *head;
     Operand a, b;
     uint32_t tn, splits;
-    uint64_t tile_rows;  // dx: 0 (they go by the count); dw: tiles of m
+    uint32_t tile_rows;  // tiles of m, of the caller's rows with dx
     float *partial;      // splits > 1: [splits][m][part_ld]
     uint64_t part_ld;    // n rounded up to 8
     Out o;
@@ -188,6 +211,31 @@ struct GradArgs {
 struct Old {
     u32x4 v[2];
 };
+
+// As load8 and store8, in whole vectors wherever all 8 elements are there: global
+// memory takes them at any element's address (dw of 32003 x 1111 in bfloat16, whose
+// rows start anywhere: 107 us element by element).
+template <bool VEC, class E>
+__device__ __forceinline__ void read8(const E *p, uint32_t have, u32x4 (&out)[sizeof(E) / 2]) {
+    if (VEC || have >= 8)
+        __builtin_memcpy(out, p, 8 * sizeof(E));
+    else
+        load8<false>(p, have, out);
+}
+template <bool VEC, class E>
+__device__ __forceinline__ void write8(E *p, uint32_t have, const float (&v)[8]) {
+    if (VEC) {
+        store8<true>(p, 8, v);
+    } else if (have >= 8) {
+        E t[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            t[i] = (E)v[i];
+        __builtin_memcpy(p, t, sizeof(t));
+    } else {
+        store8<false>(p, have, v);
+    }
+}
 
 template <class E, bool DX, bool VEC>
 __device__ __forceinline__ Old old8(const Out &o, uint32_t m, uint32_t n) {
@@ -200,10 +248,10 @@ __device__ __forceinline__ Old old8(const Out &o, uint32_t m, uint32_t n) {
     } else if (o.add) {
         const uint32_t have = o.n - n < 8 ? o.n - n : 8;
         if (o.f32) {
-            load8<VEC>((const float *)o.c + m * o.ld + n, have, f.v);
+            read8<VEC>((const float *)o.c + m * o.ld + n, have, f.v);
         } else {
             u32x4 t[1];
-            load8<VEC>((const E *)o.c + m * o.ld + n, have, t);
+            read8<VEC>((const E *)o.c + m * o.ld + n, have, t);
             f.v[0] = t[0];
         }
     }
@@ -231,7 +279,7 @@ __device__ __forceinline__ void out8(const Out &o, float inverse, uint32_t m, ui
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             v[i] *= inverse;
-        store8<VEC>((E *)o.c + o.row[m] * o.ld + n, have, v);
+        write8<VEC>((E *)o.c + o.row[m] * o.ld + n, have, v);
         return;
     }
 #pragma unroll
@@ -249,9 +297,17 @@ __device__ __forceinline__ void out8(const Out &o, float inverse, uint32_t m, ui
             v[i] += t[i];
     }
     if (o.f32)
-        store8<VEC>((float *)o.c + m * o.ld + n, have, v);
+        write8<VEC>((float *)o.c + m * o.ld + n, have, v);
     else
-        store8<VEC>((E *)o.c + m * o.ld + n, have, v);
+        write8<VEC>((E *)o.c + m * o.ld + n, have, v);
+}
+
+// The parts of dx's sums: with fewer row tiles than were launched for, their
+// workgroups take parts of k instead, which the same memory holds.
+__device__ __forceinline__ uint32_t parts_of(const GradArgs &g, uint32_t tm, uint32_t kt) {
+    if (g.splits == 1 || !tm)
+        return g.splits;
+    return min(g.splits * g.tile_rows / tm, max(kt / 4, g.splits));
 }
 
 // DX: C = dz w over the piece's classes.  Otherwise C = dz^T x over the packed
@@ -266,19 +322,20 @@ __global__ __launch_bounds__(Core::THREADS) void grad_kernel(GradArgs g) {
     } else {
         g.a.k = g.b.k = up64(count);
     }
-    const uint32_t tm = DX ? (count + Core::BM - 1) / Core::BM : (uint32_t)g.tile_rows;
-    if (blockIdx.x >= tm * g.tn)
+    const uint32_t tm = DX ? (count + Core::BM - 1) / Core::BM : g.tile_rows;
+    const uint32_t kt = (uint32_t)((g.a.k + Core::BK - 1) / Core::BK);
+    const uint32_t all = PAIR ? 2 * kt : kt;
+    const uint32_t splits = DX ? parts_of(g, tm, kt) : g.splits;
+    if (blockIdx.x >= tm * g.tn * splits)
         return;
+    const uint32_t s = blockIdx.x / (tm * g.tn);
     uint32_t ti, tj;
-    tile_of(blockIdx.x, tm, g.tn, ti, tj);
+    tile_of(blockIdx.x - s * tm * g.tn, tm, g.tn, ti, tj);
     g.a.row0 = ti * Core::BM;
     g.b.row0 = tj * Core::BN;
     const float inverse = g.head->inverse;
-    const uint32_t s = blockIdx.y;
-    const uint32_t kt = (uint32_t)((g.a.k + Core::BK - 1) / Core::BK);
-    const uint32_t all = PAIR ? 2 * kt : kt;
-    const uint32_t t0 = (uint32_t)((uint64_t)all * s / g.splits);
-    const uint32_t t1 = (uint32_t)((uint64_t)all * (s + 1) / g.splits);
+    const uint32_t t0 = (uint32_t)((uint64_t)all * s / splits);
+    const uint32_t t1 = (uint32_t)((uint64_t)all * (s + 1) / splits);
     f32x4 acc[Core::FM][Core::FN] = {};
     // of the three passes over pairs, the two that take b's one part
     if (t0 < t1)
@@ -311,10 +368,13 @@ __global__ __launch_bounds__(Core::THREADS) void grad_kernel(GradArgs g) {
 
 // The sums of the parts, in their order; 8 columns a lane.
 template <class T, bool DX>
-__global__ __launch_bounds__(256) void grad_join(GradArgs g) {
+__global__ __launch_bounds__(256) void grad_join(GradArgs g, uint32_t side) {
     using E = typename T::E;
-    if (DX)
+    uint32_t splits = g.splits;
+    if (DX) {
         g.o.m = g.head->count;
+        splits = parts_of(g, (g.o.m + side - 1) / side, (uint32_t)((g.a.k + 63) / 64));
+    }
     const uint32_t groups = (g.o.n + 7) / 8;
     const uint64_t id = (uint64_t)blockIdx.x * 256 + threadIdx.x;
     if (id >= (uint64_t)groups * g.o.m)
@@ -324,7 +384,7 @@ __global__ __launch_bounds__(256) void grad_join(GradArgs g) {
     const Old f = g.o.vec ? old8<E, DX, true>(g.o, m, n) : old8<E, DX, false>(g.o, m, n);
     float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll 4
-    for (uint32_t s = 0; s < g.splits; ++s) {
+    for (uint32_t s = 0; s < splits; ++s) {
         const float *p = g.partial + ((uint64_t)s * g.o.m + m) * g.part_ld + n;
         const f32x4 x = *(const f32x4 *)p, y = *(const f32x4 *)(p + 4);
 #pragma unroll
@@ -368,7 +428,9 @@ size_t partial_floats(size_t m, size_t n, size_t k, size_t piece) {
     size_t most = 0;
     for (const size_t have : {std::min(piece, n), last}) {
         const Plan x = plan_product(m, k, have, true), w = plan_product(have, k, m, true);
-        most = std::max(most, x.splits > 1 ? x.splits * m * kp : 0);
+        // whole tiles of rows: see parts_of
+        const size_t rows = (m + kTile[x.tile] - 1) / kTile[x.tile] * kTile[x.tile];
+        most = std::max(most, x.splits > 1 ? x.splits * rows * kp : 0);
         most = std::max(most, w.splits > 1 ? w.splits * have * kp : 0);
     }
     return most;
@@ -418,11 +480,12 @@ int launch_grad(GradArgs &g, const Plan &c, uint64_t m, hipStream_t s) {
         g.splits = c.splits;
         int rc = allow_lds(kernel, Core::LDS);
         rc = rc ? rc
-                : launch(kernel, dim3(tm * g.tn, g.splits), dim3(Core::THREADS), Core::LDS, s, g);
+                : launch(kernel, dim3(tm * g.tn * g.splits), dim3(Core::THREADS), Core::LDS, s, g);
         if (rc || g.splits == 1)
             return rc;
         const uint64_t lanes = (uint64_t)(g.o.n + 7) / 8 * m;
-        return launch(grad_join<T, DX>, dim3((uint32_t)((lanes + 255) / 256)), dim3(256), 0, s, g);
+        return launch(grad_join<T, DX>, dim3((uint32_t)((lanes + 255) / 256)), dim3(256), 0, s, g,
+                      (uint32_t)Core::BM);
     };
     if (c.tile == 0)
         return go(gemm::Core<T, 256, 256, 2, 4, 64, 2, !DX, true, STAGED, !STAGED>());

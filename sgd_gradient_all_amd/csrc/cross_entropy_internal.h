@@ -22,6 +22,22 @@ constexpr size_t kMaxTargets = 1u << 22;
 constexpr int32_t kBadTarget = 0x7fffffff;  // a class that does not exist: its results are NaN
 constexpr float kLog2e = 1.4426950408889634f;
 
+// 4 consecutive values of 16 bits from anywhere; those past `have` are 0.
+template <class E>
+__device__ __forceinline__ void load4(const E *p, uint32_t have, float (&out)[4]) {
+    E v[4];
+    if (have >= 4) {
+        __builtin_memcpy(v, p, 8);
+    } else {
+#pragma unroll
+        for (uint32_t e = 0; e < 4; ++e)
+            v[e] = e < have ? p[e] : (E)0.0f;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        out[e] = (float)v[e];
+}
+
 // What the rows kernel counts.
 struct RowsHead {
     uint32_t count;  // rows with a target

@@ -37,12 +37,34 @@ __device__ __forceinline__ float factor_of(const RowsArgs &a, uint64_t i) {
     return a.dloss ? a.dloss[i] * a.scale : a.scale;
 }
 
-// Packs the indices of the rows with a target, in their order: one workgroup,
-// 4096 targets at a time (their counts by wave are then one wave's scan).
+__device__ __forceinline__ void write_row(const RowsArgs &a, const Rows &r, uint64_t at,
+                                          uint32_t i, long long target) {
+    const bool bad = (uint64_t)target >= a.n;
+    r.row[at] = i;
+    r.target[at] = bad ? kBadTarget : (int32_t)target;
+    if (a.lse) {
+        r.lse[at] = a.lse[i];
+        r.g[at] = bad ? __builtin_nanf("") : factor_of(a, i);
+    }
+}
+
 // Gradient: factor is the power of two that takes the largest |dloss scale| to
 // [2^14, 2^15).  dz = factor dloss scale (p - wanted) is held in 16 bits, and
 // |p - wanted| <= 1: so binary16 keeps 11 bits of every p down to 2^-29 of the
 // largest row's, whatever the loss is scaled by.
+__device__ __forceinline__ void write_head(const Rows &r, uint32_t count, float top) {
+    int e = 0;
+    if (top > 0.0f) {
+        e = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127;  // infinity: 128
+        e = 14 - (e < -86 ? -86 : e > 114 ? 114 : e);
+    }
+    r.head->count = count;
+    r.head->factor = ldexpf(1.0f, e);
+    r.head->inverse = ldexpf(1.0f, -e);
+}
+
+// Packs the indices of the rows with a target, in their order: one workgroup,
+// 4096 targets at a time (their counts by wave are then one wave's scan).
 __global__ __launch_bounds__(1024) void rows_kernel(RowsArgs a, Rows r) {
     constexpr uint32_t U = 4, WAVES = 16;
     __shared__ uint32_t counts[U * WAVES], before[U * WAVES + 1];
@@ -86,14 +108,9 @@ __global__ __launch_bounds__(1024) void rows_kernel(RowsArgs a, Rows r) {
             if (t[j] >= 0) {
                 const uint32_t at = base + before[j * WAVES + wave]
                                     + (uint32_t)__popcll(have[j] & ((1ull << lane) - 1));
-                const bool bad = (uint64_t)t[j] >= a.n;
-                r.row[at] = i;
-                r.target[at] = bad ? kBadTarget : (int32_t)t[j];
-                if (a.lse) {
-                    r.lse[at] = a.lse[i];
-                    r.g[at] = bad ? __builtin_nanf("") : g[j];
+                write_row(a, r, at, i, t[j]);
+                if (a.lse)
                     top = fmaxf(top, fabsf(g[j]));
-                }
             } else if (i < a.m && a.loss) {
                 a.loss[i] = 0.0f;
                 a.lse_out[i] = 0.0f;
@@ -111,14 +128,7 @@ __global__ __launch_bounds__(1024) void rows_kernel(RowsArgs a, Rows r) {
     if (threadIdx.x == 0) {
         for (uint32_t w = 1; w < WAVES; ++w)
             top = fmaxf(top, tops[w]);
-        int e = 0;
-        if (top > 0.0f) {
-            e = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127;  // infinity: 128
-            e = 14 - (e < -86 ? -86 : e > 114 ? 114 : e);
-        }
-        r.head->count = base;
-        r.head->factor = ldexpf(1.0f, e);
-        r.head->inverse = ldexpf(1.0f, -e);
+        write_head(r, base, top);
     }
 }
 
@@ -140,6 +150,11 @@ __device__ __forceinline__ void copy_row(const uint16_t *from, uint64_t k, uint1
     }
 }
 
+__device__ __forceinline__ void zero_row(uint16_t *to, uint64_t ld) {
+    for (uint64_t c = threadIdx.x * 8; c < ld; c += 256 * 8)
+        *(u32x4 *)(to + c) = u32x4{0, 0, 0, 0};
+}
+
 __global__ __launch_bounds__(256) void matrix_kernel(const uint16_t *from, uint64_t ld, uint64_t k,
                                                      uint16_t *to, uint64_t ld_to) {
     copy_row(from + blockIdx.x * ld, k, to + blockIdx.x * ld_to, ld_to);
@@ -150,8 +165,7 @@ __global__ __launch_bounds__(256) void matrix_kernel(const uint16_t *from, uint6
 __global__ __launch_bounds__(256) void pack_kernel(RowsArgs a, Rows r) {
     const uint64_t i = blockIdx.x, count = r.head->count;
     if (i >= count && i < up64(count))
-        for (uint64_t c = threadIdx.x * 8; c < r.ld; c += 256 * 8)
-            *(u32x4 *)(r.x + i * r.ld + c) = u32x4{0, 0, 0, 0};
+        zero_row(r.x + i * r.ld, r.ld);
     if (i < count) {
         const uint16_t *from = (const uint16_t *)a.x + (uint64_t)r.row[i] * a.ldx;
         uint16_t *to = r.x + i * r.ld;
@@ -162,9 +176,71 @@ __global__ __launch_bounds__(256) void pack_kernel(RowsArgs a, Rows r) {
             a.dx[i * a.lddx + c] = 0;
 }
 
+// Both at once for few rows, where a launch counts: workgroup i counts the targets
+// before its own row.
+constexpr uint32_t kPackFew = 1024;
+
+__global__ __launch_bounds__(256) void pack_few_kernel(RowsArgs a, Rows r) {
+    __shared__ uint32_t before[4], have[4];
+    __shared__ float tops[4];
+    const uint32_t i = blockIdx.x, lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
+    auto target = [&](uint32_t at) {
+        return at < a.m && (!a.lse || factor_of(a, at) != 0.0f) ? a.target[at] : -1;
+    };
+    const long long own = target(i);
+    long long t[kPackFew / 256];
+    float g[kPackFew / 256];
+#pragma unroll
+    for (uint32_t j = 0; j < kPackFew / 256; ++j) {
+        const uint32_t at = j * 256 + threadIdx.x;
+        t[j] = target(at);
+        g[j] = a.lse && at < a.m && t[j] >= 0 ? fabsf(factor_of(a, at)) : 0.0f;
+    }
+    uint32_t b = 0, h = 0;
+    float top = 0.0f;
+#pragma unroll
+    for (uint32_t j = 0; j < kPackFew / 256; ++j) {
+        h += (uint32_t)__popcll(__ballot(t[j] >= 0));
+        b += (uint32_t)__popcll(__ballot(t[j] >= 0 && j * 256 + threadIdx.x < i));
+        top = fmaxf(top, g[j]);
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2)
+        top = fmaxf(top, __shfl_xor(top, d));
+    if (lane == 0) {
+        before[wave] = b;
+        have[wave] = h;
+        tops[wave] = top;
+    }
+    __syncthreads();
+    const uint32_t at = before[0] + before[1] + before[2] + before[3];
+    const uint32_t count = have[0] + have[1] + have[2] + have[3];
+    if (i == 0 && threadIdx.x == 0)
+        write_head(r, count, fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])));
+    if (i >= count && i < up64(count))
+        zero_row(r.x + i * r.ld, r.ld);
+    if (i >= a.m)
+        return;
+    if (own >= 0) {
+        if (threadIdx.x == 0)
+            write_row(a, r, at, i, own);
+        copy_row((const uint16_t *)a.x + i * a.ldx, a.k, r.x + at * r.ld, r.ld);
+        return;
+    }
+    if (a.loss && threadIdx.x == 0) {
+        a.loss[i] = 0.0f;
+        a.lse_out[i] = 0.0f;
+    }
+    if (a.dx)
+        for (uint64_t c = threadIdx.x; c < a.k; c += 256)
+            a.dx[i * a.lddx + c] = 0;
+}
+
 }  // namespace
 
 int pack_rows(const RowsArgs &a, const Rows &r, hipStream_t s) {
+    if (a.m <= kPackFew)
+        return launch(pack_few_kernel, dim3((uint32_t)up64(a.m)), dim3(256), 0, s, a, r);
     const int rc = launch(rows_kernel, dim3(1), dim3(1024), 0, s, a, r);
     return rc ? rc : launch(pack_kernel, dim3((uint32_t)up64(a.m)), dim3(256), 0, s, a, r);
 }
@@ -211,49 +287,69 @@ __global__ __launch_bounds__(Core::THREADS) void loss_kernel(LossArgs a) {
     if (a.x.k)
         Core::run(a.x, a.w, 0, (uint32_t)((a.x.k + Core::BK - 1) / Core::BK), 0, lds, acc);
     const uint32_t wave = threadIdx.x >> 6, l = threadIdx.x & 63u;
+    const uint32_t m0 = (wave / Core::WC) * (Core::FM * 16) + (l & 15u);
     const uint32_t n0 = (wave % Core::WC) * (Core::FN * 16) + (l >> 4) * 4;
     const uint64_t col = (uint64_t)tj * BN + n0;
-    float bias[Core::FN][4];
+    if (a.bias)
 #pragma unroll
-    for (int j = 0; j < Core::FN; ++j)
+        for (int j = 0; j < Core::FN; ++j) {
+            const uint64_t c = col + j * 16;
+            float b[4];
+            load4((const E *)a.bias + c, c < a.n ? (uint32_t)(a.n - c) : 0u, b);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint64_t c = col + j * 16 + e;
-            bias[j][e] = a.bias && c < a.n ? (float)((const E *)a.bias)[c] : 0.0f;
+            for (int i = 0; i < Core::FM; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[i][j][e] += b[e];
         }
+    uint32_t want[Core::FM];  // the target, from the lane's first column on
+#pragma unroll
+    for (int i = 0; i < Core::FM; ++i) {
+        const uint32_t row = ti * BM + m0 + i * 16;
+        want[i] = (row < count ? (uint32_t)a.rows.target[row] : ~0u) - (uint32_t)col;
+    }
     const bool whole = (uint64_t)(tj + 1) * BN <= a.n;
     gemm::wait_and_meet<0>();  // every wave is done with the tiles
     float *tops = (float *)lds, *sums = tops + Core::WC * BM, *alls = sums + Core::WC * BM;
     static_assert(3 * Core::WC * BM * 4 <= Core::LDS, "the rows' part of LDS");
 #pragma unroll
     for (int i = 0; i < Core::FM; ++i) {
-        const uint32_t in = (wave / Core::WC) * (Core::FM * 16) + i * 16 + (l & 15u);
-        const uint32_t row = ti * BM + in;
-        const uint32_t want =
-            row < count ? (uint32_t)a.rows.target[row] - (uint32_t)col : ~0u;
+        const uint32_t in = m0 + i * 16, row = ti * BM + in;
+        // few rows have their target among the wave's columns
+        if (__any(want[i] < Core::FN * 16))
+#pragma unroll
+            for (int j = 0; j < Core::FN; ++j)
+#pragma unroll
+                for (uint32_t e = 0; e < 4; ++e)
+                    if (want[i] == j * 16 + e && col + j * 16 + e < a.n)
+                        a.rows.at[row] = acc[i][j][e];
         float top = kNone, all = 0.0f;
+        if (!whole)
 #pragma unroll
-        for (int j = 0; j < Core::FN; ++j)
+            for (int j = 0; j < Core::FN; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float v = acc[i][j][e] + bias[j][e];
-                if (want == (uint32_t)(j * 16 + e) && col + j * 16 + e < a.n)
-                    a.rows.at[row] = v;
-                if (!whole && col + j * 16 + e >= a.n)
-                    v = kNone;
-                else
-                    all += v;
-                acc[i][j][e] = v;
-                top = fmaxf(top, v);
-            }
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
-        float sum = 0.0f;
+                for (int e = 0; e < 4; ++e)
+                    acc[i][j][e] = col + j * 16 + e < a.n ? acc[i][j][e] : kNone;
 #pragma unroll
         for (int j = 0; j < Core::FN; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                sum += part_of(acc[i][j][e], top);
+                top = fmaxf(top, acc[i][j][e]);
+        if (a.all)
+#pragma unroll
+            for (int j = 0; j < Core::FN; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    all += whole || col + j * 16 + e < a.n ? acc[i][j][e] : 0.0f;
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        float sum = 0.0f;
+        const float over = top == kNone ? 0.0f : top;
+#pragma unroll
+        for (int j = 0; j < Core::FN; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                sum += __builtin_amdgcn_exp2f((acc[i][j][e] - over) * kLog2e);
         sum += __shfl_xor(sum, 16);
         sum += __shfl_xor(sum, 32);
         all += __shfl_xor(all, 16);
@@ -414,6 +510,121 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_kernel(LossArgs a, uint32_
     }
 }
 
+// A decoded token or a few: no matrix instruction, whose operand takes 64 bytes of
+// a row at a time.  A wave reads four rows of w as they lie, 1 KB a time, against
+// x in LDS, adds its lanes' sums up and keeps the largest logit and sum of its rows.
+constexpr uint64_t kVectorBytes = 32768;  // of x
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2)
+        v += __shfl_xor(v, d);
+    return v;
+}
+
+template <class E>
+__device__ __forceinline__ float dot8(u32x4 a, u32x4 b, float s) {
+    E x[8], y[8];
+    __builtin_memcpy(x, &a, 16);
+    __builtin_memcpy(y, &b, 16);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        s = __builtin_fmaf((float)x[e], (float)y[e], s);
+    return s;
+}
+
+template <class T, int M>
+__global__ __launch_bounds__(256) void vector_kernel(LossArgs a) {
+    using E = typename T::E;
+    constexpr uint32_t U = 4, WAVES = 4;
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    __shared__ float tops[WAVES][M], sums[WAVES][M], alls[WAVES][M];
+    const uint32_t count = a.rows.head->count, k = (uint32_t)a.x.k;  // a multiple of 8
+    const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
+    if (!count)
+        return;
+    u32x4 *xs = (u32x4 *)lds;
+    for (uint32_t c = threadIdx.x; c < M * k / 8; c += 256) {
+        const uint32_t m = c / (k / 8);
+        xs[c] = m < count ? ((const u32x4 *)(a.rows.x + m * a.rows.ld))[c - m * (k / 8)]
+                          : u32x4{0, 0, 0, 0};
+    }
+    __syncthreads();
+    float top[M], sum[M], all[M];
+    uint32_t want[M];
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+        top[m] = kNone;
+        sum[m] = all[m] = 0.0f;
+        want[m] = (uint32_t)m < count ? (uint32_t)a.rows.target[m] : ~0u;
+    }
+    const uint64_t r0 = a.n * blockIdx.x / gridDim.x, r1 = a.n * (blockIdx.x + 1) / gridDim.x;
+    for (uint64_t row = r0 + wave * U; row < r1; row += WAVES * U) {
+        const u32x4 *w[U];
+        float acc[U][M] = {};
+#pragma unroll
+        for (uint32_t u = 0; u < U; ++u)
+            w[u] = (const u32x4 *)(a.w.plane[0] + (row + u < r1 ? row + u : r1 - 1) * a.w.ld);
+        uint32_t c = lane;
+#pragma unroll 2
+        for (; c < k / 8; c += 64) {
+            u32x4 v[U];
+#pragma unroll
+            for (uint32_t u = 0; u < U; ++u)
+                v[u] = __builtin_nontemporal_load(w[u] + c);
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                const u32x4 x = xs[m * (k / 8) + c];
+#pragma unroll
+                for (uint32_t u = 0; u < U; ++u)
+                    acc[u][m] = dot8<E>(v[u], x, acc[u][m]);
+            }
+        }
+#pragma unroll
+        for (uint32_t u = 0; u < U; ++u) {
+            const uint64_t n = row + u;
+            if (n >= r1)
+                break;
+            const float b = a.bias ? (float)((const E *)a.bias)[n] : 0.0f;
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                const float z = wave_sum(acc[u][m]) + b;
+                if (want[m] == (uint32_t)n && lane == 0)
+                    a.rows.at[m] = z;
+                all[m] += z;
+                const float old = top[m];
+                top[m] = fmaxf(old, z);
+                sum[m] = sum[m] * part_of(old, top[m]) + part_of(z, top[m]);
+            }
+        }
+    }
+    if (lane == 0)
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            tops[wave][m] = top[m];
+            sums[wave][m] = sum[m];
+            alls[wave][m] = all[m];
+        }
+    __syncthreads();
+    const uint32_t m = threadIdx.x;
+    if (m >= M || m >= count)
+        return;
+    float t = kNone, s = 0.0f, z = 0.0f;
+#pragma unroll
+    for (uint32_t v = 0; v < WAVES; ++v)
+        t = fmaxf(t, tops[v][m]);
+#pragma unroll
+    for (uint32_t v = 0; v < WAVES; ++v) {
+        s += sums[v][m] * part_of(tops[v][m], t);
+        z += alls[v][m];
+    }
+    const uint64_t at = (uint64_t)blockIdx.x * a.m + m;
+    a.top[at] = t;
+    a.sum[at] = s;
+    if (a.all)
+        a.all[at] = z;
+}
+
 // A row's parts, joined: R rows by 256 / R lanes a workgroup.
 template <int R>
 __global__ __launch_bounds__(256) void join_kernel(LossArgs a, uint32_t parts, float smoothing,
@@ -566,7 +777,14 @@ int loss(const ddl_ce_args *c, void *ws, hipStream_t s) {
     uint32_t parts = (uint32_t)((c->n + side - 1) / side);
     // straight to LDS or registers where every row starts on 16 bytes
     const bool direct = c->k % 8 == 0 && aligned16(c->w, c->ldw, 2);
-    if (direct && few(c->m)) {
+    const size_t m = c->m <= 2 ? c->m : 4;
+    if (direct && c->m <= m && m * c->k * 2 <= kVectorBytes && c->k) {
+        parts = (uint32_t)std::min<size_t>(kFewGroups, (c->n + 15) / 16);
+        rc = launch(m == 1   ? vector_kernel<T, 1>
+                    : m == 2 ? vector_kernel<T, 2>
+                             : vector_kernel<T, 4>,
+                    dim3(parts), dim3(256), m * c->k * sizeof(uint16_t), s, a);
+    } else if (direct && few(c->m)) {
         const uint32_t groups = (uint32_t)((c->n + 15) / 16);
         parts = std::min(kFewGroups, groups);
         rc = launch(c->m <= 16   ? few_kernel<T, 1>
