@@ -163,20 +163,36 @@ __global__ __launch_bounds__(Core::THREADS) void dz_kernel(DzArgs a) {
 }
 
 // db of a piece from its row tiles' sums.
-template <class O>
-__global__ __launch_bounds__(256) void db_kernel(const RowsHead *head, const float *sums,
-                                                 uint64_t ld, uint32_t side, uint32_t n, O *db,
-                                                 int add) {
-    const uint32_t c = blockIdx.x * 256 + threadIdx.x;
-    if (c >= n)
+struct DbArgs {
+    const float *sums;  // [row tile][ld]
+    uint64_t ld;
+    uint32_t side, n;   // rows of a tile; the piece's classes
+    void *db;           // of the piece, E or binary32; or null
+    int f32, add;
+};
+
+template <class E>
+__device__ __forceinline__ void db_of(const DbArgs &a, const RowsHead *head, uint32_t c) {
+    if (c >= a.n)
         return;
-    const uint32_t tm = (head->count + side - 1) / side;
+    const uint32_t tm = (head->count + a.side - 1) / a.side;
     float v = 0.0f;
 #pragma unroll 8
     for (uint32_t t = 0; t < tm; ++t)
-        v += sums[t * ld + c];
+        v += a.sums[t * a.ld + c];
     v *= head->inverse;
-    db[c] = (O)(add ? (float)db[c] + v : v);
+    if (a.f32) {
+        float *to = (float *)a.db + c;
+        *to = a.add ? *to + v : v;
+    } else {
+        E *to = (E *)a.db + c;
+        *to = (E)(a.add ? (float)*to + v : v);
+    }
+}
+
+template <class E>
+__global__ __launch_bounds__(256) void db_kernel(const RowsHead *head, DbArgs a) {
+    db_of<E>(a, head, blockIdx.x * 256 + threadIdx.x);
 }
 
 // ---------------------------------------------------------------------------
@@ -206,6 +222,7 @@ struct GradArgs {
     float *partial;      // splits > 1: [splits][m][part_ld]
     uint64_t part_ld;    // n rounded up to 8
     Out o;
+    DbArgs db;           // dw: taken by the workgroups of the first columns
 };
 
 struct Old {
@@ -341,6 +358,9 @@ __global__ __launch_bounds__(Core::THREADS) void grad_kernel(GradArgs g) {
     if (t0 < t1)
         Core::run(g.a, g.b, (PAIR ? kt : 0) + t0, (PAIR ? kt : 0) + t1, PAIR ? kt : 0, lds, acc);
     const uint32_t m0 = g.a.row0, n0 = g.b.row0;
+    if (!DX && g.db.db && tj == 0 && s == 0)
+        for (uint32_t c = threadIdx.x; c < Core::BM; c += Core::THREADS)
+            db_of<E>(g.db, g.head, m0 + c);
     if (g.splits > 1) {
         float *part = g.partial + (uint64_t)s * g.o.m * g.part_ld;
         Core::each(
@@ -427,9 +447,9 @@ size_t partial_floats(size_t m, size_t n, size_t k, size_t piece) {
     const size_t kp = (k + 7) / 8 * 8, last = n - (n - 1) / piece * piece;
     size_t most = 0;
     for (const size_t have : {std::min(piece, n), last}) {
-        const Plan x = plan_product(m, k, have, true), w = plan_product(have, k, m, true);
+        const Plan x = plan_product(m, k, have, false), w = plan_product(have, k, m, false);
         // whole tiles of rows: see parts_of
-        const size_t rows = (m + kTile[x.tile] - 1) / kTile[x.tile] * kTile[x.tile];
+        const size_t rows = (m + kSideM[x.tile] - 1) / kSideM[x.tile] * kSideM[x.tile];
         most = std::max(most, x.splits > 1 ? x.splits * rows * kp : 0);
         most = std::max(most, w.splits > 1 ? w.splits * have * kp : 0);
     }
@@ -464,9 +484,9 @@ int launch_dz(DzArgs &a, const Plan &p, uint64_t m, hipStream_t s) {
         return go(gemm::Core<T, 256, 256, 2, 4, 64, 2, false, false, STAGED, !STAGED>());
     if (p.tile == 1)
         return go(gemm::Core<T, 128, 128, 2, 2, 64, 2, false, false, STAGED>());
-    if (p.deep && !STAGED)
-        return go(gemm::Core<T, 64, 64, 2, 2, 64, kDeep, false, false, STAGED>());
-    return go(gemm::Core<T, 64, 64, 2, 2, 64, 3, false, false, STAGED>());
+    if (p.tile == 2)
+        return go(gemm::Core<T, 64, 64, 2, 2, 64, 3, false, false, STAGED>());
+    return go(gemm::Core<T, 64, 32, 4, 1, 64, 3, false, false, STAGED>());
 }
 
 template <class T, bool DX, bool PAIR, bool STAGED>
@@ -491,8 +511,6 @@ int launch_grad(GradArgs &g, const Plan &c, uint64_t m, hipStream_t s) {
         return go(gemm::Core<T, 256, 256, 2, 4, 64, 2, !DX, true, STAGED, !STAGED>());
     if (c.tile == 1)
         return go(gemm::Core<T, 128, 128, 2, 2, 64, 2, !DX, true, STAGED>());
-    if (c.deep && !STAGED)
-        return go(gemm::Core<T, 64, 64, 2, 2, 64, kDeep, !DX, true, STAGED>());
     return go(gemm::Core<T, 64, 64, 2, 2, 64, 3, !DX, true, STAGED>());
 }
 
@@ -543,14 +561,21 @@ int gradient(const ddl_ce_grad_args *c, void *ws, hipStream_t s) {
         d.dz[1] = c->dw && f32 ? b.dz[1] : nullptr;
         d.ld = (have + 63) / 64 * 64;
         d.db = c->db ? b.db : nullptr;
-        const Plan p = plan_product(m, have, k, false);
+        const Plan p = plan_product(m, have, k, true);
         rc = direct ? launch_dz<T, false>(d, p, m, s) : launch_dz<T, true>(d, p, m, s);
-        if (!rc && c->db) {
-            const dim3 grid((uint32_t)((have + 255) / 256));
-            rc = f32 ? launch(db_kernel<float>, grid, dim3(256), 0, s, b.rows.head, b.db, d.ld,
-                              kTile[p.tile], d.n, (float *)c->db + first, c->accumulate)
-                     : launch(db_kernel<E>, grid, dim3(256), 0, s, b.rows.head, b.db, d.ld,
-                              kTile[p.tile], d.n, (E *)c->db + first, c->accumulate);
+        const size_t esz = f32 ? 4 : 2;
+        DbArgs db = {};
+        if (c->db) {
+            db.sums = b.db;
+            db.ld = d.ld;
+            db.side = kSideM[p.tile];
+            db.n = d.n;
+            db.db = (uint8_t *)c->db + first * esz;
+            db.f32 = f32;
+            db.add = c->accumulate;
+            if (!rc && (!c->dw || !k))
+                rc = launch(db_kernel<E>, dim3((uint32_t)((have + 255) / 256)), dim3(256), 0, s,
+                            b.rows.head, db);
         }
         if (!rc && c->dx && k) {
             GradArgs g = {};
@@ -569,14 +594,14 @@ int gradient(const ddl_ce_grad_args *c, void *ws, hipStream_t s) {
             g.o.read = first > 0;
             g.o.write = first + have < n;
             g.o.vec = k % 8 == 0 && aligned16(c->dx, c->lddx, 2);
-            const Plan t = plan_product(m, k, have, true);
+            const Plan t = plan_product(m, k, have, false);
             rc = direct ? launch_grad<T, true, false, false>(g, t, m, s)
                         : launch_grad<T, true, false, true>(g, t, m, s);
         }
         if (!rc && c->dw && k) {
             GradArgs g = {};
-            const size_t esz = f32 ? 4 : 2;
             g.head = b.rows.head;
+            g.db = db;
             g.a = operand(b.dz[0], d.ld, d.ld, 0);
             g.a.plane[1] = b.dz[1];
             g.b = operand(b.rows.x, b.rows.ld, b.rows.ld, 0);
@@ -589,7 +614,7 @@ int gradient(const ddl_ce_grad_args *c, void *ws, hipStream_t s) {
             g.o.f32 = f32;
             g.o.add = c->accumulate;
             g.o.vec = k % 8 == 0 && aligned16(g.o.c, c->lddw, esz);
-            const Plan t = plan_product(have, k, m, true);
+            const Plan t = plan_product(have, k, m, false);
             rc = f32 ? launch_grad<T, false, true, false>(g, t, have, s)
                      : launch_grad<T, false, false, false>(g, t, have, s);
         }

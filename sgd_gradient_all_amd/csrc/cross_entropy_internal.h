@@ -114,34 +114,38 @@ constexpr size_t kPieceElements = 128u << 20;
 int pack_matrix(const void *from, size_t ld, size_t rows, size_t k, uint16_t *to, hipStream_t s);
 
 // How a product is cut, by the time that it should take: rounds of workgroups over
-// the chip, each of k tiles of 64 at what a tile was measured to take (us, with
-// the chip full of its kind: 1.3, 1.0 and 0.65 PFLOP/s), and where k is cut the
-// parts' way through memory.
-constexpr int kDeep = 8;  // tiles in LDS
+// the chip, each of k tiles of 64 at what a tile was measured to take (us; with
+// the chip full of its kind, 1.3, 1.0 and 0.65 PFLOP/s, and with one workgroup a
+// compute unit, where copies to LDS set the pace), and where k is cut the parts'
+// way through memory.
+constexpr uint32_t kSideM[4] = {256, 128, 64, 64}, kSideN[4] = {256, 128, 64, 32};
 struct Plan {
-    int tile;         // 0: 256 x 256, 1: 128 x 128, 2: 64 x 64
+    int tile;  // of kSideM x kSideN; the last one with both operands by columns only
     uint32_t splits;
-    bool deep;        // 64 x 64, one workgroup a compute unit: more tiles ahead
 };
 
-inline Plan plan_product(uint64_t m, uint64_t n, uint64_t k, bool parts) {
-    constexpr double kStep[3] = {1.65, 1.07, 0.62}, kStart[3] = {6, 4, 3};
-    constexpr uint64_t kSlots[3] = {256, 512, 768};
+// whole: no parts of k, and both operands by columns (the logits).
+inline Plan plan_product(uint64_t m, uint64_t n, uint64_t k, bool whole) {
+    constexpr double kStep[4] = {1.65, 1.07, 0.62, 0.5}, kAlone[4] = {1.65, 0.8, 0.4, 0.3};
+    constexpr double kStart[4] = {6, 4, 3, 3};
+    constexpr uint64_t kSlots[4] = {256, 512, 768, 768};
     const uint64_t kt = std::max<uint64_t>((k + 63) / 64, 1);
-    Plan best = {2, 1, false};
+    Plan best = {2, 1};
     double least = 1e300;
-    for (int t = 0; t < 3; ++t)
+    for (int t = 0; t < (whole ? 4 : 3); ++t)
         for (const uint64_t p : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64}) {
-            if (p > 1 && (!parts || kt / p < 4))
+            if (p > 1 && (whole || kt / p < 4))
                 break;
-            const uint64_t groups = tiles(m, n, t) * p, steps = (kt + p - 1) / p;
+            const uint64_t groups = ((m + kSideM[t] - 1) / kSideM[t])
+                                    * ((n + kSideN[t] - 1) / kSideN[t]) * p;
+            const double step = groups <= 256 ? kAlone[t] : kStep[t];
             double us = (double)((groups + kSlots[t] - 1) / kSlots[t])
-                        * (kStart[t] + (double)steps * kStep[t]);
+                        * (kStart[t] + (double)((kt + p - 1) / p) * step);
             if (p > 1)
                 us += 5 + (double)(p * m * n) * 8e-6 / 4;
             if (us < least) {
                 least = us;
-                best = {t, (uint32_t)p, t == 2 && groups <= 256 && steps >= 8};
+                best = {t, (uint32_t)p};
             }
         }
     return best;

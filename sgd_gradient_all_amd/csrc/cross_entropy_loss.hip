@@ -11,6 +11,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "cross_entropy_internal.h"
 
@@ -184,17 +185,20 @@ __global__ __launch_bounds__(256) void pack_few_kernel(RowsArgs a, Rows r) {
     __shared__ uint32_t before[4], have[4];
     __shared__ float tops[4];
     const uint32_t i = blockIdx.x, lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
-    auto target = [&](uint32_t at) {
-        return at < a.m && (!a.lse || factor_of(a, at) != 0.0f) ? a.target[at] : -1;
+    auto target = [&](uint32_t at, float &g) {
+        const bool in = at < a.m;
+        const long long t = a.target[in ? at : 0];
+        g = a.lse ? fabsf(factor_of(a, in ? at : 0)) : 1.0f;
+        return in && g != 0.0f ? t : -1;
     };
-    const long long own = target(i);
+    float own_g;
+    const long long own = target(i, own_g);
     long long t[kPackFew / 256];
     float g[kPackFew / 256];
 #pragma unroll
     for (uint32_t j = 0; j < kPackFew / 256; ++j) {
-        const uint32_t at = j * 256 + threadIdx.x;
-        t[j] = target(at);
-        g[j] = a.lse && at < a.m && t[j] >= 0 ? fabsf(factor_of(a, at)) : 0.0f;
+        t[j] = target(j * 256 + threadIdx.x, g[j]);
+        g[j] = t[j] >= 0 ? g[j] : 0.0f;
     }
     uint32_t b = 0, h = 0;
     float top = 0.0f;
@@ -258,6 +262,7 @@ namespace {
 
 struct LossArgs {
     Rows rows;
+    const long long *target;  // few rows, which are not packed: the caller's; or null
     Operand x, w;
     const void *bias;       // T or null
     uint64_t m, n;
@@ -381,6 +386,18 @@ __global__ __launch_bounds__(Core::THREADS) void loss_kernel(LossArgs a) {
         a.all[at] = all;
 }
 
+// Few rows' kernels take x as it lies where its rows start on 16 bytes: what a row
+// without a target gives is dropped at the end.
+__device__ __forceinline__ uint32_t rows_of(const LossArgs &a) {
+    return a.target ? (uint32_t)a.m : a.rows.head->count;
+}
+__device__ __forceinline__ uint32_t target_of(const LossArgs &a, uint32_t m) {
+    if (!a.target)
+        return (uint32_t)a.rows.target[m];
+    const long long t = a.target[m];
+    return t < 0 ? ~0u : (uint64_t)t >= a.n ? (uint32_t)kBadTarget : (uint32_t)t;
+}
+
 // Up to 64 rows: the weights are read once and bound the time, or the few steps of
 // each sum do.  A workgroup takes a run of groups of 16 columns; for each, its 8
 // waves take an eighth of k, straight into the matrix instruction's registers,
@@ -394,7 +411,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_kernel(LossArgs a, uint32_
     using E = typename T::E;
     constexpr uint32_t TURNS = R < 4 ? 2 : 1;  // as many as 64 KB of LDS hold
     __shared__ f32x4 parts[TURNS][kFewWaves][R * 16][5];  // [wave][m][n / 4], a chunk of padding
-    const uint32_t count = a.rows.head->count;
+    const uint32_t count = rows_of(a);
     const uint32_t l = threadIdx.x & 63u, wave = threadIdx.x >> 6, r = l & 15u, g = l >> 4;
     if (!count)
         return;
@@ -416,7 +433,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_kernel(LossArgs a, uint32_
 #pragma unroll
     for (uint32_t i = 0; i < EACH; ++i) {
         const uint32_t m = m0 + i * 32;
-        want[i] = m < count ? (uint32_t)a.rows.target[m] : ~0u;
+        want[i] = m < count ? target_of(a, m) : ~0u;
         top[i] = kNone;
         sum[i] = all[i] = 0.0f;
     }
@@ -539,14 +556,14 @@ __global__ __launch_bounds__(256) void vector_kernel(LossArgs a) {
     constexpr uint32_t U = 4, WAVES = 4;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     __shared__ float tops[WAVES][M], sums[WAVES][M], alls[WAVES][M];
-    const uint32_t count = a.rows.head->count, k = (uint32_t)a.x.k;  // a multiple of 8
+    const uint32_t count = rows_of(a), k = (uint32_t)a.x.k;  // a multiple of 8
     const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
     if (!count)
         return;
     u32x4 *xs = (u32x4 *)lds;
     for (uint32_t c = threadIdx.x; c < M * k / 8; c += 256) {
         const uint32_t m = c / (k / 8);
-        xs[c] = m < count ? ((const u32x4 *)(a.rows.x + m * a.rows.ld))[c - m * (k / 8)]
+        xs[c] = m < count ? ((const u32x4 *)(a.x.plane[0] + m * a.x.ld))[c - m * (k / 8)]
                           : u32x4{0, 0, 0, 0};
     }
     __syncthreads();
@@ -556,7 +573,7 @@ __global__ __launch_bounds__(256) void vector_kernel(LossArgs a) {
     for (int m = 0; m < M; ++m) {
         top[m] = kNone;
         sum[m] = all[m] = 0.0f;
-        want[m] = (uint32_t)m < count ? (uint32_t)a.rows.target[m] : ~0u;
+        want[m] = (uint32_t)m < count ? target_of(a, m) : ~0u;
     }
     const uint64_t r0 = a.n * blockIdx.x / gridDim.x, r1 = a.n * (blockIdx.x + 1) / gridDim.x;
     for (uint64_t row = r0 + wave * U; row < r1; row += WAVES * U) {
@@ -565,21 +582,32 @@ __global__ __launch_bounds__(256) void vector_kernel(LossArgs a) {
 #pragma unroll
         for (uint32_t u = 0; u < U; ++u)
             w[u] = (const u32x4 *)(a.w.plane[0] + (row + u < r1 ? row + u : r1 - 1) * a.w.ld);
-        uint32_t c = lane;
-#pragma unroll 2
-        for (; c < k / 8; c += 64) {
-            u32x4 v[U];
+        // all of a batch's loads before its products: 16 KB of w a wave in flight
+        auto batch = [&](auto size, uint32_t c) {
+            constexpr uint32_t P = decltype(size)::value;
+            u32x4 v[P][U];
 #pragma unroll
-            for (uint32_t u = 0; u < U; ++u)
-                v[u] = __builtin_nontemporal_load(w[u] + c);
-#pragma unroll
-            for (int m = 0; m < M; ++m) {
-                const u32x4 x = xs[m * (k / 8) + c];
+            for (uint32_t p = 0; p < P; ++p)
 #pragma unroll
                 for (uint32_t u = 0; u < U; ++u)
-                    acc[u][m] = dot8<E>(v[u], x, acc[u][m]);
-            }
-        }
+                    v[p][u] = __builtin_nontemporal_load(w[u] + c + p * 64);
+            if (P > 1)
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (uint32_t p = 0; p < P; ++p)
+#pragma unroll
+                for (int m = 0; m < M; ++m) {
+                    const u32x4 x = xs[m * (k / 8) + c + p * 64];
+#pragma unroll
+                    for (uint32_t u = 0; u < U; ++u)
+                        acc[u][m] = dot8<E>(v[p][u], x, acc[u][m]);
+                }
+        };
+        uint32_t c0 = 0;
+        for (; c0 + 256 <= k / 8; c0 += 256)
+            batch(std::integral_constant<uint32_t, 4>(), c0 + lane);
+        for (; c0 + lane < k / 8; c0 += 64)
+            batch(std::integral_constant<uint32_t, 1>(), c0 + lane);
 #pragma unroll
         for (uint32_t u = 0; u < U; ++u) {
             const uint64_t n = row + u;
@@ -633,7 +661,7 @@ __global__ __launch_bounds__(256) void join_kernel(LossArgs a, uint32_t parts, f
     __shared__ float tops[256], sums[256], alls[256];
     const uint32_t lane = threadIdx.x / R, in = threadIdx.x % R;
     const uint64_t row = (uint64_t)blockIdx.x * R + in;
-    const uint32_t count = a.rows.head->count;
+    const uint32_t count = rows_of(a);
     if ((uint64_t)blockIdx.x * R >= count)
         return;
     float top = kNone, sum = 0.0f, all = 0.0f;
@@ -666,10 +694,15 @@ __global__ __launch_bounds__(256) void join_kernel(LossArgs a, uint32_t parts, f
     }
     if (lane || row >= count)
         return;
-    const uint32_t to = a.rows.row[row];
+    const uint32_t to = a.target ? (uint32_t)row : a.rows.row[row];
+    const uint32_t t = target_of(a, (uint32_t)row);
+    if (t == ~0u) {
+        loss[to] = lse[to] = 0.0f;
+        return;
+    }
     const float l = top + logf(sum);
     float v = __builtin_nanf("");
-    if (a.rows.target[row] != kBadTarget) {
+    if (t != (uint32_t)kBadTarget) {
         v = l - (1.0f - smoothing) * a.rows.at[row];
         if (a.all)
             v -= smoothing * (all / (float)a.n);
@@ -696,8 +729,8 @@ struct LossCut {
 
 LossCut loss_cut(uint64_t m, uint64_t n, uint64_t k) {
     LossCut c;
-    c.plan = plan_product(m, n, k, false);
-    c.parts = (uint32_t)((n + kTile[c.plan.tile] - 1) / kTile[c.plan.tile]);
+    c.plan = plan_product(m, n, k, true);
+    c.parts = (uint32_t)((n + kSideN[c.plan.tile] - 1) / kSideN[c.plan.tile]);
     if (few(m))
         c.parts = std::max(c.parts, kFewGroups);
     // whole tiles
@@ -743,9 +776,9 @@ int launch_loss(LossArgs a, const Plan &p, uint32_t first, uint32_t last, hipStr
         return go(gemm::Core<T, 256, 256, 2, 4, 64, 2, false, false, STAGED, !STAGED>());
     if (p.tile == 1)
         return go(gemm::Core<T, 128, 128, 2, 2, 64, 2, false, false, STAGED>());
-    if (p.deep && !STAGED)
-        return go(gemm::Core<T, 64, 64, 2, 2, 64, kDeep, false, false, STAGED>());
-    return go(gemm::Core<T, 64, 64, 2, 2, 64, 3, false, false, STAGED>());
+    if (p.tile == 2)
+        return go(gemm::Core<T, 64, 64, 2, 2, 64, 3, false, false, STAGED>());
+    return go(gemm::Core<T, 64, 32, 4, 1, 64, 3, false, false, STAGED>());
 }
 
 template <class T>
@@ -762,10 +795,18 @@ int loss(const ddl_ce_args *c, void *ws, hipStream_t s) {
     r.target = c->target;
     r.loss = c->loss;
     r.lse_out = c->lse;
-    int rc = pack_rows(r, a.rows, s);
+    // straight to LDS or registers where every row starts on 16 bytes
+    const bool direct = c->k % 8 == 0 && aligned16(c->w, c->ldw, 2);
+    int rc = DDL_OK;
+    if (direct && few(c->m) && aligned16(c->x, c->ldx, 2)) {
+        a.target = c->target;
+        a.x = operand(c->x, c->ldx, c->m, c->k);
+    } else {
+        rc = pack_rows(r, a.rows, s);
+        a.x = operand(a.rows.x, a.rows.ld, c->m, c->k);
+    }
     if (rc)
         return rc;
-    a.x = operand(a.rows.x, a.rows.ld, c->m, c->k);
     a.w = operand(c->w, c->ldw, c->n, c->k);
     a.bias = c->bias;
     a.m = c->m;
@@ -773,10 +814,8 @@ int loss(const ddl_ce_args *c, void *ws, hipStream_t s) {
     if (c->smoothing == 0.0)
         a.all = nullptr;
     const LossCut t = loss_cut(c->m, c->n, c->k);
-    const uint32_t side = kTile[t.plan.tile];
+    const uint32_t side = kSideN[t.plan.tile];
     uint32_t parts = (uint32_t)((c->n + side - 1) / side);
-    // straight to LDS or registers where every row starts on 16 bytes
-    const bool direct = c->k % 8 == 0 && aligned16(c->w, c->ldw, 2);
     const size_t m = c->m <= 2 ? c->m : 4;
     if (direct && c->m <= m && m * c->k * 2 <= kVectorBytes && c->k) {
         parts = (uint32_t)std::min<size_t>(kFewGroups, (c->n + 15) / 16);
