@@ -560,14 +560,15 @@ int ddl_linear_wgrad(const ddl_wgrad_args *args, void *workspace, size_t workspa
  * loss NaN.  Rows whose dloss scale is 0 count as rows without a target.
  *
  * Logits, sums and exponentials are binary32.  The gradient takes the classes
- * in pieces: it computes their logits again and holds dz of one piece in 16 bits
- * (scaled by a power of two, so that binary16 does not underflow), which
- * dx and dw in 16 bits see as an error of up to their own rounding.  dw in
+ * in pieces: it computes their logits again and holds dz of one piece in 16 bits,
+ * which dx and dw in 16 bits see as an error of up to their own rounding.  dz is
+ * held times a power of two that goes by the largest finite |dloss scale|, so
+ * that DDL_F16 keeps it down to 2^-39 of that, however the loss is scaled.  dw in
  * DDL_F32 is computed from dz as a sum of two 16-bit values: 16 significant
  * bits in DDL_BF16, 22 in DDL_F16.  db is summed before dz is rounded.
  *
- * ld*, alignment, workspace, stream, capture and errors as in the linear layer;
- * m and n and k up to 2^22, n at least 1.  Results are the same from call to
+ * ld*, alignment, overlaps, workspace (never 0 bytes), stream, capture and errors as
+ * in the linear layer; m, n and k up to 2^22, n at least 1.  Results are the same from call to
  * call. */
 enum { DDL_CE_FORWARD = 0, DDL_CE_GRAD = 1 };
 

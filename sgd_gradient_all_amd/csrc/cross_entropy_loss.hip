@@ -49,6 +49,11 @@ __device__ __forceinline__ void write_row(const RowsArgs &a, const Rows &r, uint
     }
 }
 
+// |g| where it counts for the factor: an infinite one would take the others' digits.
+__device__ __forceinline__ float size_of(float g) {
+    return fabsf(g) < __builtin_huge_valf() ? fabsf(g) : 0.0f;
+}
+
 // Gradient: factor is the power of two that takes the largest |dloss scale| to
 // [2^14, 2^15).  dz = factor dloss scale (p - wanted) is held in 16 bits, and
 // |p - wanted| <= 1: so binary16 keeps 11 bits of every p down to 2^-29 of the
@@ -56,7 +61,7 @@ __device__ __forceinline__ void write_row(const RowsArgs &a, const Rows &r, uint
 __device__ __forceinline__ void write_head(const Rows &r, uint32_t count, float top) {
     int e = 0;
     if (top > 0.0f) {
-        e = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127;  // infinity: 128
+        e = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127;
         e = 14 - (e < -86 ? -86 : e > 114 ? 114 : e);
     }
     r.head->count = count;
@@ -111,7 +116,7 @@ __global__ __launch_bounds__(1024) void rows_kernel(RowsArgs a, Rows r) {
                                     + (uint32_t)__popcll(have[j] & ((1ull << lane) - 1));
                 write_row(a, r, at, i, t[j]);
                 if (a.lse)
-                    top = fmaxf(top, fabsf(g[j]));
+                    top = fmaxf(top, size_of(g[j]));
             } else if (i < a.m && a.loss) {
                 a.loss[i] = 0.0f;
                 a.lse_out[i] = 0.0f;
@@ -188,7 +193,7 @@ __global__ __launch_bounds__(256) void pack_few_kernel(RowsArgs a, Rows r) {
     auto target = [&](uint32_t at, float &g) {
         const bool in = at < a.m;
         const long long t = a.target[in ? at : 0];
-        g = a.lse ? fabsf(factor_of(a, in ? at : 0)) : 1.0f;
+        g = a.lse ? factor_of(a, in ? at : 0) : 1.0f;
         return in && g != 0.0f ? t : -1;
     };
     float own_g;
@@ -198,7 +203,7 @@ __global__ __launch_bounds__(256) void pack_few_kernel(RowsArgs a, Rows r) {
 #pragma unroll
     for (uint32_t j = 0; j < kPackFew / 256; ++j) {
         t[j] = target(j * 256 + threadIdx.x, g[j]);
-        g[j] = t[j] >= 0 ? g[j] : 0.0f;
+        g[j] = t[j] >= 0 ? size_of(g[j]) : 0.0f;
     }
     uint32_t b = 0, h = 0;
     float top = 0.0f;

@@ -8,8 +8,8 @@ through a tile (16 terms in a lane, 2 exchanges, 4 waves), then at most 64 parts
 in a lane and 8 exchanges, with up to 6 F32 more where the largest logit changes:
 under 600 F32 of the sum, which is what the log-sum-exp is off by.
 
-dz is off by p (slack + (4 + 3 |z - lse|) F32) + 4 F32 of its terms, and rounded
-to 16 bits: u(t), and in binary16, whose subnormal numbers end at 2^-25 where
+dz is off by p (slack + (4 + 3 |z - lse|) F32) + 4 F32 of its terms, by 2^-126 more
+where p is below binary32's normal numbers (2^x is 0 there), and rounded to 16 bits: u(t), and in binary16, whose subnormal numbers end at 2^-25 where
 the largest factor is at least 2^14, 2^-39 of that factor.  As a pair: u(t)^2.
 """
 import math
@@ -130,7 +130,7 @@ def check_grad(x, w, b, target, lse, dloss, scale, a, dx, dw, db, dw0=None, db0=
     hot.scatter_(1, target.clamp(min=0)[:, None], 1.0)
     raw = p - (1 - a) * hot - a / n
     off = p * (slack + (4 + 3 * (z - lse.double()[:, None]).abs()) * F32) \
-        + 4 * F32 * (p + hot + a / n)
+        + 4 * F32 * (p + hot + a / n) + 2.0 ** -126
     row = torch.where(have, g, 0.0)[:, None]
     dz = torch.where(have[:, None], raw * row, 0.0)
     doff = torch.where(have[:, None], off * row.abs() + raw.abs() * gslack[:, None], 0.0)
@@ -191,3 +191,343 @@ def test_gradient(m, n, k, dtype):
                                accumulate=add, workspace=workspace("grad", m, n, k))
         check_grad(x, w, b, target, lse, dloss, scale, a, dx, dw, db, dw0 if add else None,
                    db0 if add else None)
+
+
+def run_grad(x, w, b, target, lse, dloss=None, scale=1.0, a=0.0, out=torch.float32, stream=None):
+    (m, k), n = x.shape, w.shape[0]
+    dx = torch.full_like(x, 9.0)
+    dw = torch.full((n, k), 9.0, device="cuda", dtype=out)
+    db = torch.full((n,), 9.0, device="cuda", dtype=out)
+    ddl.cross_entropy_grad(x, w, target, lse, dloss=dloss, scale=scale, dx=dx, dw=dw, db=db, bias=b,
+                           smoothing=a, workspace=workspace("grad", m, n, k), stream=stream)
+    return dx, dw, db
+
+
+# (m, n, k) that take every tile of the loss and of the three products of the
+# gradient, sums in parts and whole, short last k tiles, odd rows packed, and
+# several pieces; which is which is checked on the host
+LARGE = [(3000, 6000, 136), (4096, 4096, 256), (1500, 2100, 200), (700, 500, 1096),
+         (520, 264, 4104), (2047, 9001, 1023), (1023, 12003, 111), (300, 30000, 72),
+         (8199, 20001, 72), (8192, 33000, 63), (70, 3000, 640), (5000, 40, 130),
+         (4000, 3000, 4096), (4090, 2001, 4000)]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("m,n,k", LARGE)
+def test_large(m, n, k, dtype):
+    t = T[dtype]
+    for a, bias, ignored, out, first in ((0.1, True, 0.1, "f32", 0), (0.0, False, 0.5, dtype, 1)):
+        print(f"large {m} {n} {k} {dtype} {a} {bias} {ignored} {out} {first}", flush=True)
+        x, w, b, target = inputs(m, n, k, dtype, ignored, bias)
+        off = strided(w, 0, first)  # off 16 bytes: rows go through registers
+        loss, lse = run_loss(x, off, b, target, a)
+        check_loss(x, w, b, target, a, loss, lse)
+        dx, dw, db = run_grad(x, off, b, target, lse, scale=1 / m, a=a, out=T[out])
+        lse = torch.where(target >= 0, lse, torch.zeros_like(lse))
+        check_grad(x, w, b, target, lse, None, 1 / m, a, dx, dw, db)
+
+
+@pytest.mark.parametrize("m", [1, 2, 3, 4, 5, 16, 17, 33, 64])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_few_rows(m, dtype):
+    """Every kernel for few rows, whole batches of loads and what is left of them."""
+    for n, k in ((37, 8), (5000, 2048), (3001, 2056), (2050, 4616), (100, 16392)):
+        print(f"few {m} {n} {k} {dtype}", flush=True)
+        x, w, b, target = inputs(m, n, k, dtype, 0.3, True)
+        target[0] = n - 1
+        check_loss(x, w, b, target, 0.1, *run_loss(x, w, b, target, 0.1))
+        check_loss(x, w, None, target, 0.0, *run_loss(x, w, None, target, 0.0))
+
+
+@pytest.mark.parametrize("m,n,k", [(40, 300, 72), (700, 1000, 264), (2000, 3000, 100)])
+def test_rows_without_a_target_reach_nothing(m, n, k):
+    """NaN and infinities in them, and in the factors and log-sum-exps of theirs."""
+    t = torch.bfloat16
+    x, w, b, target = inputs(m, n, k, "bf16", 0.4)
+    gone = target < 0
+    bad = torch.tensor([float("nan"), float("inf"), -float("inf")], device="cuda")
+    dirty = x.clone()
+    dirty[gone] = bad[torch.arange(int(gone.sum()), device="cuda") % 3].to(t)[:, None]
+    loss, lse = run_loss(dirty, w, b, target)
+    check_loss(x, w, b, target, 0.0, loss, lse)
+    dloss = torch.rand(m, generator=gen(3), device="cuda") + 0.5
+    dirty_lse, dirty_dloss = lse.clone(), dloss.clone()
+    dirty_lse[gone], dirty_dloss[gone] = float("nan"), float("nan")
+    got = run_grad(dirty, w, b, target, dirty_lse, dloss=dirty_dloss, scale=1 / m)
+    check_grad(x, w, b, target, lse, dloss, 1 / m, 0.0, *got)
+    # a factor of 0 is no target either
+    kept = torch.where(gone, torch.ones_like(target), target)
+    zero = torch.where(gone, torch.zeros_like(dloss), dloss)
+    again = run_grad(dirty, w, b, kept, dirty_lse, dloss=zero, scale=1 / m)
+    assert all(torch.equal(p, q) for p, q in zip(got, again))
+
+
+@pytest.mark.parametrize("m", [5, 100, 2000])
+def test_no_row_has_a_target(m):
+    x, w, b, target = inputs(m, 70, 40, "f16", 2.0)
+    loss, lse = run_loss(x, w, b, target)
+    assert (loss == 0).all() and (lse == 0).all()
+    dx, dw, db = run_grad(x, w, b, target, lse)
+    assert (dx == 0).all() and (dw == 0).all() and (db == 0).all()
+    dw.fill_(3.0)
+    ddl.cross_entropy_grad(x, w, target, lse, dw=dw, accumulate=True,
+                           workspace=workspace("grad", m, 70, 40))
+    assert (dw == 3).all()
+
+
+def test_no_rows():
+    e = lambda *s: torch.empty(*s, device="cuda")  # noqa: E731
+    w, b = normal(gen(1), 6, 8, dtype=torch.float16), normal(gen(2), 6, dtype=torch.float16)
+    x, target = e(0, 8).half(), e(0).long()
+    ddl.cross_entropy(x, w, target, e(0), e(0), bias=b)
+    for out in (torch.float32, torch.float16):
+        dw, db = torch.ones(6, 8, device="cuda", dtype=out), torch.ones(6, device="cuda", dtype=out)
+        ddl.cross_entropy_grad(x, w, target, e(0), dw=dw, db=db, bias=b, accumulate=True)
+        assert (dw == 1).all() and (db == 1).all()
+        ddl.cross_entropy_grad(x, w, target, e(0), dw=dw, db=db, bias=b)
+        assert (dw == 0).all() and (db == 0).all()
+
+
+@pytest.mark.parametrize("m,n,k", [(3, 90, 64), (30, 90, 64), (300, 700, 72)])
+def test_masked_classes(m, n, k):
+    """A bias of -inf: no share of the sum, no gradient; and rows of nothing else."""
+    x, w, b, target = inputs(m, n, k, "bf16", 0.0)
+    b[n // 2:] = -float("inf")
+    target %= n // 2
+    loss, lse = run_loss(x, w, b, target)
+    check_loss(x, w[:n // 2], b[:n // 2], target, 0.0, loss, lse)
+    dx, dw, db = run_grad(x, w, b, target, lse, scale=1 / m)
+    assert (dw[n // 2:] == 0).all() and (db[n // 2:] == 0).all()
+    check_grad(x, w[:n // 2], b[:n // 2], target, lse, None, 1 / m, 0.0, dx, dw[:n // 2],
+               db[:n // 2])
+    loss, lse = run_loss(x, w, torch.full_like(b, -float("inf")), target)
+    assert (lse == -float("inf")).all() and torch.isnan(loss).all()
+    target.fill_(n - 1)  # a masked class is wanted
+    loss, lse = run_loss(x, w, b, target)
+    assert (loss == float("inf")).all() and torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("m", [4, 50, 500])
+def test_targets_out_of_range_are_loud(m):
+    n, k = 130, 72
+    x, w, b, target = inputs(m, n, k, "f16", 0.0)
+    target[1], target[2] = n, 1 << 40
+    loss, lse = run_loss(x, w, b, target)
+    fine = torch.ones(m, device="cuda", dtype=torch.bool)
+    fine[1:3] = False
+    assert torch.isnan(loss[~fine]).all() and torch.isfinite(lse).all()
+    assert torch.isfinite(loss[fine]).all()
+    dx, dw, db = run_grad(x, w, b, target, lse)
+    assert torch.isnan(dx[~fine]).all() and torch.isfinite(dx[fine]).all()
+    assert torch.isnan(dw).all() and torch.isnan(db).all()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_a_row_with_an_infinite_factor_spoils_no_other_dx(dtype):
+    m, n, k = 60, 200, 72
+    x, w, b, target = inputs(m, n, k, dtype, 0.0)
+    _, lse = run_loss(x, w, b, target)
+    dloss = torch.full((m,), 0.25, device="cuda")
+    clean = run_grad(x, w, b, target, lse, dloss=dloss)[0]
+    dloss[7] = float("inf")
+    dx = run_grad(x, w, b, target, lse, dloss=dloss)[0]
+    fine = torch.arange(m, device="cuda") != 7
+    assert torch.equal(dx[fine], clean[fine]) and not torch.isfinite(dx[7]).any()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_scales_of_the_loss(dtype):
+    """A power of two in the loss is the same power in binary32 gradients, bit for
+    bit, up to scales whose 16-bit values would not be numbers."""
+    m, n, k = 100, 3000, 136
+    x, w, b, target = inputs(m, n, k, dtype, 0.2)
+    _, lse = run_loss(x, w, b, target)
+    _, dw, db = run_grad(x, w, b, target, lse, scale=1 / 64)
+    for e in (-60, -20, 10, 40):
+        _, dw2, db2 = run_grad(x, w, b, target, lse, scale=2.0 ** e / 64)
+        assert torch.equal(dw2, dw * 2.0 ** e) and torch.equal(db2, db * 2.0 ** e)
+    check_grad(x, w, b, target, torch.where(target >= 0, lse, torch.zeros_like(lse)), None, 1 / 64,
+               0.0, None, dw, db)
+
+
+def test_large_logits():
+    """Logits of thousands, of both signs, as sums of exponentials meet them."""
+    for m in (2, 20, 200):
+        x, w, b, target = inputs(m, 500, 64, "bf16", 0.0)
+        x = x * 400
+        loss, lse = run_loss(x, w, b, target)
+        check_loss(x, w, b, target, 0.0, loss, lse)
+        dx, dw, db = run_grad(x, w, b, target, lse, scale=1 / m)
+        check_grad(x, w, b, target, lse, None, 1 / m, 0.0, dx, dw, db)
+
+
+@pytest.mark.parametrize("a", [0.0, 0.2])
+def test_gradient_against_differences(a):
+    """The three gradients against central differences of the loss in 64 bits."""
+    m, n, k, t = 24, 50, 40, torch.bfloat16
+    x, w, b, target = inputs(m, n, k, "bf16", 0.2)
+    dloss = torch.rand(m, generator=gen(5), device="cuda") + 0.1
+    have = target >= 0
+    _, lse = run_loss(x, w, b, target, a)
+    dx, dw, db = run_grad(x, w, b, target, lse, dloss=dloss, a=a)
+
+    def total(x, w, b):
+        z = x @ w.t().contiguous() + b
+        at = z.gather(1, target.clamp(min=0)[:, None])[:, 0]
+        loss = torch.logsumexp(z, 1) - (1 - a) * at - a * z.mean(1)
+        return float((loss * dloss.double())[have].sum())
+
+    args = [v.double() for v in (x, w, b)]
+    h = 1e-4
+    z = args[0] @ args[1].t().contiguous() + args[2]
+    p = torch.exp(z - lse.double()[:, None])
+    p.scatter_add_(1, target.clamp(min=0)[:, None], torch.ones_like(p[:, :1]))
+    # of dz: a rounding to bfloat16 (dx alone; pairs and db keep 2^-16), log-sum-exps
+    # that are 600 F32 off, and differences' h^2 and 1e-16 / h of sums of 24 losses
+    size = torch.where(have, dloss, torch.zeros_like(dloss)).double()[:, None] * (p + a / n)
+    for which, got, at in ((0, dx, (3, 7)), (0, dx, (20, 39)), (1, dw, (0, 0)), (1, dw, (49, 11)),
+                           (2, db, (0,)), (2, db, (33,))):
+        ends = []
+        for s in (h, -h):
+            moved = [v.clone() for v in args]
+            moved[which][at] += s
+            ends.append(total(*moved))
+        want = (ends[0] - ends[1]) / (2 * h)
+        terms = (float((size[at[0]] * args[1][:, at[1]].abs()).sum()) if which == 0 else
+                 float((size[:, at[0]] * args[0][:, at[1]].abs()).sum()) if which == 1 else
+                 float(size[:, at[0]].sum()))
+        rounding = u(t) * (terms + abs(want)) if which == 0 else 2.0 ** -15 * terms
+        assert abs(float(got[at]) - want) <= rounding + 1000 * F32 * terms + 1e-7 * (1 + terms)
+
+
+def test_outputs_stay_inside_their_rows():
+    m, n, k, t = 300, 270, 100, torch.float16
+    x, w, b, target = inputs(m, n, k, "f16", 0.3)
+    _, lse = run_loss(x, w, b, target)
+    for out in (torch.float32, t):
+        dx = strided(torch.zeros(m, k, device="cuda", dtype=t), 5, 1)
+        dw = strided(torch.zeros(n, k, device="cuda", dtype=out), 3, 1)
+        db = torch.full((n + 2,), 5.0, device="cuda", dtype=out)
+        ddl.cross_entropy_grad(x, w, target, lse, dx=dx, dw=dw, db=db[1:-1], bias=b,
+                               workspace=workspace("grad", m, n, k))
+        for v, pad in ((dx, 5), (dw, 3)):
+            flat = v.as_strided((v.shape[0], k + pad), (k + pad, 1), v.storage_offset())
+            assert torch.isnan(flat[:, k:]).all() and torch.isfinite(v).all()
+        assert float(db[0]) == 5 and float(db[-1]) == 5
+
+
+@pytest.mark.parametrize("m,n,k", [(60, 700, 264), (1500, 3000, 200)])
+def test_same_bits_on_another_stream_and_in_a_graph(m, n, k):
+    """The loss, then the gradient from its log-sum-exps: eagerly, on another stream,
+    and captured and replayed with eager work between."""
+    x, w, b, target = inputs(m, n, k, "bf16", 0.3)
+    ws = torch.empty(max(ddl.cross_entropy_workspace(o, m, n, k) for o in ("forward", "grad")),
+                     device="cuda", dtype=torch.uint8)
+
+    def fresh():
+        return [torch.zeros(m, device="cuda"), torch.zeros(m, device="cuda"),
+                torch.zeros_like(x), torch.zeros(n, k, device="cuda"),
+                torch.zeros(n, device="cuda")]
+
+    def step(o, stream):
+        ddl.cross_entropy(x, w, target, o[0], o[1], bias=b, smoothing=0.1, workspace=ws,
+                          stream=stream)
+        ddl.cross_entropy_grad(x, w, target, o[1], scale=1 / m, dx=o[2], dw=o[3], db=o[4], bias=b,
+                               smoothing=0.1, accumulate=True, workspace=ws, stream=stream)
+
+    eager, want = fresh(), []
+    for _ in range(3):
+        step(eager, None)
+        torch.cuda.synchronize()
+        want.append([v.clone() for v in eager])
+    side, s = fresh(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for i in range(3):
+        step(side, s)
+        s.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(side, want[i]))
+    held, graph = fresh(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=s):
+        step(held, s)
+    for i in range(3):
+        target2 = target.clone()  # eager work between
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(held, want[i])), f"replay {i}"
+        assert torch.equal(target2, target)
+        (torch.randn(64, 64, device="cuda") @ torch.randn(64, 64, device="cuda")).sum().item()
+
+
+def test_classes_past_32_bits():
+    """w, dw of more than 2^32 elements: the classes at the far end."""
+    m, n, k, t = 3, (1 << 21) + 300, 2056, torch.bfloat16
+    w = torch.empty(n, k, device="cuda", dtype=t).normal_(generator=gen(8)).mul_(k ** -0.5)
+    x = normal(gen(9), m, k, dtype=t)
+    target = torch.tensor([n - 1, 5, n - 300], device="cuda")
+    print("classes past 32 bits", flush=True)
+    loss, lse = run_loss(x, w, None, target)
+    z = torch.cat([x.double() @ part.double().t().contiguous() for part in w.split(1 << 18)], 1)
+    slack = (k + 4) * F32 * float((x.double().abs().amax() * w.double().abs().amax()) * k)
+    want = torch.logsumexp(z, 1)
+    assert ((lse.double() - want).abs() <= slack + 600 * F32 + 2 * F32 * want).all()
+    at = z[torch.arange(m, device="cuda"), target]
+    assert ((loss.double() - (want - at)).abs() <= 2 * slack + 1300 * F32 + 6 * F32 * want).all()
+    dx, dw, _ = torch.empty_like(x), torch.empty(n, k, device="cuda", dtype=t), None
+    ddl.cross_entropy_grad(x, w, target, lse, dx=dx, dw=dw, workspace=workspace("grad", m, n, k))
+    p = torch.exp(z - lse.double()[:, None])
+    p[torch.arange(m, device="cuda"), target] -= 1
+    for rows in (slice(n - 300, n), slice(0, 10), slice(n // 2, n // 2 + 10)):
+        want = p[:, rows].t().contiguous() @ x.double()
+        off = p[:, rows].abs().t().contiguous() @ x.double().abs()
+        assert ((dw[rows].double() - want).abs() <= (2 * u(t) + 2 * slack + 64 * F32) * off
+                + u(t) * want.abs() + 1e-30).all()
+    want = sum(p[:, i:i + (1 << 18)] @ w[i:i + (1 << 18)].double() for i in range(0, n, 1 << 18))
+    off = sum(p[:, i:i + (1 << 18)].abs() @ w[i:i + (1 << 18)].double().abs()
+              for i in range(0, n, 1 << 18))
+    assert ((dx.double() - want).abs() <= (u(t) + 2 * slack + n * F32) * off
+            + 2 * u(t) * want.abs()).all()
+
+
+def test_rows_past_32_bits():
+    """x and dx of more than 2^32 elements: the rows at the far end."""
+    m, n, k, t = (1 << 21) + 100, 64, 2056, torch.bfloat16
+    x = torch.empty(m, k, device="cuda", dtype=t).normal_(generator=gen(10))
+    w = normal(gen(11), n, k, sigma=k ** -0.5, dtype=t)
+    target = torch.full((m,), -1, device="cuda")
+    some = torch.cat([torch.arange(50, device="cuda"), torch.arange(m - 300, m, device="cuda")])
+    target[some] = some % n
+    print("rows past 32 bits", flush=True)
+    loss, lse = run_loss(x, w, None, target)
+    check_loss(x[some], w, None, target[some], 0.0, loss[some], lse[some])
+    assert int((loss != 0).sum()) == some.numel()
+    dx = torch.full_like(x, 9.0)
+    dw = torch.empty(n, k, device="cuda")
+    ddl.cross_entropy_grad(x, w, target, lse, scale=1 / 64, dx=dx, dw=dw,
+                           workspace=workspace("grad", m, n, k))
+    check_grad(x[some], w, None, target[some], lse[some], None, 1 / 64, 0.0, dx[some], dw, None)
+    assert int((dx != 0).any(1).sum()) <= some.numel()
+
+
+def test_an_older_error_is_not_the_calls():
+    import ctypes
+    hip, p = ddl.lib(), ctypes.c_void_p()
+    x, w, b, target = inputs(20, 40, 64, "f16")
+    lse = torch.zeros(20, device="cuda")
+    h = ddl.AdamW8([(0, 64)])
+    st = [torch.zeros(64, device="cuda", dtype=t) for t in (torch.int8, torch.uint8)] \
+        + [torch.zeros(1, device="cuda") for _ in range(2)]
+    v = [torch.zeros(64, device="cuda") for _ in range(2)]
+    loss, dx, dw = torch.zeros(20, device="cuda"), torch.empty_like(x), torch.empty_like(w)
+    fw, gw = workspace("forward", 20, 40, 64), workspace("grad", 20, 40, 64)
+    torch.cuda.synchronize()
+    calls = [lambda: ddl.cross_entropy(x, w, target, loss, lse, bias=b, workspace=fw),
+             lambda: ddl.cross_entropy_grad(x, w, target, lse, dx=dx, dw=dw, bias=b, workspace=gw),
+             lambda: h.step(v[0], *st, [v[1]], lr=0.1), lambda: h.values(*st, *v)]
+    try:
+        for call in calls:
+            assert hip.hipMalloc(ctypes.byref(p), ctypes.c_size_t(1 << 60)) != 0
+            call()
+    finally:
+        hip.hipGetLastError()
+        torch.cuda.synchronize()
