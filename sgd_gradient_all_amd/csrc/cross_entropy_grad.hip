@@ -329,10 +329,10 @@ __device__ __forceinline__ uint32_t parts_of(const GradArgs &g, uint32_t tm, uin
 
 // DX: C = dz w over the piece's classes.  Otherwise C = dz^T x over the packed
 // rows, PAIR: with dz in two parts, the low ones first.
+// id: of the workgroup among the product's.
 template <class T, class Core, bool DX, bool PAIR>
-__global__ __launch_bounds__(Core::THREADS) void grad_kernel(GradArgs g) {
+__device__ __forceinline__ void grad_tile(GradArgs &g, uint32_t id, uint8_t *lds) {
     using E = typename T::E;
-    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const uint32_t count = g.head->count;
     if (DX) {
         g.a.rows = g.o.m = count;
@@ -343,11 +343,11 @@ __global__ __launch_bounds__(Core::THREADS) void grad_kernel(GradArgs g) {
     const uint32_t kt = (uint32_t)((g.a.k + Core::BK - 1) / Core::BK);
     const uint32_t all = PAIR ? 2 * kt : kt;
     const uint32_t splits = DX ? parts_of(g, tm, kt) : g.splits;
-    if (blockIdx.x >= tm * g.tn * splits)
+    if (id >= tm * g.tn * splits)
         return;
-    const uint32_t s = blockIdx.x / (tm * g.tn);
+    const uint32_t s = id / (tm * g.tn);
     uint32_t ti, tj;
-    tile_of(blockIdx.x - s * tm * g.tn, tm, g.tn, ti, tj);
+    tile_of(id - s * tm * g.tn, tm, g.tn, ti, tj);
     g.a.row0 = ti * Core::BM;
     g.b.row0 = tj * Core::BN;
     const float inverse = g.head->inverse;
@@ -384,6 +384,25 @@ __global__ __launch_bounds__(Core::THREADS) void grad_kernel(GradArgs g) {
                 out8<E, DX, false>(g.o, inverse, m0 + mi, n0 + ni, v, f);
             });
     }
+}
+
+template <class T, class Core, bool DX, bool PAIR>
+__global__ __launch_bounds__(Core::THREADS) void grad_kernel(GradArgs g) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    grad_tile<T, Core, DX, PAIR>(g, blockIdx.x, lds);
+}
+
+// Both products of a small piece in one launch, which leaves fewer compute units
+// idle than one after the other (512 x 1000 x 2048 in binary16: 40 to 33 us for
+// the whole gradient): the first `split` workgroups are dx's.
+template <class T, class X, class W, bool PAIR>
+__global__ __launch_bounds__(X::THREADS) void both_kernel(GradArgs x, GradArgs w, uint32_t split) {
+    static_assert(X::THREADS == W::THREADS, "one kind of workgroup");
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    if (blockIdx.x < split)
+        grad_tile<T, X, true, false>(x, blockIdx.x, lds);
+    else
+        grad_tile<T, W, false, PAIR>(w, blockIdx.x - split, lds);
 }
 
 // The sums of the parts, in their order; 8 columns a lane.
@@ -489,29 +508,62 @@ int launch_dz(DzArgs &a, const Plan &p, uint64_t m, hipStream_t s) {
     return go(gemm::Core<T, 64, 32, 4, 1, 64, 3, false, false, STAGED>());
 }
 
+// The workgroups of a product of m rows by tiles of Core, into g.
+template <class Core>
+uint32_t lay_out(GradArgs &g, const Plan &c, uint64_t m) {
+    g.tile_rows = (uint32_t)((m + Core::BM - 1) / Core::BM);
+    g.tn = (g.o.n + Core::BN - 1) / Core::BN;
+    g.splits = c.splits;
+    return g.tile_rows * g.tn * g.splits;
+}
+
+template <class T, bool DX>
+int launch_join(const GradArgs &g, uint64_t m, uint32_t side, hipStream_t s) {
+    if (g.splits == 1)
+        return DDL_OK;
+    const uint64_t lanes = (uint64_t)(g.o.n + 7) / 8 * m;
+    return launch(grad_join<T, DX>, dim3((uint32_t)((lanes + 255) / 256)), dim3(256), 0, s, g,
+                  side);
+}
+
 template <class T, bool DX, bool PAIR, bool STAGED>
 int launch_grad(GradArgs &g, const Plan &c, uint64_t m, hipStream_t s) {
     auto go = [&](auto core) {
         using Core = decltype(core);
         constexpr auto kernel = grad_kernel<T, Core, DX, PAIR>;
-        const uint32_t tm = (uint32_t)((m + Core::BM - 1) / Core::BM);
-        g.tn = (g.o.n + Core::BN - 1) / Core::BN;
-        g.tile_rows = tm;
-        g.splits = c.splits;
+        const uint32_t groups = lay_out<Core>(g, c, m);
         int rc = allow_lds(kernel, Core::LDS);
-        rc = rc ? rc
-                : launch(kernel, dim3(tm * g.tn * g.splits), dim3(Core::THREADS), Core::LDS, s, g);
-        if (rc || g.splits == 1)
-            return rc;
-        const uint64_t lanes = (uint64_t)(g.o.n + 7) / 8 * m;
-        return launch(grad_join<T, DX>, dim3((uint32_t)((lanes + 255) / 256)), dim3(256), 0, s, g,
-                      (uint32_t)Core::BM);
+        rc = rc ? rc : launch(kernel, dim3(groups), dim3(Core::THREADS), Core::LDS, s, g);
+        return rc ? rc : launch_join<T, DX>(g, m, Core::BM, s);
     };
     if (c.tile == 0)
         return go(gemm::Core<T, 256, 256, 2, 4, 64, 2, !DX, true, STAGED, !STAGED>());
     if (c.tile == 1)
         return go(gemm::Core<T, 128, 128, 2, 2, 64, 2, !DX, true, STAGED>());
     return go(gemm::Core<T, 64, 64, 2, 2, 64, 3, !DX, true, STAGED>());
+}
+
+// dx by 64 x 64 tiles beside dw by 64 x 64 or 128 x 128, whole sums: the parts'
+// memory is one product's.
+bool go_together(const Plan &x, const Plan &w) {
+    return x.tile == 2 && w.tile >= 1 && w.splits == 1;
+}
+
+template <class T, bool PAIR>
+int launch_both(GradArgs &x, GradArgs &w, const Plan &px, const Plan &pw, uint64_t m, uint64_t n,
+                hipStream_t s) {
+    using X = gemm::Core<T, 64, 64, 2, 2, 64, 3, false, true, false>;
+    auto go = [&](auto core) {
+        using W = decltype(core);
+        constexpr auto kernel = both_kernel<T, X, W, PAIR>;
+        constexpr int lds = X::LDS > W::LDS ? X::LDS : W::LDS;
+        const uint32_t split = lay_out<X>(x, px, m), more = lay_out<W>(w, pw, n);
+        int rc = allow_lds(kernel, lds);
+        rc = rc ? rc : launch(kernel, dim3(split + more), dim3(X::THREADS), lds, s, x, w, split);
+        return rc ? rc : launch_join<T, true>(x, m, X::BM, s);
+    };
+    return pw.tile == 1 ? go(gemm::Core<T, 128, 128, 2, 2, 64, 2, true, true, false>())
+                        : go(gemm::Core<T, 64, 64, 2, 2, 64, 3, true, true, false>());
 }
 
 template <class T>
@@ -577,29 +629,26 @@ int gradient(const ddl_ce_grad_args *c, void *ws, hipStream_t s) {
                 rc = launch(db_kernel<E>, dim3((uint32_t)((have + 255) / 256)), dim3(256), 0, s,
                             b.rows.head, db);
         }
-        if (!rc && c->dx && k) {
-            GradArgs g = {};
-            g.head = b.rows.head;
-            g.a = operand(b.dz[0], d.ld, m, have);
+        GradArgs x = {}, g = {};
+        const Plan px = plan_product(m, k, have, false), pw = plan_product(have, k, m, false);
+        if (c->dx && k) {
+            x.head = b.rows.head;
+            x.a = operand(b.dz[0], d.ld, m, have);
             // a packed w's columns past k are zeros
-            g.b = operand(w, ldw, pack ? ldw : k, have);
-            g.partial = b.partial;
-            g.part_ld = b.rows.ld;
-            g.o.n = (uint32_t)k;
-            g.o.c = c->dx;
-            g.o.ld = c->lddx;
-            g.o.sum = b.sum;
-            g.o.sum_ld = b.rows.ld;
-            g.o.row = b.rows.row;
-            g.o.read = first > 0;
-            g.o.write = first + have < n;
-            g.o.vec = k % 8 == 0 && aligned16(c->dx, c->lddx, 2);
-            const Plan t = plan_product(m, k, have, false);
-            rc = direct ? launch_grad<T, true, false, false>(g, t, m, s)
-                        : launch_grad<T, true, false, true>(g, t, m, s);
+            x.b = operand(w, ldw, pack ? ldw : k, have);
+            x.partial = b.partial;
+            x.part_ld = b.rows.ld;
+            x.o.n = (uint32_t)k;
+            x.o.c = c->dx;
+            x.o.ld = c->lddx;
+            x.o.sum = b.sum;
+            x.o.sum_ld = b.rows.ld;
+            x.o.row = b.rows.row;
+            x.o.read = first > 0;
+            x.o.write = first + have < n;
+            x.o.vec = k % 8 == 0 && aligned16(c->dx, c->lddx, 2);
         }
-        if (!rc && c->dw && k) {
-            GradArgs g = {};
+        if (c->dw && k) {
             g.head = b.rows.head;
             g.db = db;
             g.a = operand(b.dz[0], d.ld, d.ld, 0);
@@ -614,10 +663,20 @@ int gradient(const ddl_ce_grad_args *c, void *ws, hipStream_t s) {
             g.o.f32 = f32;
             g.o.add = c->accumulate;
             g.o.vec = k % 8 == 0 && aligned16(g.o.c, c->lddw, esz);
-            const Plan t = plan_product(have, k, m, false);
-            rc = f32 ? launch_grad<T, false, true, false>(g, t, have, s)
-                     : launch_grad<T, false, false, false>(g, t, have, s);
         }
+        if (rc || !k)
+            continue;
+        if (c->dx && c->dw && direct && go_together(px, pw)) {
+            rc = f32 ? launch_both<T, true>(x, g, px, pw, m, have, s)
+                     : launch_both<T, false>(x, g, px, pw, m, have, s);
+            continue;
+        }
+        if (c->dx)
+            rc = direct ? launch_grad<T, true, false, false>(x, px, m, s)
+                        : launch_grad<T, true, false, true>(x, px, m, s);
+        if (!rc && c->dw)
+            rc = f32 ? launch_grad<T, false, true, false>(g, pw, have, s)
+                     : launch_grad<T, false, false, false>(g, pw, have, s);
     }
     return rc;
 }

@@ -126,8 +126,8 @@ struct Plan {
 
 // whole: no parts of k, and both operands by columns (the logits).
 inline Plan plan_product(uint64_t m, uint64_t n, uint64_t k, bool whole) {
-    constexpr double kStep[4] = {1.65, 1.07, 0.62, 0.5}, kAlone[4] = {1.65, 0.8, 0.4, 0.3};
-    constexpr double kStart[4] = {6, 4, 3, 3};
+    constexpr double kStep[4] = {1.65, 1.07, 0.62, 0.5}, kAlone[4] = {1.65, 0.95, 0.4, 0.3};
+    constexpr double kStart[4] = {6, 4, 2.5, 2.5};
     constexpr uint64_t kSlots[4] = {256, 512, 768, 768};
     const uint64_t kt = std::max<uint64_t>((k + 63) / 64, 1);
     Plan best = {2, 1};
@@ -142,7 +142,7 @@ inline Plan plan_product(uint64_t m, uint64_t n, uint64_t k, bool whole) {
             double us = (double)((groups + kSlots[t] - 1) / kSlots[t])
                         * (kStart[t] + (double)((kt + p - 1) / p) * step);
             if (p > 1)
-                us += 5 + (double)(p * m * n) * 8e-6 / 4;
+                us += 4 + (double)(p * m * n) * 8e-6 / 8;
             if (us < least) {
                 least = us;
                 best = {t, (uint32_t)p};

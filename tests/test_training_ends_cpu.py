@@ -286,7 +286,9 @@ def test_gpu_tests_reach_every_kernel(host_driver):
     names = [n for s in sizes for n in launched(host_driver, *s)]
     seen = set()
     for n in names:
-        if "Core" in n:
+        if "both_kernel" in n:  # dx by 64 x 64 beside dw
+            seen.add(("both", int(re.findall(r"Li(\d+)ELi\d+ELi2ELi2E", n)[-1])))
+        elif "Core" in n:
             staged = re.search(r"Lb\dELb\dELb(\d)E", n).group(1)
             what = "loss" if "loss_kernel" in n else "dz" if "dz_kernel" in n else \
                 "dx" if "ELb1ELb0EEE" in n else "dw"
@@ -294,6 +296,7 @@ def test_gpu_tests_reach_every_kernel(host_driver):
     for side in ((256, 256), (128, 128), (64, 64)):
         for what in ("loss", "dz", "dx", "dw"):
             assert (what, side, False) in seen, (what, side)
+    assert ("both", 64) in seen and ("both", 128) in seen
     assert ("loss", (64, 32), False) in seen and ("dz", (64, 32), False) in seen
     for part in ("rows_kernel", "11pack_kernel", "pack_few_kernel", "matrix_kernel", "grad_join",
                  "join_kernelILi1E", "join_kernelILi32E"):
@@ -321,4 +324,5 @@ def test_each_class_is_taken_once(host_driver):
         names = host_driver("ce", 1, m, n, k, ddl.DDL_BF16, ddl.DDL_F32).split()
         pieces = max(1, -(-n // max(256, (128 << 20) // m // 256 * 256)))
         assert sum("dz_kernel" in x for x in names) == pieces
-        assert sum("grad_kernel" in x for x in names) == 2 * pieces
+        assert sum("grad_kernel" in x for x in names) + 2 * sum(
+            "both_kernel" in x for x in names) == 2 * pieces
