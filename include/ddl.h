@@ -560,12 +560,16 @@ int ddl_linear_wgrad(const ddl_wgrad_args *args, void *workspace, size_t workspa
  * loss NaN.  Rows whose dloss scale is 0 count as rows without a target.
  *
  * Logits, sums and exponentials are binary32.  The gradient takes the classes
- * in pieces: it computes their logits again and holds dz of one piece in 16 bits,
- * which dx and dw in 16 bits see as an error of up to their own rounding.  dz is
- * held times a power of two that goes by the largest finite |dloss scale|, so
- * that DDL_F16 keeps it down to 2^-39 of that, however the loss is scaled.  dw in
- * DDL_F32 is computed from dz as a sum of two 16-bit values: 16 significant
- * bits in DDL_BF16, 22 in DDL_F16.  db is summed before dz is rounded.
+ * in pieces: it computes their logits again and holds dz of one piece, to 11
+ * significant bits at least for dx and dw in 16 bits (which so are as near as a
+ * result rounded once, but for a few percent) and for dw in DDL_F32 to 22 in
+ * DDL_F16 and to 16 or, with many rows, 22 in DDL_BF16.  dz is held times a power
+ * of two that goes by the largest finite |dloss scale|, so that it keeps them down
+ * to 2^-29 of that, and is off by 2^-39 of it below, however the loss is scaled.
+ * With many rows DDL_BF16's x and w go as DDL_F16 times a power of two as well:
+ * what is under 2^-31 of the largest finite value of x, or of a piece of w, is
+ * off by 2^-39 of that.  lse has to be the loss's own.  db is summed before dz is
+ * rounded.
  *
  * ld*, alignment, overlaps, workspace (never 0 bytes), stream, capture and errors as
  * in the linear layer; m, n and k up to 2^22, n at least 1.  Results are the same from call to

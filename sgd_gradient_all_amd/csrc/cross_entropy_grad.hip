@@ -9,16 +9,26 @@
 // from there.  So the memory held is a piece's dz, whatever the number of
 // classes, and the price is one product more than with all logits kept.
 //
-// dz's rounding is the one that results see besides their own: 16-bit outputs
-// are up to sqrt(2) of their own rounding off.  Binary32 dw would lose half of
-// its digits that way, so for it dz is held as a sum of two 16-bit values (16
-// significant bits in bfloat16, 22 in binary16) and its product takes two
-// passes.  db is summed from dz before it is rounded.
+// dz's rounding to 16 bits would be one that results see besides their own: 16-bit
+// ones had 1.5 times the error of a result rounded once, and binary32 dw would lose
+// half of its digits.  So dz is held more exactly:
+//  - as a sum of two values of the operands' type (16 significant bits in bfloat16,
+//    22 in binary16): its products take two passes.  512 x 1000 x 2048 in binary16
+//    takes 42 us so, with dz rounded 31;
+//  - with bfloat16 operands, where it is faster (widens), as binary16, against x
+//    and w as binary16 too: their 8 bits fit it exactly down to 2^-31 of the largest
+//    value, which a power of two takes to the top of its range, and smaller ones to
+//    2^-39 of it.  One pass then holds dz to 11 bits, and binary32 dw takes two for
+//    22.  Finding the largest value and
+//    converting takes 4% of 8192 x 131072 x 4096: 21.3 ms, 34.4 in pairs, and 20.4
+//    with dz rounded to bfloat16.
+// db is summed from dz before it is rounded.
 #include <hip/hip_runtime.h>
 #include <math.h>
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "cross_entropy_internal.h"
 
@@ -45,9 +55,11 @@ struct DzArgs {
     float *db;              // [row tile][ld]: column sums, or null
 };
 
-template <class T, class Core>
+// D: the type that dz is held in.
+template <class T, class D, class Core>
 __global__ __launch_bounds__(Core::THREADS) void dz_kernel(DzArgs a) {
     using E = typename T::E;
+    using H = typename D::E;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     constexpr uint32_t BM = Core::BM, BN = Core::BN;
     const uint32_t count = a.rows.head->count, tm = (count + BM - 1) / BM;
@@ -123,7 +135,7 @@ __global__ __launch_bounds__(Core::THREADS) void dz_kernel(DzArgs a) {
             const uint32_t m = m0 + mi, n = n0 + ni;
             if (m >= rows || n >= a.ld)
                 return;
-            store8<true>((E *)a.dz[0] + m * a.ld + n, 8, v);
+            store8<true>((H *)a.dz[0] + m * a.ld + n, 8, v);
             if (a.db)
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
@@ -131,8 +143,8 @@ __global__ __launch_bounds__(Core::THREADS) void dz_kernel(DzArgs a) {
             if (a.dz[1]) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    v[e] -= (float)(E)v[e];
-                store8<true>((E *)a.dz[1] + m * a.ld + n, 8, v);
+                    v[e] -= (float)(H)v[e];
+                store8<true>((H *)a.dz[1] + m * a.ld + n, 8, v);
             }
         });
     if (!a.db)
@@ -180,7 +192,7 @@ __device__ __forceinline__ void db_of(const DbArgs &a, const RowsHead *head, uin
 #pragma unroll 8
     for (uint32_t t = 0; t < tm; ++t)
         v += a.sums[t * a.ld + c];
-    v *= head->inverse;
+    v = ldexpf(v, -head->exponent);
     if (a.f32) {
         float *to = (float *)a.db + c;
         *to = a.add ? *to + v : v;
@@ -193,6 +205,89 @@ __device__ __forceinline__ void db_of(const DbArgs &a, const RowsHead *head, uin
 template <class E>
 __global__ __launch_bounds__(256) void db_kernel(const RowsHead *head, DbArgs a) {
     db_of<E>(a, head, blockIdx.x * 256 + threadIdx.x);
+}
+
+// ---------------------------------------------------------------------------
+// bfloat16 as binary16
+// ---------------------------------------------------------------------------
+
+constexpr uint32_t kTops = 1024;  // workgroups that look for the largest value
+
+// The largest finite |v| of a matrix, by its bits, of each workgroup's rows.
+// head: the rows are the packed ones.
+__global__ __launch_bounds__(256) void largest_kernel(const uint16_t *p, uint64_t ld,
+                                                      uint64_t rows, uint64_t cols,
+                                                      const RowsHead *head, uint32_t *tops) {
+    __shared__ uint32_t wave_top[4];
+    if (head)
+        rows = head->count;
+    uint32_t top = 0;
+    for (uint64_t r = blockIdx.x; r < rows; r += kTops)
+        for (uint64_t c = threadIdx.x * 8; c < cols; c += 256 * 8) {
+            uint16_t v[8];
+            if (c + 8 <= cols)
+                __builtin_memcpy(v, p + r * ld + c, 16);
+            else
+                for (uint32_t e = 0; e < 8; ++e)
+                    v[e] = c + e < cols ? p[r * ld + c + e] : (uint16_t)0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t x = v[e] & 0x7fffu;
+                top = max(top, x < 0x7f80u ? x : 0u);
+            }
+        }
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2)
+        top = max(top, (uint32_t)__shfl_xor((int)top, d));
+    if ((threadIdx.x & 63u) == 0)
+        wave_top[threadIdx.x >> 6] = top;
+    __syncthreads();
+    if (threadIdx.x == 0)
+        tops[blockIdx.x] = max(max(wave_top[0], wave_top[1]), max(wave_top[2], wave_top[3]));
+}
+
+// The matrix times the power of two that takes its largest value to [2^14, 2^15),
+// as binary16, rows of zeros behind it up to a multiple of 64.
+constexpr uint32_t kConvertRows = 8;  // of a workgroup
+
+__global__ __launch_bounds__(256) void convert_kernel(const uint16_t *p, uint64_t ld,
+                                                      uint64_t rows, uint64_t cols,
+                                                      const RowsHead *head, const uint32_t *tops,
+                                                      int *exponent, uint16_t *to, uint64_t ld_to) {
+    __shared__ uint32_t wave_top[4];
+    if (head)
+        rows = head->count;
+    const uint64_t r0 = (uint64_t)blockIdx.x * kConvertRows;
+    if (r0 >= up64(rows))
+        return;
+    uint32_t top = 0;
+#pragma unroll
+    for (uint32_t i = 0; i < kTops; i += 256)
+        top = max(top, tops[i + threadIdx.x]);
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2)
+        top = max(top, (uint32_t)__shfl_xor((int)top, d));
+    if ((threadIdx.x & 63u) == 0)
+        wave_top[threadIdx.x >> 6] = top;
+    __syncthreads();
+    top = max(max(wave_top[0], wave_top[1]), max(wave_top[2], wave_top[3]));
+    const int e = top ? 14 - ((int)(top >> 7) - 127) : 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0)
+        *exponent = e;
+    for (uint64_t r = r0; r < r0 + kConvertRows; ++r)
+        for (uint64_t c = threadIdx.x * 8; c < ld_to; c += 256 * 8) {
+            uint16_t v[8];
+            _Float16 h[8];
+            if (r < rows && c + 8 <= cols)
+                __builtin_memcpy(v, p + r * ld + c, 16);
+            else
+                for (uint32_t x = 0; x < 8; ++x)
+                    v[x] = r < rows && c + x < cols ? p[r * ld + c + x] : (uint16_t)0;
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+                h[x] = (_Float16)ldexpf(__builtin_bit_cast(float, (uint32_t)v[x] << 16), e);
+            __builtin_memcpy(to + r * ld_to + c, h, 16);
+        }
 }
 
 // ---------------------------------------------------------------------------
@@ -275,13 +370,17 @@ __device__ __forceinline__ Old old8(const Out &o, uint32_t m, uint32_t n) {
     return f;
 }
 
+// The product is the gradient's times 2^exponent.
 template <class E, bool DX, bool VEC>
-__device__ __forceinline__ void out8(const Out &o, float inverse, uint32_t m, uint32_t n,
+__device__ __forceinline__ void out8(const Out &o, int exponent, uint32_t m, uint32_t n,
                                      float (&v)[8], const Old &f) {
     if (m >= o.m || n >= o.n)
         return;
     const uint32_t have = o.n - n < 8 ? o.n - n : 8;
     float t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] = ldexpf(v[i], -exponent);
     if (DX) {
         if (o.read) {
             widen8<float>(f.v, t);
@@ -293,15 +392,9 @@ __device__ __forceinline__ void out8(const Out &o, float inverse, uint32_t m, ui
             store8<true>(o.sum + m * o.sum_ld + n, 8, v);
             return;
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] *= inverse;
         write8<VEC>((E *)o.c + o.row[m] * o.ld + n, have, v);
         return;
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        v[i] *= inverse;
     if (o.add) {
         if (o.f32) {
             widen8<float>(f.v, t);
@@ -328,11 +421,11 @@ __device__ __forceinline__ uint32_t parts_of(const GradArgs &g, uint32_t tm, uin
 }
 
 // DX: C = dz w over the piece's classes.  Otherwise C = dz^T x over the packed
-// rows, PAIR: with dz in two parts, the low ones first.
+// rows.  PAIR: with dz in two parts, the low ones first.  E: the type of results in
+// 16 bits.
 // id: of the workgroup among the product's.
-template <class T, class Core, bool DX, bool PAIR>
+template <class E, class Core, bool DX, bool PAIR>
 __device__ __forceinline__ void grad_tile(GradArgs &g, uint32_t id, uint8_t *lds) {
-    using E = typename T::E;
     const uint32_t count = g.head->count;
     if (DX) {
         g.a.rows = g.o.m = count;
@@ -350,7 +443,7 @@ __device__ __forceinline__ void grad_tile(GradArgs &g, uint32_t id, uint8_t *lds
     tile_of(id - s * tm * g.tn, tm, g.tn, ti, tj);
     g.a.row0 = ti * Core::BM;
     g.b.row0 = tj * Core::BN;
-    const float inverse = g.head->inverse;
+    const int exponent = g.head->exponent + (DX ? g.head->w_exponent : g.head->x_exponent);
     const uint32_t t0 = (uint32_t)((uint64_t)all * s / splits);
     const uint32_t t1 = (uint32_t)((uint64_t)all * (s + 1) / splits);
     f32x4 acc[Core::FM][Core::FN] = {};
@@ -374,41 +467,40 @@ __device__ __forceinline__ void grad_tile(GradArgs &g, uint32_t id, uint8_t *lds
             acc, lds,
             [&](uint32_t mi, uint32_t ni) { return old8<E, DX, true>(g.o, m0 + mi, n0 + ni); },
             [&](uint32_t mi, uint32_t ni, float (&v)[8], const Old &f) {
-                out8<E, DX, true>(g.o, inverse, m0 + mi, n0 + ni, v, f);
+                out8<E, DX, true>(g.o, exponent, m0 + mi, n0 + ni, v, f);
             });
     } else {
         Core::template each<false, 1>(
             acc, lds,
             [&](uint32_t mi, uint32_t ni) { return old8<E, DX, false>(g.o, m0 + mi, n0 + ni); },
             [&](uint32_t mi, uint32_t ni, float (&v)[8], const Old &f) {
-                out8<E, DX, false>(g.o, inverse, m0 + mi, n0 + ni, v, f);
+                out8<E, DX, false>(g.o, exponent, m0 + mi, n0 + ni, v, f);
             });
     }
 }
 
-template <class T, class Core, bool DX, bool PAIR>
+template <class E, class Core, bool DX, bool PAIR>
 __global__ __launch_bounds__(Core::THREADS) void grad_kernel(GradArgs g) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    grad_tile<T, Core, DX, PAIR>(g, blockIdx.x, lds);
+    grad_tile<E, Core, DX, PAIR>(g, blockIdx.x, lds);
 }
 
 // Both products of a small piece in one launch, which leaves fewer compute units
 // idle than one after the other (512 x 1000 x 2048 in binary16: 40 to 33 us for
 // the whole gradient): the first `split` workgroups are dx's.
-template <class T, class X, class W, bool PAIR>
+template <class E, class X, class W>
 __global__ __launch_bounds__(X::THREADS) void both_kernel(GradArgs x, GradArgs w, uint32_t split) {
     static_assert(X::THREADS == W::THREADS, "one kind of workgroup");
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     if (blockIdx.x < split)
-        grad_tile<T, X, true, false>(x, blockIdx.x, lds);
+        grad_tile<E, X, true, true>(x, blockIdx.x, lds);
     else
-        grad_tile<T, W, false, PAIR>(w, blockIdx.x - split, lds);
+        grad_tile<E, W, false, true>(w, blockIdx.x - split, lds);
 }
 
 // The sums of the parts, in their order; 8 columns a lane.
-template <class T, bool DX>
+template <class E, bool DX>
 __global__ __launch_bounds__(256) void grad_join(GradArgs g, uint32_t side) {
-    using E = typename T::E;
     uint32_t splits = g.splits;
     if (DX) {
         g.o.m = g.head->count;
@@ -419,7 +511,7 @@ __global__ __launch_bounds__(256) void grad_join(GradArgs g, uint32_t side) {
     if (id >= (uint64_t)groups * g.o.m)
         return;
     const uint32_t m = (uint32_t)(id / groups), n = (uint32_t)(id % groups) * 8;
-    const float inverse = g.head->inverse;
+    const int exponent = g.head->exponent + (DX ? g.head->w_exponent : g.head->x_exponent);
     const Old f = g.o.vec ? old8<E, DX, true>(g.o, m, n) : old8<E, DX, false>(g.o, m, n);
     float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll 4
@@ -433,9 +525,9 @@ __global__ __launch_bounds__(256) void grad_join(GradArgs g, uint32_t side) {
         }
     }
     if (g.o.vec)
-        out8<E, DX, true>(g.o, inverse, m, n, v, f);
+        out8<E, DX, true>(g.o, exponent, m, n, v, f);
     else
-        out8<E, DX, false>(g.o, inverse, m, n, v, f);
+        out8<E, DX, false>(g.o, exponent, m, n, v, f);
 }
 
 // ---------------------------------------------------------------------------
@@ -444,10 +536,22 @@ __global__ __launch_bounds__(256) void grad_join(GradArgs g, uint32_t side) {
 
 bool packs(uint64_t m, uint64_t k) { return k % 8 && m >= kPackGrad; }
 
+// bfloat16 operands go as binary16 where the passes that it saves, two or, with dw
+// in binary32, one, cost more than three or five launches and the pass over w, 6
+// bytes of each of its elements.  In us, in pairs and so, dw in 16 bits:
+//   512 x 5000 x 2048 105, 101;  1024 x 5000 x 2048 152, 136;
+//   256 x 65536 x 4096 776, 1027;  512 x 65536 x 4096 1267, 1257;
+// and in binary32:
+//   4096 x 1000 x 2560 182, 187;  2048 x 4096 x 4096 337, 313;
+//   512 x 65536 x 4096 1349, 1577;  1024 x 32000 x 4096 1199, 1169.
+bool widens(uint64_t m, uint64_t n, uint64_t k, uint32_t passes) {
+    return m * passes >= 1024 && (double)m * (double)n * (double)k * passes >= 2e10;
+}
+
 // Classes of a piece: as many as dz and a packed w have room for, whole tiles, but
 // all of them where they fit.
 size_t piece_columns(size_t m, size_t n, size_t k) {
-    const size_t most = packs(m, k) ? std::max(m, k) : m;
+    const size_t most = packs(m, k) || widens(m, n, k, 2) ? std::max(m, k) : m;
     const size_t fit = std::max<size_t>(kPieceElements / most / 256, 1) * 256;
     return std::min<size_t>(fit, up64(n));
 }
@@ -455,8 +559,10 @@ size_t piece_columns(size_t m, size_t n, size_t k) {
 struct Buffers {
     Rows rows;
     uint16_t *dz[2];
-    uint16_t *w;
-    float *sum;      // dx's over the pieces: [m][ld]
+    uint16_t *w;         // packed
+    uint16_t *x16, *w16; // bfloat16 as binary16
+    uint32_t *tops;
+    float *sum;          // dx's over the pieces: [m][ld]
     float *db;
     float *partial;
 };
@@ -482,20 +588,24 @@ Buffers carve_grad(Carve &c, size_t m, size_t n, size_t k) {
     b.dz[0] = c.take<uint16_t>(up64(m) * piece);
     b.dz[1] = c.take<uint16_t>(up64(m) * piece);
     b.w = c.take<uint16_t>(packs(m, k) ? piece * b.rows.ld : 0);
+    const bool wide = widens(m, n, k, 2);
+    b.x16 = c.take<uint16_t>(wide ? up64(m) * b.rows.ld : 0);
+    b.w16 = c.take<uint16_t>(wide ? up64(piece) * b.rows.ld : 0);
+    b.tops = c.take<uint32_t>(wide ? kTops : 0);
     b.sum = c.take<float>(piece < n ? m * b.rows.ld : 0);
     b.db = c.take<float>((m + 63) / 64 * piece);
     b.partial = c.take<float>(partial_floats(m, n, k, piece));
     return b;
 }
 
-template <class T, bool STAGED>
+template <class T, class D, bool STAGED>
 int launch_dz(DzArgs &a, const Plan &p, uint64_t m, hipStream_t s) {
     auto go = [&](auto core) {
         using Core = decltype(core);
         a.tn = (a.n + Core::BN - 1) / Core::BN;
-        const int rc = allow_lds(dz_kernel<T, Core>, Core::LDS);
+        const int rc = allow_lds(dz_kernel<T, D, Core>, Core::LDS);
         return rc ? rc
-                  : launch(dz_kernel<T, Core>,
+                  : launch(dz_kernel<T, D, Core>,
                            dim3((uint32_t)((m + Core::BM - 1) / Core::BM) * a.tn),
                            dim3(Core::THREADS), Core::LDS, s, a);
     };
@@ -517,24 +627,25 @@ uint32_t lay_out(GradArgs &g, const Plan &c, uint64_t m) {
     return g.tile_rows * g.tn * g.splits;
 }
 
-template <class T, bool DX>
+template <class E, bool DX>
 int launch_join(const GradArgs &g, uint64_t m, uint32_t side, hipStream_t s) {
     if (g.splits == 1)
         return DDL_OK;
     const uint64_t lanes = (uint64_t)(g.o.n + 7) / 8 * m;
-    return launch(grad_join<T, DX>, dim3((uint32_t)((lanes + 255) / 256)), dim3(256), 0, s, g,
+    return launch(grad_join<E, DX>, dim3((uint32_t)((lanes + 255) / 256)), dim3(256), 0, s, g,
                   side);
 }
 
-template <class T, bool DX, bool PAIR, bool STAGED>
+// T: the type of the operands, E: of results in 16 bits.
+template <class T, class E, bool DX, bool PAIR, bool STAGED>
 int launch_grad(GradArgs &g, const Plan &c, uint64_t m, hipStream_t s) {
     auto go = [&](auto core) {
         using Core = decltype(core);
-        constexpr auto kernel = grad_kernel<T, Core, DX, PAIR>;
+        constexpr auto kernel = grad_kernel<E, Core, DX, PAIR>;
         const uint32_t groups = lay_out<Core>(g, c, m);
         int rc = allow_lds(kernel, Core::LDS);
         rc = rc ? rc : launch(kernel, dim3(groups), dim3(Core::THREADS), Core::LDS, s, g);
-        return rc ? rc : launch_join<T, DX>(g, m, Core::BM, s);
+        return rc ? rc : launch_join<E, DX>(g, m, Core::BM, s);
     };
     if (c.tile == 0)
         return go(gemm::Core<T, 256, 256, 2, 4, 64, 2, !DX, true, STAGED, !STAGED>());
@@ -549,18 +660,19 @@ bool go_together(const Plan &x, const Plan &w) {
     return x.tile == 2 && w.tile >= 1 && w.splits == 1;
 }
 
-template <class T, bool PAIR>
+template <class T>
 int launch_both(GradArgs &x, GradArgs &w, const Plan &px, const Plan &pw, uint64_t m, uint64_t n,
                 hipStream_t s) {
+    using E = typename T::E;
     using X = gemm::Core<T, 64, 64, 2, 2, 64, 3, false, true, false>;
     auto go = [&](auto core) {
         using W = decltype(core);
-        constexpr auto kernel = both_kernel<T, X, W, PAIR>;
+        constexpr auto kernel = both_kernel<E, X, W>;
         constexpr int lds = X::LDS > W::LDS ? X::LDS : W::LDS;
         const uint32_t split = lay_out<X>(x, px, m), more = lay_out<W>(w, pw, n);
         int rc = allow_lds(kernel, lds);
         rc = rc ? rc : launch(kernel, dim3(split + more), dim3(X::THREADS), lds, s, x, w, split);
-        return rc ? rc : launch_join<T, true>(x, m, X::BM, s);
+        return rc ? rc : launch_join<E, true>(x, m, X::BM, s);
     };
     return pw.tile == 1 ? go(gemm::Core<T, 128, 128, 2, 2, 64, 2, true, true, false>())
                         : go(gemm::Core<T, 64, 64, 2, 2, 64, 3, true, true, false>());
@@ -590,7 +702,21 @@ int gradient(const ddl_ce_grad_args *c, void *ws, hipStream_t s) {
     const size_t piece = piece_columns(m, n, k);
     // straight to LDS where w's rows start on 16 bytes, or a packed piece's do
     const bool pack = packs(m, k), direct = pack || (k % 8 == 0 && aligned16(l.w, l.ldw, 2));
-    const size_t ldw = pack ? b.rows.ld : l.ldw;
+    const size_t ldw = pack ? b.rows.ld : l.ldw, ld16 = b.rows.ld;
+    const bool wide =
+        std::is_same<T, Bfloat>::value && widens(m, n, k, (c->dx ? 1 : 0) + (c->dw && !f32 ? 1 : 0));
+    // the matrix's largest value, then its binary16 form
+    auto widen = [&](const uint16_t *p, size_t ld, size_t rows, const RowsHead *head, int *exponent,
+                     uint16_t *to) {
+        const int fail = launch(largest_kernel, dim3(kTops), dim3(256), 0, s, p, ld, rows, k, head,
+                                b.tops);
+        const uint32_t groups = (uint32_t)(up64(rows) / kConvertRows);
+        return fail ? fail
+                    : launch(convert_kernel, dim3(groups), dim3(256), 0, s, p, ld, rows, k, head,
+                             b.tops, exponent, to, ld16);
+    };
+    if (!rc && wide && c->dw)
+        rc = widen(b.rows.x, ld16, m, b.rows.head, &b.rows.head->x_exponent, b.x16);
     for (size_t first = 0; first < n && !rc; first += piece) {
         const size_t have = std::min(piece, n - first);
         const uint16_t *w = (const uint16_t *)l.w + first * l.ldw;
@@ -610,11 +736,17 @@ int gradient(const ddl_ce_grad_args *c, void *ws, hipStream_t s) {
         d.smooth = (float)(l.smoothing / (double)n);
         d.wanted = (float)(1.0 - l.smoothing);
         d.dz[0] = b.dz[0];
-        d.dz[1] = c->dw && f32 ? b.dz[1] : nullptr;
+        d.dz[1] = !wide || (c->dw && f32) ? b.dz[1] : nullptr;
         d.ld = (have + 63) / 64 * 64;
         d.db = c->db ? b.db : nullptr;
         const Plan p = plan_product(m, have, k, true);
-        rc = direct ? launch_dz<T, false>(d, p, m, s) : launch_dz<T, true>(d, p, m, s);
+        if (wide)
+            rc = direct ? launch_dz<T, Half, false>(d, p, m, s)
+                        : launch_dz<T, Half, true>(d, p, m, s);
+        else
+            rc = direct ? launch_dz<T, T, false>(d, p, m, s) : launch_dz<T, T, true>(d, p, m, s);
+        if (!rc && wide && c->dx)
+            rc = widen(w, ldw, have, nullptr, &b.rows.head->w_exponent, b.w16);
         const size_t esz = f32 ? 4 : 2;
         DbArgs db = {};
         if (c->db) {
@@ -634,8 +766,13 @@ int gradient(const ddl_ce_grad_args *c, void *ws, hipStream_t s) {
         if (c->dx && k) {
             x.head = b.rows.head;
             x.a = operand(b.dz[0], d.ld, m, have);
+            x.a.plane[1] = b.dz[1];
             // a packed w's columns past k are zeros
             x.b = operand(w, ldw, pack ? ldw : k, have);
+            if (wide) {  // so are its rows past the piece, and dz's columns
+                x.a.k = up64(have);
+                x.b = operand(b.w16, ld16, ld16, up64(have));
+            }
             x.partial = b.partial;
             x.part_ld = b.rows.ld;
             x.o.n = (uint32_t)k;
@@ -653,7 +790,7 @@ int gradient(const ddl_ce_grad_args *c, void *ws, hipStream_t s) {
             g.db = db;
             g.a = operand(b.dz[0], d.ld, d.ld, 0);
             g.a.plane[1] = b.dz[1];
-            g.b = operand(b.rows.x, b.rows.ld, b.rows.ld, 0);
+            g.b = operand(wide ? b.x16 : b.rows.x, ld16, ld16, 0);
             g.partial = b.partial;
             g.part_ld = b.rows.ld;
             g.o.m = (uint32_t)have;
@@ -666,17 +803,25 @@ int gradient(const ddl_ce_grad_args *c, void *ws, hipStream_t s) {
         }
         if (rc || !k)
             continue;
+        if constexpr (std::is_same<T, Bfloat>::value) {
+            if (wide) {
+                if (c->dx)
+                    rc = launch_grad<Half, E, true, false, false>(x, px, m, s);
+                if (!rc && c->dw)
+                    rc = f32 ? launch_grad<Half, E, false, true, false>(g, pw, have, s)
+                             : launch_grad<Half, E, false, false, false>(g, pw, have, s);
+                continue;
+            }
+        }
         if (c->dx && c->dw && direct && go_together(px, pw)) {
-            rc = f32 ? launch_both<T, true>(x, g, px, pw, m, have, s)
-                     : launch_both<T, false>(x, g, px, pw, m, have, s);
+            rc = launch_both<T>(x, g, px, pw, m, have, s);
             continue;
         }
         if (c->dx)
-            rc = direct ? launch_grad<T, true, false, false>(x, px, m, s)
-                        : launch_grad<T, true, false, true>(x, px, m, s);
+            rc = direct ? launch_grad<T, E, true, true, false>(x, px, m, s)
+                        : launch_grad<T, E, true, true, true>(x, px, m, s);
         if (!rc && c->dw)
-            rc = f32 ? launch_grad<T, false, true, false>(g, pw, have, s)
-                     : launch_grad<T, false, false, false>(g, pw, have, s);
+            rc = launch_grad<T, E, false, true, false>(g, pw, have, s);
     }
     return rc;
 }

@@ -41,8 +41,10 @@ __device__ __forceinline__ void load4(const E *p, uint32_t have, float (&out)[4]
 // What the rows kernel counts.
 struct RowsHead {
     uint32_t count;  // rows with a target
-    float factor;    // a power of two that dz is held times (see rows_kernel)
-    float inverse;
+    float factor;    // a power of two that dz is held times (see write_head)
+    int exponent;    // its exponent
+    // those of x and of the piece of w, as the products with dz take them
+    int x_exponent, w_exponent;
 };
 
 // The packed rows, on the device.

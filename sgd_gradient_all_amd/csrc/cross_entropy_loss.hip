@@ -66,7 +66,8 @@ __device__ __forceinline__ void write_head(const Rows &r, uint32_t count, float 
     }
     r.head->count = count;
     r.head->factor = ldexpf(1.0f, e);
-    r.head->inverse = ldexpf(1.0f, -e);
+    r.head->exponent = e;
+    r.head->x_exponent = r.head->w_exponent = 0;
 }
 
 // Packs the indices of the rows with a target, in their order: one workgroup,

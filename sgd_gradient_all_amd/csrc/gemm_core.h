@@ -121,6 +121,14 @@ __device__ __forceinline__ void load16_to_lds(const uint8_t *p, uint32_t lds) {
                  : "m0");
 }
 #pragma clang diagnostic pop
+// A base of copies, which the wave shares, in scalar registers: the compiler may
+// have computed it in the others.
+__device__ __forceinline__ const uint8_t *scalar(const uint8_t *p) {
+    const uint64_t v = (uint64_t)p;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+    return (const uint8_t *)((uint64_t)hi << 32 | lo);
+}
 // Waits until at most N of the wave's copies to LDS are in flight and its own
 // LDS accesses are done, then for the workgroup's other waves.
 template <int N>
@@ -299,7 +307,8 @@ struct Core {
         auto base = [&](bool is_a, uint32_t t) {
             const uint32_t pass = !pairs || t >= 2 * pairs ? 2 : t < pairs ? 0 : 1;
             const uint64_t k0 = (uint64_t)(t - pass * pairs) * BK;
-            return Base{is_a ? sa.base(a, pass == 1, k0) : sb.base(b, pass == 0, k0), a.k - k0};
+            return Base{scalar(is_a ? sa.base(a, pass == 1, k0) : sb.base(b, pass == 0, k0)),
+                        a.k - k0};
         };
         uint32_t a_now = lds0, a_next = lds0 + BYTES_A;
         uint32_t b_now = lds0 + 2 * BYTES_A, b_next = b_now + BYTES_B, b_third = b_next + BYTES_B;

@@ -136,10 +136,12 @@ def check_grad(x, w, b, target, lse, dloss, scale, a, dx, dw, db, dw0=None, db0=
     doff = torch.where(have[:, None], off * row.abs() + raw.abs() * gslack[:, None], 0.0)
     top = float(row.abs().max()) if m else 0.0
     floor = torch.where(have[:, None], 2.0 ** -39 * top, 0.0)
-    one = doff + u(t) * (dz.abs() + doff) + floor
+    one = doff + 2.0 ** -11 * (dz.abs() + doff) + floor
     pair = doff + u(t) ** 2 * (dz.abs() + doff) + floor
     xd, wd = x.double(), w.double()
     xd = torch.where(have[:, None], xd, 0.0)
+    # binary16 takes the largest to 2^14 or more, and is off by at most 2^-25
+    xoff, woff = (2.0 ** -39 * float(v.abs().max()) if v.numel() else 0.0 for v in (xd, wd))
 
     def near(got, want, slack):
         v = got.dtype
@@ -148,12 +150,14 @@ def check_grad(x, w, b, target, lse, dloss, scale, a, dx, dw, db, dw0=None, db0=
         assert torch.isfinite(got).all()
         assert (d <= limit).all(), f"{int((d > limit).sum())} off, {float((d - limit).max())}"
     if dx is not None:
-        near(dx, dz @ wd, one @ wd.abs() + (n + 8) * F32 * (dz.abs() @ wd.abs()))
+        near(dx, dz @ wd, one @ wd.abs() + (n + 8) * F32 * (dz.abs() @ wd.abs())
+             + woff * one.sum(1)[:, None] + woff * dz.abs().sum(1)[:, None])
         assert (dx[~have] == 0).all()
     if dw is not None:
         part = pair if dw.dtype == torch.float32 else one
         want, s = dz.t().contiguous() @ xd, dz.abs().t().contiguous() @ xd.abs()
-        limit = part.t().contiguous() @ xd.abs() + (2 * m + 8) * F32 * s
+        limit = part.t().contiguous() @ xd.abs() + (2 * m + 8) * F32 * s \
+            + xoff * (part + dz.abs()).sum(0)[:, None]
         if dw0 is not None:
             want = want + dw0.double()
             limit = limit + F32 * want.abs() * 2
@@ -164,6 +168,60 @@ def check_grad(x, w, b, target, lse, dloss, scale, a, dx, dw, db, dw0=None, db0=
             want = want + db0.double()
             limit = limit + F32 * want.abs() * 2
         near(db, want, limit)
+
+
+# bfloat16 operands in pairs, and, from 1e10 products a pass on, as binary16: both
+# outputs' types and an odd k, which is packed
+ONCE = [(65, 63, 65), (300, 520, 2056), (512, 9800, 2056), (1030, 8200, 2400), (1100, 9001, 2051)]
+
+
+@pytest.mark.parametrize("dtype,out", [("f16", "f16"), ("f16", "f32"), ("bf16", "bf16"),
+                                       ("bf16", "f32")])
+@pytest.mark.parametrize("m,n,k", ONCE)
+def test_gradient_is_rounded_once(m, n, k, dtype, out):
+    """What dz loses is small beside the result's own rounding.  Rounding to nearest
+    leaves a result of p bits an error of about 2^-p / sqrt(3) of its binade; dz's 11
+    bits against bfloat16's 8 add an eighth of it, whose square is 1 / 64, and a root
+    of 1 + 3 / 64 covers sums whose terms cancel by a factor of sqrt(3)."""
+    x, w, b, target = inputs(m, n, k, dtype, 0.2)
+    z, _ = logits(x, w, b)
+    lse = torch.logsumexp(z, 1).float()
+    dx = torch.empty(m, k, device="cuda", dtype=T[dtype])
+    dw, db = torch.empty(n, k, device="cuda", dtype=T[out]), None
+    ddl.cross_entropy_grad(x, w, target, lse, scale=1 / m, dx=dx, dw=dw, bias=b,
+                           workspace=workspace("grad", m, n, k))
+    check_grad(x, w, b, target, lse, None, 1 / m, 0.0, dx, dw, db)
+    dz = torch.exp(z - lse.double()[:, None])
+    dz[torch.arange(m), target.clamp(min=0)] -= 1
+    dz = torch.where((target >= 0)[:, None], dz / m, 0.0)
+    for got, want in ((dx, dz @ w.double()), (dw, dz.t().contiguous() @ x.double())):
+        if got.dtype == torch.float32:
+            continue  # by check_grad alone
+        off, own = ((v.double() - want).norm().item() for v in (got, want.to(got.dtype)))
+        print(f"{m} {n} {k} {dtype} {off / own}")
+        assert off <= own * (1 + 3 / 64) ** 0.5
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("large", [0, 90, -90])
+def test_gradient_of_a_wide_range(large, out):
+    """bfloat16 values past binary16's range, and far apart."""
+    m, n, k = 1030, 8200, 2400
+    x, w, b, target = inputs(m, n, k, "bf16", 0.2)
+    g = gen(9)
+    far = torch.exp2(-torch.randint(0, 30, (k,), generator=g, device="cuda").float())
+    x = (x.float() * far * 2.0 ** large).to(torch.bfloat16)
+    w = (w.float() * torch.exp2(-torch.randint(0, 30, (n, 1), generator=g, device="cuda").float())
+         * 2.0 ** -large).to(torch.bfloat16)
+    x[target < 0] = float("inf")
+    clean = torch.where((target >= 0)[:, None], x, 0)
+    z, _ = logits(clean, w, b)
+    lse = torch.logsumexp(z, 1).float()
+    dx = torch.empty(m, k, device="cuda", dtype=torch.bfloat16)
+    dw = torch.empty(n, k, device="cuda", dtype=T[out])
+    ddl.cross_entropy_grad(x, w, target, lse, scale=1 / m, dx=dx, dw=dw, bias=b,
+                           workspace=workspace("grad", m, n, k))
+    check_grad(clean, w, b, target, lse, None, 1 / m, 0.0, dx, dw, None)
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
