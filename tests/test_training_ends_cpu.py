@@ -291,7 +291,7 @@ def test_gpu_tests_reach_every_kernel(host_driver):
         elif "Core" in n:
             staged = re.search(r"Lb\dELb\dELb(\d)E", n).group(1)
             what = "loss" if "loss_kernel" in n else "dz" if "dz_kernel" in n else \
-                "dx" if "ELb1ELb0EEE" in n else "dw"
+                "dx" if re.search(r"Lb1ELb\dEEE", n) else "dw"
             seen.add((what, tile(n), staged == "1"))
     for side in ((256, 256), (128, 128), (64, 64)):
         for what in ("loss", "dz", "dx", "dw"):
@@ -307,6 +307,13 @@ def test_gpu_tests_reach_every_kernel(host_driver):
     pieces = [sum("dz_kernel" in n for n in
                   host_driver("ce", 1, *s, ddl.DDL_F16, ddl.DDL_F32).split()) for s in sizes]
     assert max(pieces) >= 2
+    # bfloat16 as binary16: dx in one pass, dw in one or in two
+    names = [n for s in gpu_tests.ONCE for out in (ddl.DDL_F32, ddl.DDL_BF16)
+             for n in host_driver("ce", 1, *s, ddl.DDL_BF16, out).split()]
+    assert any("convert_kernel" in n for n in names)
+    turned = [re.search(r"Lb(\d)ELb(\d)EEE", n).groups() for n in names
+              if "grad_kernelIDF16b" in n and "4HalfE" in n]
+    assert {("1", "0"), ("0", "0"), ("0", "1")} <= set(turned)
 
 
 @pytest.mark.parametrize("m,n,k,side", [
