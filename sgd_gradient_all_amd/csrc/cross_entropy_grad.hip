@@ -20,7 +20,7 @@
 //    value, which a power of two takes to the top of its range, and smaller ones to
 //    2^-39 of it.  One pass then holds dz to 11 bits, and binary32 dw takes two for
 //    22.  Finding the largest value and
-//    converting takes 4% of 8192 x 131072 x 4096: 21.3 ms, 34.4 in pairs, and 20.4
+//    converting takes 3% of 8192 x 131072 x 4096: 21.3 ms, 34.4 in pairs, and 20.4
 //    with dz rounded to bfloat16.
 // db is summed from dz before it is rounded.
 #include <hip/hip_runtime.h>
@@ -221,20 +221,30 @@ __global__ __launch_bounds__(256) void largest_kernel(const uint16_t *p, uint64_
     __shared__ uint32_t wave_top[4];
     if (head)
         rows = head->count;
+    constexpr uint32_t U = 4;  // rows at a time: 134 MB take 29 us, 47 with one
     uint32_t top = 0;
-    for (uint64_t r = blockIdx.x; r < rows; r += kTops)
+    for (uint64_t r = blockIdx.x; r < rows; r += U * kTops)
         for (uint64_t c = threadIdx.x * 8; c < cols; c += 256 * 8) {
-            uint16_t v[8];
-            if (c + 8 <= cols)
-                __builtin_memcpy(v, p + r * ld + c, 16);
-            else
-                for (uint32_t e = 0; e < 8; ++e)
-                    v[e] = c + e < cols ? p[r * ld + c + e] : (uint16_t)0;
+            uint16_t v[U][8];
+            if (r + (U - 1) * kTops < rows && c + 8 <= cols) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const uint32_t x = v[e] & 0x7fffu;
-                top = max(top, x < 0x7f80u ? x : 0u);
+                for (uint32_t i = 0; i < U; ++i)
+                    __builtin_memcpy(v[i], p + (r + i * kTops) * ld + c, 16);
+            } else {
+                for (uint32_t i = 0; i < U; ++i)
+#pragma unroll
+                    for (uint32_t e = 0; e < 8; ++e)
+                        v[i][e] = r + i * kTops < rows && c + e < cols
+                                      ? p[(r + i * kTops) * ld + c + e]
+                                      : (uint16_t)0;
             }
+#pragma unroll
+            for (uint32_t i = 0; i < U; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t x = v[i][e] & 0x7fffu;
+                    top = max(top, x < 0x7f80u ? x : 0u);
+                }
         }
 #pragma unroll
     for (int d = 1; d < 64; d *= 2)
@@ -486,7 +496,7 @@ __global__ __launch_bounds__(Core::THREADS) void grad_kernel(GradArgs g) {
 }
 
 // Both products of a small piece in one launch, which leaves fewer compute units
-// idle than one after the other (512 x 1000 x 2048 in binary16: 40 to 33 us for
+// idle than one after the other (512 x 1000 x 2048 in binary16: 56 to 42 us for
 // the whole gradient): the first `split` workgroups are dx's.
 template <class E, class X, class W>
 __global__ __launch_bounds__(X::THREADS) void both_kernel(GradArgs x, GradArgs w, uint32_t split) {

@@ -279,6 +279,11 @@ def launched(host_driver, m, n, k):
     return names
 
 
+def product(name):
+    """(dx and not dw, dz in two parts) of a product with dz."""
+    return re.findall(r"Lb(\d)ELb(\d)EEE", name)[-1]
+
+
 def test_gpu_tests_reach_every_kernel(host_driver):
     """Their sizes take every tile in every product, sums whole and in parts, rows
     through registers and packed, several pieces, and the kernels for few rows."""
@@ -291,7 +296,7 @@ def test_gpu_tests_reach_every_kernel(host_driver):
         elif "Core" in n:
             staged = re.search(r"Lb\dELb\dELb(\d)E", n).group(1)
             what = "loss" if "loss_kernel" in n else "dz" if "dz_kernel" in n else \
-                "dx" if re.search(r"Lb1ELb\dEEE", n) else "dw"
+                "dx" if product(n)[0] == "1" else "dw"
             seen.add((what, tile(n), staged == "1"))
     for side in ((256, 256), (128, 128), (64, 64)):
         for what in ("loss", "dz", "dx", "dw"):
@@ -311,8 +316,7 @@ def test_gpu_tests_reach_every_kernel(host_driver):
     names = [n for s in gpu_tests.ONCE for out in (ddl.DDL_F32, ddl.DDL_BF16)
              for n in host_driver("ce", 1, *s, ddl.DDL_BF16, out).split()]
     assert any("convert_kernel" in n for n in names)
-    turned = [re.search(r"Lb(\d)ELb(\d)EEE", n).groups() for n in names
-              if "grad_kernelIDF16b" in n and "4HalfE" in n]
+    turned = [product(n) for n in names if "grad_kernelIDF16b" in n and "4HalfE" in n]
     assert {("1", "0"), ("0", "0"), ("0", "1")} <= set(turned)
 
 
