@@ -562,13 +562,12 @@ int ddl_linear_wgrad(const ddl_wgrad_args *args, void *workspace, size_t workspa
  * Logits, sums and exponentials are binary32.  The gradient takes the classes
  * in pieces: it computes their logits again and holds dz of one piece, to 11
  * significant bits at least for dx and dw in 16 bits (which so are as near as a
- * result rounded once, but for a few percent) and for dw in DDL_F32 to 22 in
- * DDL_F16 and to 16 or, with many rows, 22 in DDL_BF16.  dz is held times a power
- * of two that goes by the largest finite |dloss scale|, so that it keeps them down
- * to 2^-29 of that, and is off by 2^-39 of it below, however the loss is scaled.
- * With many rows DDL_BF16's x and w go as DDL_F16 times a power of two as well:
- * what is under 2^-31 of the largest finite value of x, or of a piece of w, is
- * off by 2^-39 of that.  lse has to be the loss's own.  db is summed before dz is
+ * result rounded once, but for a few percent) and to 22 for dw in DDL_F32.  dz is
+ * held times a power of two that goes by the largest finite |dloss scale|, so that
+ * it keeps them down to 2^-29 of that, and is off by 2^-39 of it below, however the
+ * loss is scaled.  DDL_BF16's x, for dw in DDL_F32 and with many rows, and w, with
+ * many rows, go as DDL_F16 times a power of two as well: what is under 2^-31 of the
+ * largest finite value of x, or of a piece of w, is off by 2^-39 of that.  lse has to be the loss's own.  db is summed before dz is
  * rounded.
  *
  * ld*, alignment, overlaps, workspace (never 0 bytes), stream, capture and errors as

@@ -13,15 +13,16 @@
 // ones had 1.5 times the error of a result rounded once, and binary32 dw would lose
 // half of its digits.  So dz is held more exactly:
 //  - as a sum of two values of the operands' type (16 significant bits in bfloat16,
-//    22 in binary16): its products take two passes.  512 x 1000 x 2048 in binary16
-//    takes 42 us so, with dz rounded 31;
+//    22 in binary16), whose products take two passes: 512 x 1000 x 2048 in binary16
+//    42 us, with dz rounded 31.  bfloat16 with binary32 dw writes dz in two parts of
+//    binary16 beside these, which dw takes with x as binary16 (below): 22 bits for
+//    16, and 512 x 5000 x 2048 121 us for 110;
 //  - with bfloat16 operands, where it is faster (widens), as binary16, against x
 //    and w as binary16 too: their 8 bits fit it exactly down to 2^-31 of the largest
 //    value, which a power of two takes to the top of its range, and smaller ones to
 //    2^-39 of it.  One pass then holds dz to 11 bits, and binary32 dw takes two for
-//    22.  Finding the largest value and
-//    converting takes 3% of 8192 x 131072 x 4096: 21.3 ms, 34.4 in pairs, and 20.4
-//    with dz rounded to bfloat16.
+//    22.  Finding the largest value and converting takes 3% of 8192 x 131072 x 4096:
+//    21.3 ms, 34.4 in two parts of bfloat16, and 20.4 with dz rounded to it.
 // db is summed from dz before it is rounded.
 #include <hip/hip_runtime.h>
 #include <math.h>
@@ -51,9 +52,23 @@ struct DzArgs {
     uint32_t first;         // its first class
     float smooth, wanted;   // a / n, 1 - a
     uint16_t *dz[2];        // [up64(count)][ld]; the low parts: or null
+    uint16_t *half[2];      // bfloat16: dz once more, in two parts of binary16; or null
     uint64_t ld;            // n rounded up to 64; rows past count and columns past n are 0
     float *db;              // [row tile][ld]: column sums, or null
 };
+
+// 8 values as V, to the second plane (or null) what that leaves of them.
+template <class V>
+__device__ __forceinline__ void put(uint16_t *const (&to)[2], uint64_t at, const float (&v)[8]) {
+    store8<true>((V *)to[0] + at, 8, v);
+    if (!to[1])
+        return;
+    float left[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        left[e] = v[e] - (float)(V)v[e];
+    store8<true>((V *)to[1] + at, 8, left);
+}
 
 // D: the type that dz is held in.
 template <class T, class D, class Core>
@@ -135,17 +150,15 @@ __global__ __launch_bounds__(Core::THREADS) void dz_kernel(DzArgs a) {
             const uint32_t m = m0 + mi, n = n0 + ni;
             if (m >= rows || n >= a.ld)
                 return;
-            store8<true>((H *)a.dz[0] + m * a.ld + n, 8, v);
+            const uint64_t at = m * a.ld + n;
             if (a.db)
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     sums[e] += v[e];
-            if (a.dz[1]) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    v[e] -= (float)(H)v[e];
-                store8<true>((H *)a.dz[1] + m * a.ld + n, 8, v);
-            }
+            if constexpr (std::is_same<D, Bfloat>::value)
+                if (a.half[0])
+                    put<_Float16>(a.half, at, v);
+            put<H>(a.dz, at, v);
         });
     if (!a.db)
         return;
@@ -547,15 +560,15 @@ __global__ __launch_bounds__(256) void grad_join(GradArgs g, uint32_t side) {
 bool packs(uint64_t m, uint64_t k) { return k % 8 && m >= kPackGrad; }
 
 // bfloat16 operands go as binary16 where the passes that it saves, two or, with dw
-// in binary32, one, cost more than three or five launches and the pass over w, 6
-// bytes of each of its elements.  In us, in pairs and so, dw in 16 bits:
+// in binary32, one, cost more than five launches and the pass over w, 6 bytes of
+// each of its elements.  In us, in parts and so, dw in 16 bits:
 //   512 x 5000 x 2048 105, 101;  1024 x 5000 x 2048 152, 136;
 //   256 x 65536 x 4096 776, 1027;  512 x 65536 x 4096 1267, 1257;
 // and in binary32:
-//   4096 x 1000 x 2560 182, 187;  2048 x 4096 x 4096 337, 313;
-//   512 x 65536 x 4096 1349, 1577;  1024 x 32000 x 4096 1199, 1169.
+//   1024 x 5000 x 1024 143, 123;  2048 x 600 x 4096 146, 150;
+//   512 x 65536 x 4096 1460, 1577;  1024 x 32000 x 4096 1216, 1138.
 bool widens(uint64_t m, uint64_t n, uint64_t k, uint32_t passes) {
-    return m * passes >= 1024 && (double)m * (double)n * (double)k * passes >= 2e10;
+    return m * passes >= 1024 && (double)m * (double)n * (double)k >= 5e9;
 }
 
 // Classes of a piece: as many as dz and a packed w have room for, whole tiles, but
@@ -568,7 +581,7 @@ size_t piece_columns(size_t m, size_t n, size_t k) {
 
 struct Buffers {
     Rows rows;
-    uint16_t *dz[2];
+    uint16_t *dz[2], *half[2];
     uint16_t *w;         // packed
     uint16_t *x16, *w16; // bfloat16 as binary16
     uint32_t *tops;
@@ -598,10 +611,12 @@ Buffers carve_grad(Carve &c, size_t m, size_t n, size_t k) {
     b.dz[0] = c.take<uint16_t>(up64(m) * piece);
     b.dz[1] = c.take<uint16_t>(up64(m) * piece);
     b.w = c.take<uint16_t>(packs(m, k) ? piece * b.rows.ld : 0);
-    const bool wide = widens(m, n, k, 2);
-    b.x16 = c.take<uint16_t>(wide ? up64(m) * b.rows.ld : 0);
+    const bool wide = widens(m, n, k, 2), always = widens(m, n, k, 1);
+    for (uint16_t *&plane : b.half)
+        plane = c.take<uint16_t>(always ? 0 : up64(m) * piece);
+    b.x16 = c.take<uint16_t>(up64(m) * b.rows.ld);
     b.w16 = c.take<uint16_t>(wide ? up64(piece) * b.rows.ld : 0);
-    b.tops = c.take<uint32_t>(wide ? kTops : 0);
+    b.tops = c.take<uint32_t>(kTops);
     b.sum = c.take<float>(piece < n ? m * b.rows.ld : 0);
     b.db = c.take<float>((m + 63) / 64 * piece);
     b.partial = c.take<float>(partial_floats(m, n, k, piece));
@@ -670,7 +685,8 @@ bool go_together(const Plan &x, const Plan &w) {
     return x.tile == 2 && w.tile >= 1 && w.splits == 1;
 }
 
-template <class T>
+// TW: the type of dw's operands.
+template <class T, class TW>
 int launch_both(GradArgs &x, GradArgs &w, const Plan &px, const Plan &pw, uint64_t m, uint64_t n,
                 hipStream_t s) {
     using E = typename T::E;
@@ -684,8 +700,8 @@ int launch_both(GradArgs &x, GradArgs &w, const Plan &px, const Plan &pw, uint64
         rc = rc ? rc : launch(kernel, dim3(split + more), dim3(X::THREADS), lds, s, x, w, split);
         return rc ? rc : launch_join<E, true>(x, m, X::BM, s);
     };
-    return pw.tile == 1 ? go(gemm::Core<T, 128, 128, 2, 2, 64, 2, true, true, false>())
-                        : go(gemm::Core<T, 64, 64, 2, 2, 64, 3, true, true, false>());
+    return pw.tile == 1 ? go(gemm::Core<TW, 128, 128, 2, 2, 64, 2, true, true, false>())
+                        : go(gemm::Core<TW, 64, 64, 2, 2, 64, 3, true, true, false>());
 }
 
 template <class T>
@@ -713,8 +729,10 @@ int gradient(const ddl_ce_grad_args *c, void *ws, hipStream_t s) {
     // straight to LDS where w's rows start on 16 bytes, or a packed piece's do
     const bool pack = packs(m, k), direct = pack || (k % 8 == 0 && aligned16(l.w, l.ldw, 2));
     const size_t ldw = pack ? b.rows.ld : l.ldw, ld16 = b.rows.ld;
+    const bool bf = std::is_same<T, Bfloat>::value, dw32 = c->dw && f32;
     const bool wide =
-        std::is_same<T, Bfloat>::value && widens(m, n, k, (c->dx ? 1 : 0) + (c->dw && !f32 ? 1 : 0));
+        bf && (c->dx ? widens(m, n, k, c->dw && !f32 ? 2 : 1) : dw32 || widens(m, n, k, 1));
+    const bool twice = bf && !wide && dw32;  // in either type
     // the matrix's largest value, then its binary16 form
     auto widen = [&](const uint16_t *p, size_t ld, size_t rows, const RowsHead *head, int *exponent,
                      uint16_t *to) {
@@ -725,7 +743,7 @@ int gradient(const ddl_ce_grad_args *c, void *ws, hipStream_t s) {
                     : launch(convert_kernel, dim3(groups), dim3(256), 0, s, p, ld, rows, k, head,
                              b.tops, exponent, to, ld16);
     };
-    if (!rc && wide && c->dw)
+    if (!rc && (wide || twice) && c->dw && k)
         rc = widen(b.rows.x, ld16, m, b.rows.head, &b.rows.head->x_exponent, b.x16);
     for (size_t first = 0; first < n && !rc; first += piece) {
         const size_t have = std::min(piece, n - first);
@@ -746,7 +764,9 @@ int gradient(const ddl_ce_grad_args *c, void *ws, hipStream_t s) {
         d.smooth = (float)(l.smoothing / (double)n);
         d.wanted = (float)(1.0 - l.smoothing);
         d.dz[0] = b.dz[0];
-        d.dz[1] = !wide || (c->dw && f32) ? b.dz[1] : nullptr;
+        d.dz[1] = !wide || dw32 ? b.dz[1] : nullptr;
+        if (twice)
+            std::copy(b.half, b.half + 2, d.half);
         d.ld = (have + 63) / 64 * 64;
         d.db = c->db ? b.db : nullptr;
         const Plan p = plan_product(m, have, k, true);
@@ -755,7 +775,7 @@ int gradient(const ddl_ce_grad_args *c, void *ws, hipStream_t s) {
                         : launch_dz<T, Half, true>(d, p, m, s);
         else
             rc = direct ? launch_dz<T, T, false>(d, p, m, s) : launch_dz<T, T, true>(d, p, m, s);
-        if (!rc && wide && c->dx)
+        if (!rc && wide && c->dx && k)
             rc = widen(w, ldw, have, nullptr, &b.rows.head->w_exponent, b.w16);
         const size_t esz = f32 ? 4 : 2;
         DbArgs db = {};
@@ -798,9 +818,9 @@ int gradient(const ddl_ce_grad_args *c, void *ws, hipStream_t s) {
         if (c->dw && k) {
             g.head = b.rows.head;
             g.db = db;
-            g.a = operand(b.dz[0], d.ld, d.ld, 0);
-            g.a.plane[1] = b.dz[1];
-            g.b = operand(wide ? b.x16 : b.rows.x, ld16, ld16, 0);
+            g.a = operand(twice ? b.half[0] : b.dz[0], d.ld, d.ld, 0);
+            g.a.plane[1] = twice ? b.half[1] : b.dz[1];
+            g.b = operand(wide || twice ? b.x16 : b.rows.x, ld16, ld16, 0);
             g.partial = b.partial;
             g.part_ld = b.rows.ld;
             g.o.m = (uint32_t)have;
@@ -824,14 +844,19 @@ int gradient(const ddl_ce_grad_args *c, void *ws, hipStream_t s) {
             }
         }
         if (c->dx && c->dw && direct && go_together(px, pw)) {
-            rc = launch_both<T>(x, g, px, pw, m, have, s);
+            if constexpr (std::is_same<T, Bfloat>::value)
+                rc = twice ? launch_both<T, Half>(x, g, px, pw, m, have, s)
+                           : launch_both<T, T>(x, g, px, pw, m, have, s);
+            else
+                rc = launch_both<T, T>(x, g, px, pw, m, have, s);
             continue;
         }
         if (c->dx)
             rc = direct ? launch_grad<T, E, true, true, false>(x, px, m, s)
                         : launch_grad<T, E, true, true, true>(x, px, m, s);
         if (!rc && c->dw)
-            rc = launch_grad<T, E, false, true, false>(g, pw, have, s);
+            rc = twice ? launch_grad<Half, E, false, true, false>(g, pw, have, s)
+                       : launch_grad<T, E, false, true, false>(g, pw, have, s);
     }
     return rc;
 }
