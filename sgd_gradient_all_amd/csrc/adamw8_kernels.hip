@@ -14,9 +14,8 @@
 // e4m3 values for m and v's root it is 16% and 13%.
 //
 // A code is the one whose root is nearest to the value's.  Which one that is is
-// decided in binary64, where the card is as fast as in binary32: it then does
-// not depend on how sums are contracted, and the same step gives the same codes
-// everywhere.  A v over 0 keeps at least k = 1: rounded to 0 it would leave eps
+// decided in binary64, where the card is as fast as in binary32, with every term
+// rounded as the formula reads: the same step gives the same codes everywhere.  A v over 0 keeps at least k = 1: rounded to 0 it would leave eps
 // alone under an m that is not 0.
 //
 // Bound by memory: 16 bytes an element with binary16 gradients and copies, against
@@ -64,7 +63,7 @@ struct Adam8Args {
     States s;
     float *w;
     void *copy;
-    double b1, b2, c1, c2;  // c = 1 - b; b1 / 127^2 and b2 / 255^4
+    double b1, b2, c1, c2;  // c = 1 - b
     float step, root, eps;  // lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
     float keep;             // 1 - lr decay
     int vec, subnormal;     // subnormal: eps does not cover roots of subnormal v
@@ -153,13 +152,18 @@ __device__ __forceinline__ void store4(X *p, uint32_t lane, uint32_t count, cons
 struct Moments {
     double m, v;
 };
+// dm, dv: b times the block's scale.  A block's largest m is often from k = 127, as
+// b s + c g, and midway between two binary32 numbers (of 0.9 s + 0.1 g with
+// binary16 g 1 in 12): which one the scale becomes goes by the last bit
+// of binary64.  So terms are rounded one by one, as the formula reads, and the
+// share of the largest k is 1.
 __device__ __forceinline__ Moments moments(const Adam8Args &a, double dm, double dv, int8_t km,
                                            uint8_t kv, float g) {
     const double ge = (double)g;
     const float k = (float)km, h = (float)kv;
     const double h2 = (double)(h * h);
-    return {__builtin_fma(dm, (double)(k * fabsf(k)), a.c1 * ge),
-            __builtin_fma(dv, h2 * h2, a.c2 * ge * ge)};
+    return {dm * ((double)(k * fabsf(k)) * (1 / kM)) + a.c1 * ge,
+            dv * (h2 * h2 * (1 / kV)) + a.c2 * ge * ge};
 }
 
 // A wave's two blocks from element `at` on, `count` elements of them.
@@ -445,8 +449,8 @@ int ddl_adamw8_step(ddl_adamw8 h, const void *grad, int grad_dtype, signed char 
     a.s = {(int8_t *)m, v, m_scale, v_scale};
     a.w = r.w[0];
     a.copy = copy;
-    a.b1 = beta1 / kM;
-    a.b2 = beta2 / kV;
+    a.b1 = beta1;
+    a.b2 = beta2;
     a.c1 = 1 - beta1;
     a.c2 = 1 - beta2;
     a.step = (float)(lr / (1 - std::pow(beta1, (double)step)));

@@ -135,6 +135,33 @@ def test_first_steps_follow_the_definition():
                     <= slack + 4 * F32 * w0[at].abs()).all()
 
 
+@pytest.mark.parametrize("b1,b2", [(0.9, 0.95), (0.8, 0.999)])
+def test_scales_between_two_binary32_numbers(b1, b2):
+    """0.9 s + 0.1 g is often midway: it goes by the last bit of the formula's sum in
+    64 bits, term by term."""
+    blocks = 20000
+    g_, n = gen(12), blocks * B
+    h = ddl.AdamW8([(0, n)])
+    st = states(g_, n, blocks)
+    st[0][::B], st[1][::B] = 127, 255
+    gr = normal(g_, n, 1e-3, torch.float16)
+    gr[::B] = normal(g_, blocks, 1e-2, torch.float16).abs()
+    before, w = [t.clone() for t in st], torch.zeros(n, device="cuda")
+    h.step(gr, *st, [w], lr=1e-2, beta1=b1, beta2=b2, step=9)
+    g = gr.double()
+    m, v = (x.view(blocks, B) for x in (before[0].double(), before[1].double()))
+    m = b1 * (m * m.abs() / 127 ** 2 * before[2].double()[:, None]) + (1 - b1) * g.view(blocks, B)
+    v = b2 * ((v / 255) ** 4 * before[3].double()[:, None]) + (1 - b2) * (g * g).view(blocks, B)
+    top = m.abs().amax(1)
+    # the 29 bits behind binary32's: a half and at most 4 last bits of binary64 beside
+    rest = (top.view(torch.int64) & ((1 << 29) - 1)) - (1 << 28)
+    assert int((rest.abs() <= 4).sum()) > 100 or b1 != 0.9
+    assert torch.equal(st[2], top.float())
+    # (1 - b2) g g may be rounded in another order: where that is not near a half
+    rest = (v.amax(1).view(torch.int64) & ((1 << 29) - 1)) - (1 << 28)
+    assert torch.equal(st[3][rest.abs() > 4], v.amax(1).float()[rest.abs() > 4])
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 def test_not_finite_gradients_spoil_their_block_alone(bad):
     h = ddl.AdamW8([(0, 1024)])
