@@ -202,6 +202,31 @@ def test_gradient_is_rounded_once(m, n, k, dtype, out):
         assert off <= own * (1 + 3 / 64) ** 0.5
 
 
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("bf16", "f32"), ("f16", "f32")])
+@pytest.mark.parametrize("m,n,k", [(1100, 4801, 1000), (600, 9000, 1001), (130, 700, 264)])
+def test_gradients_alone_and_of_few_of_the_rows(m, n, k, dtype, out):
+    """Each output without the others, and none, one, or half of the rows with a
+    target, whatever the others hold."""
+    x, w, b, target = inputs(m, n, k, dtype, 0.0)
+    z, _ = logits(x, w, b)
+    lse = torch.logsumexp(z, 1).float()
+    ws = workspace("grad", m, n, k)
+    for rows in (0, 1, m // 2, m):
+        have = target.clone()
+        have[rows:] = -1
+        bad = x.clone()
+        bad[rows:] = float("nan")
+        for which in ((1, 1, 1), (1, 0, 0), (0, 1, 0), (0, 0, 1), (0, 1, 1)):
+            print(f"alone {m} {n} {k} {dtype} {out} {rows} {which}", flush=True)
+            dx = torch.full((m, k), 7.0, device="cuda", dtype=T[dtype]) if which[0] else None
+            dw = torch.full((n, k), 7.0, device="cuda", dtype=T[out]) if which[1] else None
+            db = torch.full((n,), 7.0, device="cuda", dtype=T[out]) if which[2] else None
+            ws.fill_(255)
+            ddl.cross_entropy_grad(bad, w, have, lse, scale=1 / m, dx=dx, dw=dw, db=db, bias=b,
+                                   workspace=ws)
+            check_grad(x, w, b, have, lse, None, 1 / m, 0.0, dx, dw, db)
+
+
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 @pytest.mark.parametrize("large", [0, 90, -90])
 def test_gradient_of_a_wide_range(large, out):
@@ -474,7 +499,7 @@ def test_outputs_stay_inside_their_rows():
         assert float(db[0]) == 5 and float(db[-1]) == 5
 
 
-@pytest.mark.parametrize("m,n,k", [(60, 700, 264), (1500, 3000, 200)])
+@pytest.mark.parametrize("m,n,k", [(60, 700, 264), (1500, 3000, 200), (1500, 4001, 1001)])
 def test_same_bits_on_another_stream_and_in_a_graph(m, n, k):
     """The loss, then the gradient from its log-sum-exps: eagerly, on another stream,
     and captured and replayed with eager work between."""
