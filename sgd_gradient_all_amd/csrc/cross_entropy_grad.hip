@@ -592,7 +592,7 @@ struct Buffers {
 
 // The largest of the products' parts, over whole pieces and the last one.
 size_t partial_floats(size_t m, size_t n, size_t k, size_t piece) {
-    const size_t kp = (k + 7) / 8 * 8, last = n - (n - 1) / piece * piece;
+    const size_t kp = up64(k), last = n - (n - 1) / piece * piece;
     size_t most = 0;
     for (const size_t have : {std::min(piece, n), last}) {
         const Plan x = plan_product(m, k, have, false), w = plan_product(have, k, m, false);
@@ -756,8 +756,9 @@ int gradient(const ddl_ce_grad_args *c, void *ws, hipStream_t s) {
         }
         DzArgs d = {};
         d.rows = b.rows;
-        d.x = operand(b.rows.x, b.rows.ld, m, k);
-        d.w = operand(w, ldw, have, k);
+        // zeros past k on both sides of packed ones
+        d.x = operand(b.rows.x, b.rows.ld, m, pack ? b.rows.ld : k);
+        d.w = operand(w, ldw, have, pack ? ldw : k);
         d.bias = l.bias ? (const uint16_t *)l.bias + first : nullptr;
         d.n = (uint32_t)have;
         d.first = (uint32_t)first;

@@ -56,7 +56,7 @@ struct Rows {
     float *g;         // gradient: the factor of the row's dz
     float *at;        // loss: the target's logit
     uint16_t *x;      // [up64(count)][ld], zeros behind the k-th element and the last row
-    uint64_t ld;      // k rounded up to 8
+    uint64_t ld;      // k rounded up to 64: rows are whole lines of 128 bytes
 };
 
 // Sums over the packed rows run over whole k tiles: rows of zeros fill the last.
@@ -83,7 +83,7 @@ inline Rows carve_rows(Carve &c, size_t m, size_t k) {
     r.lse = c.take<float>(m);
     r.g = c.take<float>(m);
     r.at = c.take<float>(m);
-    r.ld = (k + 7) / 8 * 8;
+    r.ld = up64(k);
     r.x = c.take<uint16_t>(up64(m) * r.ld);
     return r;
 }

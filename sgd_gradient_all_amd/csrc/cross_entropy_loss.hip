@@ -257,7 +257,7 @@ int pack_rows(const RowsArgs &a, const Rows &r, hipStream_t s) {
 
 int pack_matrix(const void *from, size_t ld, size_t rows, size_t k, uint16_t *to, hipStream_t s) {
     return launch(matrix_kernel, dim3((uint32_t)rows), dim3(256), 0, s, (const uint16_t *)from,
-                  (uint64_t)ld, (uint64_t)k, to, (uint64_t)((k + 7) / 8 * 8));
+                  (uint64_t)ld, (uint64_t)k, to, (uint64_t)up64(k));
 }
 
 namespace {
@@ -837,11 +837,12 @@ int loss(const ddl_ce_args *c, void *ws, hipStream_t s) {
                                  : few_kernel<T, 4>,
                     dim3(parts), dim3(kFewWaves * 64), 0, s, a, groups);
     } else if (t.piece) {
+        a.x.k = a.rows.ld;  // zeros past k on both sides
         for (size_t first = 0; first < c->n && !rc; first += t.piece) {
             const size_t have = std::min(t.piece, c->n - first);
             rc = pack_matrix((const uint16_t *)c->w + first * c->ldw, c->ldw, have, c->k, buf.w, s);
             // tiles go by their columns' places in the whole of w
-            a.w = operand(buf.w - first * a.rows.ld, a.rows.ld, c->n, c->k);
+            a.w = operand(buf.w - first * a.rows.ld, a.rows.ld, c->n, a.rows.ld);
             if (!rc)
                 rc = launch_loss<T, false>(a, t.plan, (uint32_t)(first / side),
                                            (uint32_t)((first + have + side - 1) / side), s);
