@@ -226,37 +226,55 @@ __global__ __launch_bounds__(256) void db_kernel(const RowsHead *head, DbArgs a)
 
 constexpr uint32_t kTops = 1024;  // workgroups that look for the largest value
 
+// One of up to two matrices that a launch takes, x and a piece of w: two launches
+// less for 4 us each.
+struct Widened {
+    const uint16_t *p;
+    uint64_t ld, rows;
+    const RowsHead *head;  // the rows are the packed ones; or null
+    uint32_t *tops;        // [kTops]
+    int *exponent;
+    uint16_t *to;
+    uint32_t groups;       // workgroups of convert_kernel
+};
+struct WidenArgs {
+    Widened of[2];
+    uint64_t cols, ld_to;
+};
+
 // The largest finite |v| of a matrix, by its bits, of each workgroup's rows.
-// head: the rows are the packed ones.
-__global__ __launch_bounds__(256) void largest_kernel(const uint16_t *p, uint64_t ld,
-                                                      uint64_t rows, uint64_t cols,
-                                                      const RowsHead *head, uint32_t *tops) {
+__global__ __launch_bounds__(256) void largest_kernel(WidenArgs a) {
     __shared__ uint32_t wave_top[4];
-    if (head)
-        rows = head->count;
-    constexpr uint32_t U = 4;  // rows at a time: 134 MB take 29 us, 47 with one
+    const Widened x = blockIdx.x < kTops ? a.of[0] : a.of[1];
+    const uint32_t block = blockIdx.x % kTops;
+    const uint16_t *p = x.p;
+    const uint64_t ld = x.ld, cols = a.cols, rows = x.head ? x.head->count : x.rows;
+    constexpr uint32_t U = 4;  // rows at a time: 134 MB take 26 us, 47 with one
     uint32_t top = 0;
-    for (uint64_t r = blockIdx.x; r < rows; r += U * kTops)
+    for (uint64_t r = block; r < rows; r += U * kTops)
         for (uint64_t c = threadIdx.x * 8; c < cols; c += 256 * 8) {
             uint16_t v[U][8];
-            if (r + (U - 1) * kTops < rows && c + 8 <= cols) {
+            const uint16_t *row[U];  // the last one again where there are no more
+#pragma unroll
+            for (uint32_t i = 0; i < U; ++i)
+                row[i] = p + min(r + i * kTops, rows - 1) * ld + c;
+            if (c + 8 <= cols) {
 #pragma unroll
                 for (uint32_t i = 0; i < U; ++i)
-                    __builtin_memcpy(v[i], p + (r + i * kTops) * ld + c, 16);
+                    __builtin_memcpy(v[i], row[i], 16);
             } else {
+#pragma unroll
                 for (uint32_t i = 0; i < U; ++i)
 #pragma unroll
                     for (uint32_t e = 0; e < 8; ++e)
-                        v[i][e] = r + i * kTops < rows && c + e < cols
-                                      ? p[(r + i * kTops) * ld + c + e]
-                                      : (uint16_t)0;
+                        v[i][e] = c + e < cols ? row[i][e] : (uint16_t)0;
             }
 #pragma unroll
             for (uint32_t i = 0; i < U; ++i)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const uint32_t x = v[i][e] & 0x7fffu;
-                    top = max(top, x < 0x7f80u ? x : 0u);
+                    const uint32_t u = v[i][e] & 0x7fffu;
+                    top = max(top, u < 0x7f80u ? u : 0u);
                 }
         }
 #pragma unroll
@@ -266,27 +284,29 @@ __global__ __launch_bounds__(256) void largest_kernel(const uint16_t *p, uint64_
         wave_top[threadIdx.x >> 6] = top;
     __syncthreads();
     if (threadIdx.x == 0)
-        tops[blockIdx.x] = max(max(wave_top[0], wave_top[1]), max(wave_top[2], wave_top[3]));
+        x.tops[block] = max(max(wave_top[0], wave_top[1]), max(wave_top[2], wave_top[3]));
 }
 
 // The matrix times the power of two that takes its largest value to [2^14, 2^15),
 // as binary16, rows of zeros behind it up to a multiple of 64.
 constexpr uint32_t kConvertRows = 8;  // of a workgroup
 
-__global__ __launch_bounds__(256) void convert_kernel(const uint16_t *p, uint64_t ld,
-                                                      uint64_t rows, uint64_t cols,
-                                                      const RowsHead *head, const uint32_t *tops,
-                                                      int *exponent, uint16_t *to, uint64_t ld_to) {
+__global__ __launch_bounds__(256) void convert_kernel(WidenArgs a) {
     __shared__ uint32_t wave_top[4];
-    if (head)
-        rows = head->count;
-    const uint64_t r0 = (uint64_t)blockIdx.x * kConvertRows;
+    const bool second = blockIdx.x >= a.of[0].groups;
+    const Widened m = second ? a.of[1] : a.of[0];
+    const uint32_t block = blockIdx.x - (second ? a.of[0].groups : 0u);
+    const uint16_t *p = m.p;
+    uint16_t *to = m.to;
+    const uint64_t ld = m.ld, ld_to = a.ld_to, cols = a.cols;
+    const uint64_t rows = m.head ? m.head->count : m.rows;
+    const uint64_t r0 = (uint64_t)block * kConvertRows;
     if (r0 >= up64(rows))
         return;
     uint32_t top = 0;
 #pragma unroll
     for (uint32_t i = 0; i < kTops; i += 256)
-        top = max(top, tops[i + threadIdx.x]);
+        top = max(top, m.tops[i + threadIdx.x]);
 #pragma unroll
     for (int d = 1; d < 64; d *= 2)
         top = max(top, (uint32_t)__shfl_xor((int)top, d));
@@ -295,21 +315,32 @@ __global__ __launch_bounds__(256) void convert_kernel(const uint16_t *p, uint64_
     __syncthreads();
     top = max(max(wave_top[0], wave_top[1]), max(wave_top[2], wave_top[3]));
     const int e = top ? 14 - ((int)(top >> 7) - 127) : 0;
-    if (blockIdx.x == 0 && threadIdx.x == 0)
-        *exponent = e;
-    for (uint64_t r = r0; r < r0 + kConvertRows; ++r)
+    if (block == 0 && threadIdx.x == 0)
+        *m.exponent = e;
+    constexpr uint32_t U = 4;  // rows at a time
+    for (uint64_t r = r0; r < r0 + kConvertRows; r += U)
         for (uint64_t c = threadIdx.x * 8; c < ld_to; c += 256 * 8) {
-            uint16_t v[8];
-            _Float16 h[8];
-            if (r < rows && c + 8 <= cols)
-                __builtin_memcpy(v, p + r * ld + c, 16);
-            else
-                for (uint32_t x = 0; x < 8; ++x)
-                    v[x] = r < rows && c + x < cols ? p[r * ld + c + x] : (uint16_t)0;
+            uint16_t v[U][8];
+            if (r + U <= rows && c + 8 <= cols) {
 #pragma unroll
-            for (int x = 0; x < 8; ++x)
-                h[x] = (_Float16)ldexpf(__builtin_bit_cast(float, (uint32_t)v[x] << 16), e);
-            __builtin_memcpy(to + r * ld_to + c, h, 16);
+                for (uint32_t i = 0; i < U; ++i)
+                    __builtin_memcpy(v[i], p + (r + i) * ld + c, 16);
+            } else {
+#pragma unroll
+                for (uint32_t i = 0; i < U; ++i)
+#pragma unroll
+                    for (uint32_t x = 0; x < 8; ++x)
+                        v[i][x] = r + i < rows && c + x < cols ? p[(r + i) * ld + c + x]
+                                                               : (uint16_t)0;
+            }
+#pragma unroll
+            for (uint32_t i = 0; i < U; ++i) {
+                _Float16 h[8];
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                    h[x] = (_Float16)ldexpf(__builtin_bit_cast(float, (uint32_t)v[i][x] << 16), e);
+                __builtin_memcpy(to + (r + i) * ld_to + c, h, 16);
+            }
         }
 }
 
@@ -616,7 +647,7 @@ Buffers carve_grad(Carve &c, size_t m, size_t n, size_t k) {
         plane = c.take<uint16_t>(always ? 0 : up64(m) * piece);
     b.x16 = c.take<uint16_t>(up64(m) * b.rows.ld);
     b.w16 = c.take<uint16_t>(wide ? up64(piece) * b.rows.ld : 0);
-    b.tops = c.take<uint32_t>(kTops);
+    b.tops = c.take<uint32_t>(2 * kTops);
     b.sum = c.take<float>(piece < n ? m * b.rows.ld : 0);
     b.db = c.take<float>((m + 63) / 64 * piece);
     b.partial = c.take<float>(partial_floats(m, n, k, piece));
@@ -733,18 +764,6 @@ int gradient(const ddl_ce_grad_args *c, void *ws, hipStream_t s) {
     const bool wide =
         bf && (c->dx ? widens(m, n, k, c->dw && !f32 ? 2 : 1) : dw32 || widens(m, n, k, 1));
     const bool twice = bf && !wide && dw32;  // in either type
-    // the matrix's largest value, then its binary16 form
-    auto widen = [&](const uint16_t *p, size_t ld, size_t rows, const RowsHead *head, int *exponent,
-                     uint16_t *to) {
-        const int fail = launch(largest_kernel, dim3(kTops), dim3(256), 0, s, p, ld, rows, k, head,
-                                b.tops);
-        const uint32_t groups = (uint32_t)(up64(rows) / kConvertRows);
-        return fail ? fail
-                    : launch(convert_kernel, dim3(groups), dim3(256), 0, s, p, ld, rows, k, head,
-                             b.tops, exponent, to, ld16);
-    };
-    if (!rc && (wide || twice) && c->dw && k)
-        rc = widen(b.rows.x, ld16, m, b.rows.head, &b.rows.head->x_exponent, b.x16);
     for (size_t first = 0; first < n && !rc; first += piece) {
         const size_t have = std::min(piece, n - first);
         const uint16_t *w = (const uint16_t *)l.w + first * l.ldw;
@@ -754,6 +773,28 @@ int gradient(const ddl_ce_grad_args *c, void *ws, hipStream_t s) {
                 break;
             w = b.w;
         }
+        WidenArgs v = {};
+        v.cols = k;
+        v.ld_to = ld16;
+        uint32_t count = 0;
+        auto widen = [&](const uint16_t *p, size_t ld, size_t rows, const RowsHead *head,
+                         int *exponent, uint16_t *to) {
+            v.of[count] = {p,  ld, rows, head, b.tops + count * kTops, exponent,
+                           to, (uint32_t)(up64(rows) / kConvertRows)};
+            ++count;
+        };
+        if ((wide || twice) && c->dw && k && first == 0)
+            widen(b.rows.x, ld16, m, b.rows.head, &b.rows.head->x_exponent, b.x16);
+        if (wide && c->dx && k)
+            widen(w, ldw, have, nullptr, &b.rows.head->w_exponent, b.w16);
+        if (count && !rc) {
+            rc = launch(largest_kernel, dim3(count * kTops), dim3(256), 0, s, v);
+            rc = rc ? rc
+                    : launch(convert_kernel, dim3(v.of[0].groups + v.of[1].groups), dim3(256), 0, s,
+                             v);
+        }
+        if (rc)
+            break;
         DzArgs d = {};
         d.rows = b.rows;
         // zeros past k on both sides of packed ones
@@ -776,8 +817,6 @@ int gradient(const ddl_ce_grad_args *c, void *ws, hipStream_t s) {
                         : launch_dz<T, Half, true>(d, p, m, s);
         else
             rc = direct ? launch_dz<T, T, false>(d, p, m, s) : launch_dz<T, T, true>(d, p, m, s);
-        if (!rc && wide && c->dx && k)
-            rc = widen(w, ldw, have, nullptr, &b.rows.head->w_exponent, b.w16);
         const size_t esz = f32 ? 4 : 2;
         DbArgs db = {};
         if (c->db) {
