@@ -542,14 +542,14 @@ __global__ __launch_bounds__(Core::THREADS) void grad_kernel(GradArgs g) {
 // Both products of a small piece in one launch, which leaves fewer compute units
 // idle than one after the other (512 x 1000 x 2048 in binary16: 56 to 42 us for
 // the whole gradient): the first `split` workgroups are dx's.
-template <class E, class X, class W>
+template <class E, class X, class W, bool PAIRX, bool PAIRW>
 __global__ __launch_bounds__(X::THREADS) void both_kernel(GradArgs x, GradArgs w, uint32_t split) {
     static_assert(X::THREADS == W::THREADS, "one kind of workgroup");
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     if (blockIdx.x < split)
-        grad_tile<E, X, true, true>(x, blockIdx.x, lds);
+        grad_tile<E, X, true, PAIRX>(x, blockIdx.x, lds);
     else
-        grad_tile<E, W, false, true>(w, blockIdx.x - split, lds);
+        grad_tile<E, W, false, PAIRW>(w, blockIdx.x - split, lds);
 }
 
 // The sums of the parts, in their order; 8 columns a lane.
@@ -591,15 +591,15 @@ __global__ __launch_bounds__(256) void grad_join(GradArgs g, uint32_t side) {
 bool packs(uint64_t m, uint64_t k) { return k % 8 && m >= kPackGrad; }
 
 // bfloat16 operands go as binary16 where the passes that it saves, two or, with dw
-// in binary32, one, cost more than five launches and the pass over w, 6 bytes of
-// each of its elements.  In us, in parts and so, dw in 16 bits:
-//   512 x 5000 x 2048 105, 101;  1024 x 5000 x 2048 152, 136;
+// in binary32, one, cost more than two launches and the pass over w, 6 bytes of each
+// of its elements.  In us, in parts and so, dw in 16 bits:
+//   512 x 1000 x 2048 41, 44;  700 x 1000 x 2048 56, 54;  1024 x 1000 x 2048 65, 56;
 //   256 x 65536 x 4096 776, 1027;  512 x 65536 x 4096 1267, 1257;
 // and in binary32:
-//   1024 x 5000 x 1024 143, 123;  2048 x 600 x 4096 146, 150;
+//   1024 x 1000 x 1024 51, 51;  1024 x 1000 x 2048 75, 68;  4096 x 1000 x 300 81, 69;
 //   512 x 65536 x 4096 1460, 1577;  1024 x 32000 x 4096 1216, 1138.
 bool widens(uint64_t m, uint64_t n, uint64_t k, uint32_t passes) {
-    return m * passes >= 1024 && (double)m * (double)n * (double)k >= 5e9;
+    return m * passes >= 1024 && (double)m * (double)n * (double)k >= 1.2e9;
 }
 
 // Classes of a piece: as many as dz and a packed w have room for, whole tiles, but
@@ -716,15 +716,14 @@ bool go_together(const Plan &x, const Plan &w) {
     return x.tile == 2 && w.tile >= 1 && w.splits == 1;
 }
 
-// TW: the type of dw's operands.
-template <class T, class TW>
+// TX, TW: the types of dx's and dw's operands.
+template <class E, class TX, bool PAIRX, class TW, bool PAIRW>
 int launch_both(GradArgs &x, GradArgs &w, const Plan &px, const Plan &pw, uint64_t m, uint64_t n,
                 hipStream_t s) {
-    using E = typename T::E;
-    using X = gemm::Core<T, 64, 64, 2, 2, 64, 3, false, true, false>;
+    using X = gemm::Core<TX, 64, 64, 2, 2, 64, 3, false, true, false>;
     auto go = [&](auto core) {
         using W = decltype(core);
-        constexpr auto kernel = both_kernel<E, X, W>;
+        constexpr auto kernel = both_kernel<E, X, W, PAIRX, PAIRW>;
         constexpr int lds = X::LDS > W::LDS ? X::LDS : W::LDS;
         const uint32_t split = lay_out<X>(x, px, m), more = lay_out<W>(w, pw, n);
         int rc = allow_lds(kernel, lds);
@@ -873,7 +872,13 @@ int gradient(const ddl_ce_grad_args *c, void *ws, hipStream_t s) {
         }
         if (rc || !k)
             continue;
+        const bool both = c->dx && c->dw && go_together(px, pw);
         if constexpr (std::is_same<T, Bfloat>::value) {
+            if (wide && both) {
+                rc = f32 ? launch_both<E, Half, false, Half, true>(x, g, px, pw, m, have, s)
+                         : launch_both<E, Half, false, Half, false>(x, g, px, pw, m, have, s);
+                continue;
+            }
             if (wide) {
                 if (c->dx)
                     rc = launch_grad<Half, E, true, false, false>(x, px, m, s);
@@ -883,12 +888,9 @@ int gradient(const ddl_ce_grad_args *c, void *ws, hipStream_t s) {
                 continue;
             }
         }
-        if (c->dx && c->dw && direct && go_together(px, pw)) {
-            if constexpr (std::is_same<T, Bfloat>::value)
-                rc = twice ? launch_both<T, Half>(x, g, px, pw, m, have, s)
-                           : launch_both<T, T>(x, g, px, pw, m, have, s);
-            else
-                rc = launch_both<T, T>(x, g, px, pw, m, have, s);
+        if (both && direct) {
+            rc = twice ? launch_both<E, T, true, Half, true>(x, g, px, pw, m, have, s)
+                       : launch_both<E, T, true, T, true>(x, g, px, pw, m, have, s);
             continue;
         }
         if (c->dx)

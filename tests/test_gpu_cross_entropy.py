@@ -170,9 +170,10 @@ def check_grad(x, w, b, target, lse, dloss, scale, a, dx, dw, db, dw0=None, db0=
         near(db, want, limit)
 
 
-# bfloat16 operands in pairs, and, from 5e9 products on, as binary16: both
+# bfloat16 operands in pairs, and, from 1.2e9 products on, as binary16: both
 # outputs' types and an odd k, which is packed
-ONCE = [(65, 63, 65), (300, 520, 2056), (512, 9800, 2056), (1030, 8200, 2400), (1100, 9001, 2051)]
+ONCE = [(65, 63, 65), (300, 520, 2056), (512, 9800, 2056), (1030, 8200, 2400), (1100, 9001, 2051),
+        (700, 1000, 2048), (1100, 1000, 1201)]
 
 
 @pytest.mark.parametrize("dtype,out", [("f16", "f16"), ("f16", "f32"), ("bf16", "bf16"),

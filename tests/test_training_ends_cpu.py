@@ -318,6 +318,9 @@ def test_gpu_tests_reach_every_kernel(host_driver):
     assert any("convert_kernel" in n for n in names)
     turned = [product(n) for n in names if "grad_kernelIDF16b" in n and "4HalfE" in n]
     assert {("1", "0"), ("0", "0"), ("0", "1")} <= set(turned)
+    both = [re.findall(r"Lb(\d)ELb(\d)EE", n)[-1] for n in names
+            if "both_kernelIDF16b" in n and "6Bfloat" not in n]
+    assert {("0", "0"), ("0", "1")} <= set(both)
 
 
 @pytest.mark.parametrize("m,n,k,side", [
