@@ -16,13 +16,13 @@
 //    22 in binary16), whose products take two passes: 512 x 1000 x 2048 in binary16
 //    42 us, with dz rounded 31.  bfloat16 with binary32 dw writes dz in two parts of
 //    binary16 beside these, which dw takes with x as binary16 (below): 22 bits for
-//    16, and 512 x 5000 x 2048 121 us for 110;
+//    16, and 512 x 5000 x 2048 119 us for 110;
 //  - with bfloat16 operands, where it is faster (widens), as binary16, against x
 //    and w as binary16 too: their 8 bits fit it exactly down to 2^-31 of the largest
 //    value, which a power of two takes to the top of its range, and smaller ones to
 //    2^-39 of it.  One pass then holds dz to 11 bits, and binary32 dw takes two for
 //    22.  Finding the largest value and converting takes 3% of 8192 x 131072 x 4096:
-//    21.3 ms, 34.4 in two parts of bfloat16, and 20.4 with dz rounded to it.
+//    20.8 ms, 34.4 in two parts of bfloat16.
 // db is summed from dz before it is rounded.
 #include <hip/hip_runtime.h>
 #include <math.h>
@@ -369,7 +369,7 @@ struct GradArgs {
     uint32_t tn, splits;
     uint32_t tile_rows;  // tiles of m, of the caller's rows with dx
     float *partial;      // splits > 1: [splits][m][part_ld]
-    uint64_t part_ld;    // n rounded up to 8
+    uint64_t part_ld;    // n rounded up to 64
     Out o;
     DbArgs db;           // dw: taken by the workgroups of the first columns
 };
@@ -588,7 +588,7 @@ __global__ __launch_bounds__(256) void grad_join(GradArgs g, uint32_t side) {
 // host
 // ---------------------------------------------------------------------------
 
-bool packs(uint64_t m, uint64_t k) { return k % 8 && m >= kPackGrad; }
+bool packs(uint64_t k) { return k % 8; }
 
 // bfloat16 operands go as binary16 where the passes that it saves, two or, with dw
 // in binary32, one, cost more than two launches and the pass over w, 6 bytes of each
@@ -605,7 +605,7 @@ bool widens(uint64_t m, uint64_t n, uint64_t k, uint32_t passes) {
 // Classes of a piece: as many as dz and a packed w have room for, whole tiles, but
 // all of them where they fit.
 size_t piece_columns(size_t m, size_t n, size_t k) {
-    const size_t most = packs(m, k) || widens(m, n, k, 2) ? std::max(m, k) : m;
+    const size_t most = packs(k) || widens(m, n, k, 2) ? std::max(m, k) : m;
     const size_t fit = std::max<size_t>(kPieceElements / most / 256, 1) * 256;
     return std::min<size_t>(fit, up64(n));
 }
@@ -641,7 +641,7 @@ Buffers carve_grad(Carve &c, size_t m, size_t n, size_t k) {
     const size_t piece = piece_columns(m, n, k);
     b.dz[0] = c.take<uint16_t>(up64(m) * piece);
     b.dz[1] = c.take<uint16_t>(up64(m) * piece);
-    b.w = c.take<uint16_t>(packs(m, k) ? piece * b.rows.ld : 0);
+    b.w = c.take<uint16_t>(packs(k) ? piece * b.rows.ld : 0);
     const bool wide = widens(m, n, k, 2), always = widens(m, n, k, 1);
     for (uint16_t *&plane : b.half)
         plane = c.take<uint16_t>(always ? 0 : up64(m) * piece);
@@ -757,7 +757,7 @@ int gradient(const ddl_ce_grad_args *c, void *ws, hipStream_t s) {
     int rc = pack_rows(r, b.rows, s);
     const size_t piece = piece_columns(m, n, k);
     // straight to LDS where w's rows start on 16 bytes, or a packed piece's do
-    const bool pack = packs(m, k), direct = pack || (k % 8 == 0 && aligned16(l.w, l.ldw, 2));
+    const bool pack = packs(k), direct = pack || (k % 8 == 0 && aligned16(l.w, l.ldw, 2));
     const size_t ldw = pack ? b.rows.ld : l.ldw, ld16 = b.rows.ld;
     const bool bf = std::is_same<T, Bfloat>::value, dw32 = c->dw && f32;
     const bool wide =

@@ -107,9 +107,11 @@ struct RowsArgs {
 int pack_rows(const RowsArgs &a, const Rows &r, hipStream_t s);
 
 // Rows of k elements that do not start on 16 bytes go through registers on their
-// way to LDS; from this many rows of x on, a piece of w is packed first.  A row of
-// w costs 4 k bytes then, each product with it loses its third more.
-constexpr size_t kPackLoss = 768, kPackGrad = 384;
+// way to LDS, or a piece of w is packed first: for the gradient, whose three products
+// take it, always (in us, through registers and packed: 20 x 1000 x 501 34, 22;
+// 300 x 50001 x 2051 1022, 593; 4 x 20000 x 1001 72, 73); for the loss from this many
+// rows of x on (768 x 20000 x 1001 51, 55; 1000 x 20000 x 1001 85, 80).
+constexpr size_t kPackLoss = 1000;
 // Elements of a piece of w, and of dz, that a call holds at a time.
 constexpr size_t kPieceElements = 128u << 20;
 // to: rows of up8(k) elements, zeros behind the k-th.
