@@ -122,8 +122,7 @@ def work(case):
 # ---------------------------------------------------------------------------
 # 8-bit states: m is scale (k / 127)^2 with k's sign, k = -127 .. 127; v is
 # scale (k / 255)^4, k = 0 .. 255; the scale is the block's largest magnitude
-# in binary32, and k the nearest to the value's own root; a v over 0 keeps at
-# least k = 1, since the step divides by its root
+# in binary32, and k the nearest to the value's own root
 # ---------------------------------------------------------------------------
 
 def _decode(m, v, m_scale, v_scale):
@@ -140,7 +139,6 @@ def _encode(m, v):
     b = v / torch.where(sv > 0, sv.double(), one)[:, None]
     a = torch.round(127 * torch.sqrt(a)).clamp(max=127) * torch.sign(m)
     b = torch.round(255 * torch.sqrt(torch.sqrt(b))).clamp(max=255)
-    b = torch.where(v > 0, b.clamp(min=1), b)
     return a.to(torch.int8), b.to(torch.uint8), sm, sv
 
 
@@ -374,7 +372,6 @@ def _exact_adamw8(case, s):
         safe = torch.where(top > 0, top, torch.ones_like(top))
         k = torch.bucketize(m.abs() / safe[0][block], m_border).double()
         h = torch.bucketize(v / safe[1][block], v_border).double()
-        h[(v > 0) & (h == 0)] = 1.0
         mv[at] = torch.sign(m) * (k / 127) ** 2 * top[0][block]
         vv[at] = (h / 255) ** 4 * top[1][block]
         for cp in copy:
