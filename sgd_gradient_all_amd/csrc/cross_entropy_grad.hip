@@ -48,7 +48,7 @@ struct DzArgs {
     Rows rows;
     Operand x, w;           // w: the piece's rows
     const void *bias;       // T, the piece's, or null
-    uint32_t tn, n;         // the piece's tiles and columns
+    uint32_t tn, n;         // the piece's tiles, which cover ld, and columns
     uint32_t first;         // its first class
     float smooth, wanted;   // a / n, 1 - a
     uint16_t *dz[2];        // [up64(count)][ld]; the low parts: or null
@@ -87,7 +87,8 @@ __global__ __launch_bounds__(Core::THREADS) void dz_kernel(DzArgs a) {
     a.w.row0 = tj * BN;
     const float factor = a.rows.head->factor;
     f32x4 acc[Core::FM][Core::FN] = {};
-    if (a.x.k)
+    // a tile of 32 columns may lie past the last class: its dz is 0
+    if (a.x.k && a.w.row0 < a.n)
         Core::run(a.x, a.w, 0, (uint32_t)((a.x.k + Core::BK - 1) / Core::BK), 0, lds, acc);
     // dz in place of the logits.  A lane holds, of row l % 16 of each of its FM
     // fragments, 4 columns of each of the FN fragments.
@@ -658,7 +659,7 @@ template <class T, class D, bool STAGED>
 int launch_dz(DzArgs &a, const Plan &p, uint64_t m, hipStream_t s) {
     auto go = [&](auto core) {
         using Core = decltype(core);
-        a.tn = (a.n + Core::BN - 1) / Core::BN;
+        a.tn = (uint32_t)((a.ld + Core::BN - 1) / Core::BN);
         const int rc = allow_lds(dz_kernel<T, D, Core>, Core::LDS);
         return rc ? rc
                   : launch(dz_kernel<T, D, Core>,

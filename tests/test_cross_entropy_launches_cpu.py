@@ -1,0 +1,65 @@
+"""The cross entropy's kernels and grids, on a fake runtime."""
+import os
+import re
+import subprocess
+
+import pytest
+
+import sgd_gradient_all_amd as ddl
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def launches(tmp_path_factory):
+    """launches(op, m, n, k, dtype, out, woff): [(kernel, workgroups)]"""
+    tmp = tmp_path_factory.mktemp("launch_grids")
+    hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+    csrc, objects = os.path.join(ROOT, "sgd_gradient_all_amd", "csrc"), []
+    for name in ("cross_entropy_loss.hip", "cross_entropy_grad.hip"):
+        objects.append(str(tmp / (name + ".o")))
+        subprocess.run([hipcc, "--offload-arch=gfx950", "--offload-host-only", "-O1", "-std=c++17",
+                        "-fPIC", "-c", os.path.join(csrc, name), "-o", objects[-1]], check=True)
+    exe = str(tmp / "launch_grids")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-D__HIP_PLATFORM_AMD__", "-I/opt/rocm/include",
+                    os.path.join(ROOT, "tests", "launch_grid_driver.cpp"),
+                    os.path.join(csrc, "optimizer.cpp"), *objects, "-o", exe,
+                    "-Wl,--unresolved-symbols=ignore-in-object-files"], check=True)
+
+    def run(op, m, n, k, dtype, out=ddl.DDL_F32, woff=0):
+        args = [exe, op, m, n, k, dtype, out, woff]
+        done = subprocess.run(list(map(str, args)), capture_output=True, text=True, timeout=60)
+        assert done.returncode == 0, done.stdout + done.stderr
+        return [(line.split()[0], int(line.split()[1])) for line in done.stdout.splitlines()]
+    return run
+
+
+def tile(name):
+    return tuple(map(int, re.search(r"Core.*?Li(\d+)ELi(\d+)E", name).groups()))
+
+
+@pytest.mark.parametrize("dtype", [ddl.DDL_BF16, ddl.DDL_F16])
+@pytest.mark.parametrize("m,n,k", [
+    (1024, 1050, 2048), (1024, 1056, 1152), (512, 992, 4096), (600, 800, 4096),
+    (1024, 1030, 4096), (1100, 1049, 1201), (1146, 1241, 1255), (549, 2321, 1608),
+    (1024, 1024, 2048), (1, 1, 8), (3, 33, 64), (65, 97, 64), (4096, 10, 64), (300, 520, 2056)])
+def test_tiles_of_dz_cover_what_the_products_read(m, n, k, dtype, launches):
+    """The products' sums run over whole k tiles: 64 columns of dz at a time, those
+    past the last class too, and 64 rows."""
+    for out in (ddl.DDL_F32, dtype):
+        got = [(tile(name), grid) for name, grid in launches(1, m, n, k, dtype, out)
+               if "dz_kernel" in name]
+        assert len(got) == 1
+        (side_m, side_n), grid = got[0]
+        across = grid // -(-m // side_m)
+        assert across * side_n >= -(-n // 64) * 64
+        assert -(-m // side_m) * side_m >= -(-m // 64) * 64
+
+
+def test_narrow_tiles_are_among_them(launches):
+    """bfloat16 operands as binary16 beside 64 x 32 tiles of dz."""
+    for m, n, k in ((1024, 1050, 2048), (512, 992, 4096), (1100, 1049, 1201)):
+        for out in (ddl.DDL_F32, ddl.DDL_BF16):
+            names = [x for x, _ in launches(1, m, n, k, ddl.DDL_BF16, out)]
+            dz = [x for x in names if "dz_kernel" in x]
+            assert [tile(x) for x in dz] == [(64, 32)]
