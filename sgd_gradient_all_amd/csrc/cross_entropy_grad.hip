@@ -18,9 +18,9 @@
 //    binary16 beside these, which dw takes with x as binary16 (below): 22 bits for
 //    16, and 512 x 5000 x 2048 119 us for 110;
 //  - with bfloat16 operands, where it is faster (widens), as binary16, against x
-//    and w as binary16 too: their 8 bits fit it exactly down to 2^-31 of the largest
-//    value, which a power of two takes to the top of its range, and smaller ones to
-//    2^-39 of it.  One pass then holds dz to 11 bits, and binary32 dw takes two for
+//    and w as binary16 too: their 8 bits fit it exactly down to 2^-31 of a column's
+//    largest value, which a power of two takes to the top of its range, and smaller
+//    ones to 2^-39 of it.  One pass then holds dz to 11 bits, and binary32 dw takes two for
 //    22.  Finding the largest value and converting takes 3% of 8192 x 131072 x 4096:
 //    20.8 ms, 34.4 in two parts of bfloat16.
 // db is summed from dz before it is rounded.
@@ -225,7 +225,9 @@ __global__ __launch_bounds__(256) void db_kernel(const RowsHead *head, DbArgs a)
 // bfloat16 as binary16
 // ---------------------------------------------------------------------------
 
-constexpr uint32_t kTops = 1024;  // workgroups that look for the largest value
+// Every column goes times a power of two of its own, which takes its largest value
+// to [2^14, 2^15): a column of x or w is one of dw or dx, which takes the power back,
+// so one that is small throughout loses nothing.
 
 // One of up to two matrices that a launch takes, x and a piece of w: two launches
 // less for 4 us each.
@@ -233,32 +235,61 @@ struct Widened {
     const uint16_t *p;
     uint64_t ld, rows;
     const RowsHead *head;  // the rows are the packed ones; or null
-    uint32_t *tops;        // [kTops]
-    int *exponent;
+    uint32_t *tops;        // [ld_to]: the columns' largest, by their bits; 0 before
+    uint32_t *next;        // [ld_to]: cleared for the next piece; or null
     uint16_t *to;
-    uint32_t groups;       // workgroups of convert_kernel
+    uint32_t seek, groups; // workgroups of largest_kernel, by columns, and of convert_kernel
 };
 struct WidenArgs {
     Widened of[2];
     uint64_t cols, ld_to;
 };
 
-// The largest finite |v| of a matrix, by its bits, of each workgroup's rows.
+// The exponent of a column whose largest value has the bits top.
+__device__ __forceinline__ int column_exponent(uint32_t top) {
+    return top ? 14 - ((int)(top >> 7) - 127) : 0;
+}
+// Those of 8 columns; tops: or null.
+__device__ __forceinline__ void column_exponents(const uint32_t *tops, uint32_t n, int (&e)[8]) {
+    u32x4 t[2] = {};
+    if (tops) {
+        t[0] = *(const u32x4 *)(tops + n);
+        t[1] = *(const u32x4 *)(tops + n + 4);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        e[i] = column_exponent(t[i / 4][i % 4]);
+}
+
+// The largest finite |v| of each column.  A workgroup takes 512 columns of every
+// `seek`-th four rows: few rows by fewer workgroups, which meet at the same words at
+// the end (1024 x 1000 x 2048, the whole gradient: 57 us with a workgroup for 16 rows,
+// 64 with one for 4), many rows by no more than kTopGroups (1023 x 32003 x 1111 309 us,
+// with 64 of them 329).
+constexpr uint32_t kTopColumns = 512, kTopRows = 16, kTopGroups = 256;
+
 __global__ __launch_bounds__(256) void largest_kernel(WidenArgs a) {
-    __shared__ uint32_t wave_top[4];
-    const Widened x = blockIdx.x < kTops ? a.of[0] : a.of[1];
-    const uint32_t block = blockIdx.x % kTops;
+    __shared__ uint32_t top[kTopColumns];
+    const Widened x = blockIdx.z ? a.of[1] : a.of[0];
     const uint16_t *p = x.p;
     const uint64_t ld = x.ld, cols = a.cols, rows = x.head ? x.head->count : x.rows;
-    constexpr uint32_t U = 4;  // rows at a time: 134 MB take 26 us, 47 with one
-    uint32_t top = 0;
-    for (uint64_t r = block; r < rows; r += U * kTops)
-        for (uint64_t c = threadIdx.x * 8; c < cols; c += 256 * 8) {
+    const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
+    const uint64_t c0 = (uint64_t)blockIdx.y * kTopColumns, c = c0 + lane * 8;
+    if (blockIdx.x >= x.seek)
+        return;
+    for (uint32_t i = threadIdx.x; i < kTopColumns; i += 256)
+        top[i] = 0;
+    __syncthreads();
+    constexpr uint32_t U = 4;  // rows at a time
+    const uint64_t step = (uint64_t)x.seek * 4;
+    uint32_t most[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (c < cols)
+        for (uint64_t r = blockIdx.x * 4 + wave; r < rows; r += U * step) {
             uint16_t v[U][8];
             const uint16_t *row[U];  // the last one again where there are no more
 #pragma unroll
             for (uint32_t i = 0; i < U; ++i)
-                row[i] = p + min(r + i * kTops, rows - 1) * ld + c;
+                row[i] = p + min(r + i * step, rows - 1) * ld + c;
             if (c + 8 <= cols) {
 #pragma unroll
                 for (uint32_t i = 0; i < U; ++i)
@@ -275,25 +306,24 @@ __global__ __launch_bounds__(256) void largest_kernel(WidenArgs a) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const uint32_t u = v[i][e] & 0x7fffu;
-                    top = max(top, u < 0x7f80u ? u : 0u);
+                    most[e] = max(most[e], u < 0x7f80u ? u : 0u);
                 }
         }
 #pragma unroll
-    for (int d = 1; d < 64; d *= 2)
-        top = max(top, (uint32_t)__shfl_xor((int)top, d));
-    if ((threadIdx.x & 63u) == 0)
-        wave_top[threadIdx.x >> 6] = top;
+    for (int e = 0; e < 8; ++e)
+        if (most[e])
+            atomicMax(&top[lane * 8 + e], most[e]);
     __syncthreads();
-    if (threadIdx.x == 0)
-        x.tops[block] = max(max(wave_top[0], wave_top[1]), max(wave_top[2], wave_top[3]));
+    // a maximum is the same in any order
+    for (uint32_t i = threadIdx.x; i < kTopColumns; i += 256)
+        if (top[i])
+            atomicMax(&x.tops[c0 + i], top[i]);
 }
 
-// The matrix times the power of two that takes its largest value to [2^14, 2^15),
-// as binary16, rows of zeros behind it up to a multiple of 64.
+// The matrix as binary16, rows of zeros behind it up to a multiple of 64.
 constexpr uint32_t kConvertRows = 8;  // of a workgroup
 
 __global__ __launch_bounds__(256) void convert_kernel(WidenArgs a) {
-    __shared__ uint32_t wave_top[4];
     const bool second = blockIdx.x >= a.of[0].groups;
     const Widened m = second ? a.of[1] : a.of[0];
     const uint32_t block = blockIdx.x - (second ? a.of[0].groups : 0u);
@@ -302,25 +332,17 @@ __global__ __launch_bounds__(256) void convert_kernel(WidenArgs a) {
     const uint64_t ld = m.ld, ld_to = a.ld_to, cols = a.cols;
     const uint64_t rows = m.head ? m.head->count : m.rows;
     const uint64_t r0 = (uint64_t)block * kConvertRows;
+    if (m.next)
+        for (uint64_t i = (uint64_t)block * 256 + threadIdx.x; i < ld_to;
+             i += (uint64_t)m.groups * 256)
+            m.next[i] = 0;
     if (r0 >= up64(rows))
         return;
-    uint32_t top = 0;
-#pragma unroll
-    for (uint32_t i = 0; i < kTops; i += 256)
-        top = max(top, m.tops[i + threadIdx.x]);
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2)
-        top = max(top, (uint32_t)__shfl_xor((int)top, d));
-    if ((threadIdx.x & 63u) == 0)
-        wave_top[threadIdx.x >> 6] = top;
-    __syncthreads();
-    top = max(max(wave_top[0], wave_top[1]), max(wave_top[2], wave_top[3]));
-    const int e = top ? 14 - ((int)(top >> 7) - 127) : 0;
-    if (block == 0 && threadIdx.x == 0)
-        *m.exponent = e;
     constexpr uint32_t U = 4;  // rows at a time
-    for (uint64_t r = r0; r < r0 + kConvertRows; r += U)
-        for (uint64_t c = threadIdx.x * 8; c < ld_to; c += 256 * 8) {
+    for (uint64_t c = threadIdx.x * 8; c < ld_to; c += 256 * 8) {
+        int e[8];
+        column_exponents(m.tops, (uint32_t)c, e);
+        for (uint64_t r = r0; r < r0 + kConvertRows; r += U) {
             uint16_t v[U][8];
             if (r + U <= rows && c + 8 <= cols) {
 #pragma unroll
@@ -339,10 +361,12 @@ __global__ __launch_bounds__(256) void convert_kernel(WidenArgs a) {
                 _Float16 h[8];
 #pragma unroll
                 for (int x = 0; x < 8; ++x)
-                    h[x] = (_Float16)ldexpf(__builtin_bit_cast(float, (uint32_t)v[i][x] << 16), e);
+                    h[x] =
+                        (_Float16)ldexpf(__builtin_bit_cast(float, (uint32_t)v[i][x] << 16), e[x]);
                 __builtin_memcpy(to + (r + i) * ld_to + c, h, 16);
             }
         }
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -366,6 +390,7 @@ struct Out {
 
 struct GradArgs {
     const RowsHead *head;
+    const uint32_t *tops;  // b's columns', where it was converted; or null
     Operand a, b;
     uint32_t tn, splits;
     uint32_t tile_rows;  // tiles of m, of the caller's rows with dx
@@ -425,9 +450,9 @@ __device__ __forceinline__ Old old8(const Out &o, uint32_t m, uint32_t n) {
     return f;
 }
 
-// The product is the gradient's times 2^exponent.
+// The product is the gradient's times 2^exponent of each column.
 template <class E, bool DX, bool VEC>
-__device__ __forceinline__ void out8(const Out &o, int exponent, uint32_t m, uint32_t n,
+__device__ __forceinline__ void out8(const Out &o, const int (&exponent)[8], uint32_t m, uint32_t n,
                                      float (&v)[8], const Old &f) {
     if (m >= o.m || n >= o.n)
         return;
@@ -435,7 +460,7 @@ __device__ __forceinline__ void out8(const Out &o, int exponent, uint32_t m, uin
     float t[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        v[i] = ldexpf(v[i], -exponent);
+        v[i] = ldexpf(v[i], -exponent[i]);
     if (DX) {
         if (o.read) {
             widen8<float>(f.v, t);
@@ -465,6 +490,14 @@ __device__ __forceinline__ void out8(const Out &o, int exponent, uint32_t m, uin
         write8<VEC>((float *)o.c + m * o.ld + n, have, v);
     else
         write8<VEC>((E *)o.c + m * o.ld + n, have, v);
+}
+
+// Of the product's columns n .. n + 7: dz's and b's.
+__device__ __forceinline__ void exponents_of(const GradArgs &g, uint32_t n, int (&e)[8]) {
+    column_exponents(n < g.o.n ? g.tops : nullptr, n, e);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        e[i] += g.head->exponent;
 }
 
 // The parts of dx's sums: with fewer row tiles than were launched for, their
@@ -498,7 +531,6 @@ __device__ __forceinline__ void grad_tile(GradArgs &g, uint32_t id, uint8_t *lds
     tile_of(id - s * tm * g.tn, tm, g.tn, ti, tj);
     g.a.row0 = ti * Core::BM;
     g.b.row0 = tj * Core::BN;
-    const int exponent = g.head->exponent + (DX ? g.head->w_exponent : g.head->x_exponent);
     const uint32_t t0 = (uint32_t)((uint64_t)all * s / splits);
     const uint32_t t1 = (uint32_t)((uint64_t)all * (s + 1) / splits);
     f32x4 acc[Core::FM][Core::FN] = {};
@@ -509,6 +541,9 @@ __device__ __forceinline__ void grad_tile(GradArgs &g, uint32_t id, uint8_t *lds
     if (!DX && g.db.db && tj == 0 && s == 0)
         for (uint32_t c = threadIdx.x; c < Core::BM; c += Core::THREADS)
             db_of<E>(g.db, g.head, m0 + c);
+    int exponent[8];
+    if (g.splits == 1)
+        exponents_of(g, n0 + Core::column(), exponent);
     if (g.splits > 1) {
         float *part = g.partial + (uint64_t)s * g.o.m * g.part_ld;
         Core::each(
@@ -566,7 +601,8 @@ __global__ __launch_bounds__(256) void grad_join(GradArgs g, uint32_t side) {
     if (id >= (uint64_t)groups * g.o.m)
         return;
     const uint32_t m = (uint32_t)(id / groups), n = (uint32_t)(id % groups) * 8;
-    const int exponent = g.head->exponent + (DX ? g.head->w_exponent : g.head->x_exponent);
+    int exponent[8];
+    exponents_of(g, n, exponent);
     const Old f = g.o.vec ? old8<E, DX, true>(g.o, m, n) : old8<E, DX, false>(g.o, m, n);
     float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll 4
@@ -616,7 +652,7 @@ struct Buffers {
     uint16_t *dz[2], *half[2];
     uint16_t *w;         // packed
     uint16_t *x16, *w16; // bfloat16 as binary16
-    uint32_t *tops;
+    uint32_t *tops[3];   // of x, and of the even and the odd pieces of w
     float *sum;          // dx's over the pieces: [m][ld]
     float *db;
     float *partial;
@@ -648,7 +684,11 @@ Buffers carve_grad(Carve &c, size_t m, size_t n, size_t k) {
         plane = c.take<uint16_t>(always ? 0 : up64(m) * piece);
     b.x16 = c.take<uint16_t>(up64(m) * b.rows.ld);
     b.w16 = c.take<uint16_t>(wide ? up64(piece) * b.rows.ld : 0);
-    b.tops = c.take<uint32_t>(2 * kTops);
+    uint32_t *tops = c.take<uint32_t>(3 * b.rows.ld);
+    for (size_t i = 0; i < 3; ++i)
+        b.tops[i] = tops + i * b.rows.ld;
+    b.rows.clear = tops;
+    b.rows.clear_count = 3 * b.rows.ld;
     b.sum = c.take<float>(piece < n ? m * b.rows.ld : 0);
     b.db = c.take<float>((m + 63) / 64 * piece);
     b.partial = c.take<float>(partial_floats(m, n, k, piece));
@@ -778,17 +818,21 @@ int gradient(const ddl_ce_grad_args *c, void *ws, hipStream_t s) {
         v.ld_to = ld16;
         uint32_t count = 0;
         auto widen = [&](const uint16_t *p, size_t ld, size_t rows, const RowsHead *head,
-                         int *exponent, uint16_t *to) {
-            v.of[count] = {p,  ld, rows, head, b.tops + count * kTops, exponent,
-                           to, (uint32_t)(up64(rows) / kConvertRows)};
+                         uint32_t *tops, uint32_t *next, uint16_t *to) {
+            const uint32_t seek =
+                (uint32_t)std::min<size_t>((rows + kTopRows - 1) / kTopRows, kTopGroups);
+            v.of[count] = {p,    ld, rows, head, tops,
+                           next, to, seek, (uint32_t)(up64(rows) / kConvertRows)};
             ++count;
         };
+        const size_t odd = first / piece % 2;
         if ((wide || twice) && c->dw && k && first == 0)
-            widen(b.rows.x, ld16, m, b.rows.head, &b.rows.head->x_exponent, b.x16);
+            widen(b.rows.x, ld16, m, b.rows.head, b.tops[0], nullptr, b.x16);
         if (wide && c->dx && k)
-            widen(w, ldw, have, nullptr, &b.rows.head->w_exponent, b.w16);
+            widen(w, ldw, have, nullptr, b.tops[1 + odd], b.tops[2 - odd], b.w16);
         if (count && !rc) {
-            rc = launch(largest_kernel, dim3(count * kTops), dim3(256), 0, s, v);
+            const dim3 groups(std::max(v.of[0].seek, v.of[1].seek), (uint32_t)((k + kTopColumns - 1) / kTopColumns), count);
+            rc = launch(largest_kernel, groups, dim3(256), 0, s, v);
             rc = rc ? rc
                     : launch(convert_kernel, dim3(v.of[0].groups + v.of[1].groups), dim3(256), 0, s,
                              v);
@@ -840,6 +884,7 @@ int gradient(const ddl_ce_grad_args *c, void *ws, hipStream_t s) {
             // a packed w's columns past k are zeros
             x.b = operand(w, ldw, pack ? ldw : k, have);
             if (wide) {  // so are its rows past the piece, and dz's columns
+                x.tops = b.tops[1 + odd];
                 x.a.k = up64(have);
                 x.b = operand(b.w16, ld16, ld16, up64(have));
             }
@@ -860,6 +905,7 @@ int gradient(const ddl_ce_grad_args *c, void *ws, hipStream_t s) {
             g.db = db;
             g.a = operand(twice ? b.half[0] : b.dz[0], d.ld, d.ld, 0);
             g.a.plane[1] = twice ? b.half[1] : b.dz[1];
+            g.tops = wide || twice ? b.tops[0] : nullptr;
             g.b = operand(wide || twice ? b.x16 : b.rows.x, ld16, ld16, 0);
             g.partial = b.partial;
             g.part_ld = b.rows.ld;

@@ -43,8 +43,6 @@ struct RowsHead {
     uint32_t count;  // rows with a target
     float factor;    // a power of two that dz is held times (see write_head)
     int exponent;    // its exponent
-    // those of x and of the piece of w, as the products with dz take them
-    int x_exponent, w_exponent;
 };
 
 // The packed rows, on the device.
@@ -57,6 +55,9 @@ struct Rows {
     float *at;        // loss: the target's logit
     uint16_t *x;      // [up64(count)][ld], zeros behind the k-th element and the last row
     uint64_t ld;      // k rounded up to 64: rows are whole lines of 128 bytes
+    // cleared with the packing, for kernels that take maxima there
+    uint32_t *clear;
+    uint64_t clear_count;
 };
 
 // Sums over the packed rows run over whole k tiles: rows of zeros fill the last.
@@ -85,6 +86,8 @@ inline Rows carve_rows(Carve &c, size_t m, size_t k) {
     r.at = c.take<float>(m);
     r.ld = up64(k);
     r.x = c.take<uint16_t>(up64(m) * r.ld);
+    r.clear = nullptr;
+    r.clear_count = 0;
     return r;
 }
 

@@ -67,7 +67,6 @@ __device__ __forceinline__ void write_head(const Rows &r, uint32_t count, float 
     r.head->count = count;
     r.head->factor = ldexpf(1.0f, e);
     r.head->exponent = e;
-    r.head->x_exponent = r.head->w_exponent = 0;
 }
 
 // Packs the indices of the rows with a target, in their order: one workgroup,
@@ -162,6 +161,12 @@ __device__ __forceinline__ void zero_row(uint16_t *to, uint64_t ld) {
         *(u32x4 *)(to + c) = u32x4{0, 0, 0, 0};
 }
 
+__device__ __forceinline__ void clear_words(const Rows &r) {
+    for (uint64_t i = blockIdx.x * 256 + threadIdx.x; i < r.clear_count;
+         i += (uint64_t)gridDim.x * 256)
+        r.clear[i] = 0;
+}
+
 __global__ __launch_bounds__(256) void matrix_kernel(const uint16_t *from, uint64_t ld, uint64_t k,
                                                      uint16_t *to, uint64_t ld_to) {
     copy_row(from + blockIdx.x * ld, k, to + blockIdx.x * ld_to, ld_to);
@@ -171,6 +176,7 @@ __global__ __launch_bounds__(256) void matrix_kernel(const uint16_t *from, uint6
 // caller's row of that index is not packed.
 __global__ __launch_bounds__(256) void pack_kernel(RowsArgs a, Rows r) {
     const uint64_t i = blockIdx.x, count = r.head->count;
+    clear_words(r);
     if (i >= count && i < up64(count))
         zero_row(r.x + i * r.ld, r.ld);
     if (i < count) {
@@ -191,6 +197,7 @@ __global__ __launch_bounds__(256) void pack_few_kernel(RowsArgs a, Rows r) {
     __shared__ uint32_t before[4], have[4];
     __shared__ float tops[4];
     const uint32_t i = blockIdx.x, lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
+    clear_words(r);
     auto target = [&](uint32_t at, float &g) {
         const bool in = at < a.m;
         const long long t = a.target[in ? at : 0];

@@ -476,6 +476,12 @@ struct Core {
         }
     }
 
+    // The n, within the tile, of all that `each` hands to this lane, not TURNED.
+    __device__ __forceinline__ static uint32_t column() {
+        const uint32_t wave = threadIdx.x >> 6, l = threadIdx.x & 63u;
+        return (wave % WC) * (FN * 16) + l % (2 * FN) * 8;
+    }
+
     // then(m, n, v, fetch(m, n)) for every 8 consecutive n of a row m of the
     // wave's results (both within the tile); TURNED: for every 8 consecutive m
     // of a column n.  They go through the wave's own part of LDS, so that 8

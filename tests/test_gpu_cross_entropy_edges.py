@@ -31,3 +31,63 @@ def test_columns_past_the_last_class(m, n, k, out):
         if first is not None:
             assert all(torch.equal(p, q) for p, q in zip(first, (dx, dw, db)))
         first = dx, dw, db
+
+
+def terms(x, w, b, target, lse, scale):
+    """dz in 64 bits and what it is off by, held in 11 and in 22 bits, as check_grad
+    has it (without smoothing)."""
+    z, slack = ce.logits(x, w, b)
+    have = (target >= 0)[:, None]
+    hot = torch.zeros_like(z)
+    hot.scatter_(1, target.clamp(min=0)[:, None], 1.0)
+    far = (z - lse.double()[:, None]).abs()
+    p = torch.exp(z - lse.double()[:, None])
+    dz = torch.where(have, (p - hot) * scale, 0.0)
+    off = p * (slack + (4 + 3 * far) * ce.F32) + 4 * ce.F32 * (p + hot) + 2.0 ** -126
+    off = torch.where(have, off * scale, 0.0) + ce.F32 * dz.abs()
+    floor = torch.where(have, 2.0 ** -39 * scale, 0.0)
+    return dz, off + 2.0 ** -11 * (dz.abs() + off) + floor, \
+        off + 2.0 ** -22 * (dz.abs() + off) + floor
+
+
+def near(got, want, slack):
+    limit = slack + (want.abs() + slack) * ce.u(got.dtype) * 1.01
+    assert torch.isfinite(got).all()
+    d = (got.double() - want).abs()
+    assert (d <= limit).all(), f"{int((d > limit).sum())} off, {float((d - limit).max())}"
+
+
+def check_columns(x, w, b, target, lse, scale, dx, dw):
+    """As check_grad, but what x and w are off by goes by their columns: 2^-39 of a
+    column's largest value."""
+    (m, n), (xd, wd) = (x.shape[0], w.shape[0]), (x.double(), w.double())
+    dz, one, pair = terms(x, w, b, target, lse, scale)
+    part = pair if dw.dtype == torch.float32 else one
+    xoff, woff = (2.0 ** -39 * v.abs().amax(0)[None, :] for v in (xd, wd))
+    near(dx, dz @ wd, one @ wd.abs() + (n + 8) * ce.F32 * (dz.abs() @ wd.abs())
+         + (one + dz.abs()).sum(1)[:, None] * woff)
+    dzt, part = dz.t().contiguous(), part.t().contiguous()
+    near(dw, dzt @ xd, part @ xd.abs() + (2 * m + 8) * ce.F32 * (dzt.abs() @ xd.abs())
+         + (part + dzt.abs()).sum(1)[:, None] * xoff)
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("m,n,k", [(1030, 8200, 2400), (1100, 9001, 2051), (600, 9000, 1001),
+                                   (300, 520, 2056), (8192, 33000, 72)])
+def test_a_column_that_is_small_throughout(m, n, k, out):
+    """Columns of x and w 2^-60 and 2^-45 of the others keep their digits, with few
+    rows and with many, in one piece of the classes and in several."""
+    x, w, b, target = ce.inputs(m, n, k, "bf16", 0.0)
+    w[:, 5::7] = (w[:, 5::7].float() * 2.0 ** -60).bfloat16()
+    x[:, 3::5] = (x[:, 3::5].float() * 2.0 ** -45).bfloat16()
+    w[n // 2:, 1] = 0  # of one that is 0 in a half of the classes
+    w[:, 2], x[:, 4] = 0, 0
+    z, _ = ce.logits(x, w, b)
+    lse = torch.logsumexp(z, 1).float()
+    dx = torch.empty(m, k, device="cuda", dtype=torch.bfloat16)
+    dw = torch.empty(n, k, device="cuda", dtype=ce.T[out])
+    print(f"small columns {m} {n} {k} {out}", flush=True)
+    ddl.cross_entropy_grad(x, w, target, lse, scale=1 / m, dx=dx, dw=dw, bias=b,
+                           workspace=ce.workspace("grad", m, n, k))
+    check_columns(x, w, b, target, lse, 1 / m, dx, dw)
+    assert (dx[:, 2] == 0).all() and (dw[:, 4] == 0).all()
