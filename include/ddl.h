@@ -568,7 +568,9 @@ int ddl_linear_wgrad(const ddl_wgrad_args *args, void *workspace, size_t workspa
  * loss is scaled.  DDL_BF16's x, for dw in DDL_F32 and with many rows, and w, with
  * many rows, go as DDL_F16 times a power of two for each column as well: what is under
  * 2^-31 of the largest finite value of its column of x, or of a piece of w, is off by
- * 2^-39 of that.  lse has to be the loss's own.  db is summed before dz is rounded.
+ * 2^-39 of that.  Classes whose bias is -inf do not count for it without smoothing
+ * (where one is wanted, and the loss infinite, larger values of its w come out as about
+ * that largest one).  lse has to be the loss's own.  db is summed before dz is rounded.
  *
  * ld*, alignment, overlaps, workspace (never 0 bytes), stream, capture and errors as
  * in the linear layer; m, n and k up to 2^22, n at least 1.  Results are the same from call to

@@ -228,6 +228,10 @@ __global__ __launch_bounds__(256) void db_kernel(const RowsHead *head, DbArgs a)
 // Every column goes times a power of two of its own, which takes its largest value
 // to [2^14, 2^15): a column of x or w is one of dw or dx, which takes the power back,
 // so one that is small throughout loses nothing.
+//
+// Classes whose bias is -inf may hold anything: their dz is 0, without smoothing and
+// unless one is wanted, so they do not count for the power and what passes binary16's
+// range is held at its end (infinity would make 0 times it NaN).
 
 // One of up to two matrices that a launch takes, x and a piece of w: two launches
 // less for 4 us each.
@@ -235,6 +239,7 @@ struct Widened {
     const uint16_t *p;
     uint64_t ld, rows;
     const RowsHead *head;  // the rows are the packed ones; or null
+    const uint16_t *bias;  // the rows are classes, some perhaps with a bias of -inf; or null
     uint32_t *tops;        // [ld_to]: the columns' largest, by their bits; 0 before
     uint32_t *next;        // [ld_to]: cleared for the next piece; or null
     uint16_t *to;
@@ -244,6 +249,10 @@ struct WidenArgs {
     Widened of[2];
     uint64_t cols, ld_to;
 };
+
+__device__ __forceinline__ bool never_wanted(const uint16_t *bias, uint64_t row) {
+    return bias && bias[row] == 0xff80u;
+}
 
 // The exponent of a column whose largest value has the bits top.
 __device__ __forceinline__ int column_exponent(uint32_t top) {
@@ -287,9 +296,13 @@ __global__ __launch_bounds__(256) void largest_kernel(WidenArgs a) {
         for (uint64_t r = blockIdx.x * 4 + wave; r < rows; r += U * step) {
             uint16_t v[U][8];
             const uint16_t *row[U];  // the last one again where there are no more
+            uint32_t bits[U];
 #pragma unroll
-            for (uint32_t i = 0; i < U; ++i)
-                row[i] = p + min(r + i * step, rows - 1) * ld + c;
+            for (uint32_t i = 0; i < U; ++i) {
+                const uint64_t at = min(r + i * step, rows - 1);
+                row[i] = p + at * ld + c;
+                bits[i] = never_wanted(x.bias, at) ? 0u : 0x7fffu;
+            }
             if (c + 8 <= cols) {
 #pragma unroll
                 for (uint32_t i = 0; i < U; ++i)
@@ -305,7 +318,7 @@ __global__ __launch_bounds__(256) void largest_kernel(WidenArgs a) {
             for (uint32_t i = 0; i < U; ++i)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const uint32_t u = v[i][e] & 0x7fffu;
+                    const uint32_t u = v[i][e] & bits[i];
                     most[e] = max(most[e], u < 0x7f80u ? u : 0u);
                 }
         }
@@ -358,11 +371,16 @@ __global__ __launch_bounds__(256) void convert_kernel(WidenArgs a) {
             }
 #pragma unroll
             for (uint32_t i = 0; i < U; ++i) {
+                const float most = r + i < rows && never_wanted(m.bias, r + i)
+                                       ? 65504.0f
+                                       : __builtin_huge_valf();
                 _Float16 h[8];
 #pragma unroll
-                for (int x = 0; x < 8; ++x)
-                    h[x] =
-                        (_Float16)ldexpf(__builtin_bit_cast(float, (uint32_t)v[i][x] << 16), e[x]);
+                for (int x = 0; x < 8; ++x) {
+                    const float f =
+                        ldexpf(__builtin_bit_cast(float, (uint32_t)v[i][x] << 16), e[x]);
+                    h[x] = (_Float16)(fabsf(f) > most ? copysignf(most, f) : f);
+                }
                 __builtin_memcpy(to + (r + i) * ld_to + c, h, 16);
             }
         }
@@ -818,18 +836,20 @@ int gradient(const ddl_ce_grad_args *c, void *ws, hipStream_t s) {
         v.ld_to = ld16;
         uint32_t count = 0;
         auto widen = [&](const uint16_t *p, size_t ld, size_t rows, const RowsHead *head,
-                         uint32_t *tops, uint32_t *next, uint16_t *to) {
+                         const uint16_t *bias, uint32_t *tops, uint32_t *next, uint16_t *to) {
             const uint32_t seek =
                 (uint32_t)std::min<size_t>((rows + kTopRows - 1) / kTopRows, kTopGroups);
-            v.of[count] = {p,    ld, rows, head, tops,
-                           next, to, seek, (uint32_t)(up64(rows) / kConvertRows)};
+            v.of[count] = {p,    ld,   rows, head, bias,
+                           tops, next, to,   seek, (uint32_t)(up64(rows) / kConvertRows)};
             ++count;
         };
         const size_t odd = first / piece % 2;
         if ((wide || twice) && c->dw && k && first == 0)
-            widen(b.rows.x, ld16, m, b.rows.head, b.tops[0], nullptr, b.x16);
+            widen(b.rows.x, ld16, m, b.rows.head, nullptr, b.tops[0], nullptr, b.x16);
         if (wide && c->dx && k)
-            widen(w, ldw, have, nullptr, b.tops[1 + odd], b.tops[2 - odd], b.w16);
+            widen(w, ldw, have, nullptr,
+                  l.bias && l.smoothing == 0.0 ? (const uint16_t *)l.bias + first : nullptr,
+                  b.tops[1 + odd], b.tops[2 - odd], b.w16);
         if (count && !rc) {
             const dim3 groups(std::max(v.of[0].seek, v.of[1].seek), (uint32_t)((k + kTopColumns - 1) / kTopColumns), count);
             rc = launch(largest_kernel, groups, dim3(256), 0, s, v);

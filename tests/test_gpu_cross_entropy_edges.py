@@ -91,3 +91,46 @@ def test_a_column_that_is_small_throughout(m, n, k, out):
                            workspace=ce.workspace("grad", m, n, k))
     check_columns(x, w, b, target, lse, 1 / m, dx, dw)
     assert (dx[:, 2] == 0).all() and (dw[:, 4] == 0).all()
+
+
+@pytest.mark.parametrize("huge", [1.0, 2.0 ** 40, 2.0 ** 66, 2.0 ** 100])
+@pytest.mark.parametrize("m,n,k", [(1030, 8200, 2400), (1100, 9001, 2051), (300, 520, 2056),
+                                   (8192, 33000, 72)])
+def test_never_wanted_classes_may_hold_anything(m, n, k, huge):
+    """Padding of a vocabulary, with a bias of -inf and large weights, changes no
+    other class's share of dx, wherever it lies."""
+    x, w, b, target = ce.inputs(m, n, k, "bf16", 0.2)
+    pad = torch.arange(n, device="cuda") % 97 == 5
+    pad[-100:] = True
+    target = torch.where((target >= 0) & pad[target.clamp(min=0)], 0, target)
+    b[pad] = -float("inf")
+    z, _ = ce.logits(x, w, b)
+    lse = torch.logsumexp(z, 1).float()
+    w[pad] = (w[pad].float() * huge).bfloat16()
+    for out in (torch.bfloat16, torch.float32):
+        dx = torch.empty(m, k, device="cuda", dtype=torch.bfloat16)
+        dw, db = (torch.empty(*s, device="cuda", dtype=out) for s in ((n, k), (n,)))
+        print(f"never wanted {m} {n} {k} {huge} {out}", flush=True)
+        ddl.cross_entropy_grad(x, w, target, lse, scale=1 / m, dx=dx, dw=dw, db=db, bias=b,
+                               workspace=ce.workspace("grad", m, n, k))
+        assert (dw[pad] == 0).all() and (db[pad] == 0).all()
+        place = torch.cumsum(~pad, 0) - 1
+        kept = torch.where(target >= 0, place[target.clamp(min=0)], target)
+        check_columns(x, w[~pad], b[~pad], kept, lse, 1 / m, dx, dw[~pad])
+
+
+def test_a_never_wanted_class_that_is_wanted():
+    """Its loss is infinite; with weights like the others' its gradient is exact."""
+    m, n, k = 1030, 8200, 2400
+    x, w, b, target = ce.inputs(m, n, k, "bf16", 0.0)
+    b[7] = -float("inf")
+    target[::50] = 7
+    z, _ = ce.logits(x, w, b)
+    lse = torch.logsumexp(z, 1).float()
+    dx = torch.empty(m, k, device="cuda", dtype=torch.bfloat16)
+    dw = torch.empty(n, k, device="cuda")
+    ddl.cross_entropy_grad(x, w, target, lse, scale=1 / m, dx=dx, dw=dw, bias=b,
+                           workspace=ce.workspace("grad", m, n, k))
+    far = b.clone()
+    far[7] = -1e4  # the same shares, in numbers
+    check_columns(x, w, far, target, lse, 1 / m, dx, dw)
