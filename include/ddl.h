@@ -557,7 +557,8 @@ int ddl_linear_wgrad(const ddl_wgrad_args *args, void *workspace, size_t workspa
  * so is its gradient, whatever x holds there.  A target of n or more makes the
  * row's loss, and every gradient that the row reaches, NaN.  bias may be -inf in
  * classes that are never wanted; a row whose logits are all -inf has lse -inf and
- * loss NaN.  Rows whose dloss scale is 0 count as rows without a target.
+ * loss NaN.  dloss scale is rounded once, to binary32; rows where it is 0 count as rows
+ * without a target.
  *
  * Logits, sums and exponentials are binary32.  The gradient takes the classes
  * in pieces: it computes their logits again and holds dz of one piece, to 11

@@ -85,7 +85,7 @@ __global__ __launch_bounds__(Core::THREADS) void dz_kernel(DzArgs a) {
     a.x.row0 = ti * BM;
     a.x.rows = count;
     a.w.row0 = tj * BN;
-    const float factor = a.rows.head->factor;
+    const int exponent = a.rows.head->exponent;
     f32x4 acc[Core::FM][Core::FN] = {};
     // a tile of 32 columns may lie past the last class: its dz is 0
     if (a.x.k && a.w.row0 < a.n)
@@ -103,7 +103,7 @@ __global__ __launch_bounds__(Core::THREADS) void dz_kernel(DzArgs a) {
         const uint32_t row = row0 + i * 16;
         const bool in = row < count;
         lse[i] = in ? a.rows.lse[row] : 0.0f;
-        g[i] = in ? a.rows.g[row] * factor : 0.0f;
+        g[i] = in ? ldexpf(a.rows.g[row], exponent) : 0.0f;
         want[i] = (in ? (uint32_t)a.rows.target[row] : ~0u) - a.first - col;
     }
     if (a.bias)
@@ -810,7 +810,7 @@ int gradient(const ddl_ce_grad_args *c, void *ws, hipStream_t s) {
     r.target = l.target;
     r.lse = l.lse;
     r.dloss = c->dloss;
-    r.scale = (float)c->scale;
+    r.scale = c->scale;
     r.dx = (uint16_t *)c->dx;
     r.lddx = c->lddx;
     int rc = pack_rows(r, b.rows, s);

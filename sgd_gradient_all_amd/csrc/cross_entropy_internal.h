@@ -41,8 +41,7 @@ __device__ __forceinline__ void load4(const E *p, uint32_t have, float (&out)[4]
 // What the rows kernel counts.
 struct RowsHead {
     uint32_t count;  // rows with a target
-    float factor;    // a power of two that dz is held times (see write_head)
-    int exponent;    // its exponent
+    int exponent;    // of the power of two that dz is held times (see write_head)
 };
 
 // The packed rows, on the device.
@@ -101,7 +100,7 @@ struct RowsArgs {
     const long long *target;
     float *loss, *lse_out;
     const float *lse, *dloss;
-    float scale;
+    double scale;
     uint16_t *dx;
     uint64_t lddx;
 };

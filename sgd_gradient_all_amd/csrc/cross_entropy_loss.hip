@@ -33,9 +33,9 @@ __device__ __forceinline__ float part_of(float v, float top) {
 // rows
 // ---------------------------------------------------------------------------
 
-// The factor of row i's dz.
+// The factor of row i's dz: rounded once, so that neither side's range is a limit.
 __device__ __forceinline__ float factor_of(const RowsArgs &a, uint64_t i) {
-    return a.dloss ? a.dloss[i] * a.scale : a.scale;
+    return (float)(a.dloss ? (double)a.dloss[i] * a.scale : a.scale);
 }
 
 __device__ __forceinline__ void write_row(const RowsArgs &a, const Rows &r, uint64_t at,
@@ -54,18 +54,18 @@ __device__ __forceinline__ float size_of(float g) {
     return fabsf(g) < __builtin_huge_valf() ? fabsf(g) : 0.0f;
 }
 
-// Gradient: factor is the power of two that takes the largest |dloss scale| to
-// [2^14, 2^15).  dz = factor dloss scale (p - wanted) is held in 16 bits, and
-// |p - wanted| <= 1: so binary16 keeps 11 bits of every p down to 2^-29 of the
-// largest row's, whatever the loss is scaled by.
+// Gradient: the exponent is that of the power of two that takes the largest
+// |dloss scale| to [2^14, 2^15): from -113 to 163, which no binary32 factor holds.
+// dz = 2^exponent dloss scale (p - wanted) is held in 16 bits, and |p - wanted| <= 1:
+// so binary16 keeps 11 bits of every p down to 2^-29 of the largest row's, whatever
+// the loss is scaled by.
 __device__ __forceinline__ void write_head(const Rows &r, uint32_t count, float top) {
     int e = 0;
     if (top > 0.0f) {
-        e = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127;
-        e = 14 - (e < -86 ? -86 : e > 114 ? 114 : e);
+        (void)frexpf(top, &e);  // top = f 2^e, f in [1/2, 1)
+        e = 15 - e;
     }
     r.head->count = count;
-    r.head->factor = ldexpf(1.0f, e);
     r.head->exponent = e;
 }
 

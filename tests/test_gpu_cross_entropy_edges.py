@@ -134,3 +134,29 @@ def test_a_never_wanted_class_that_is_wanted():
     far = b.clone()
     far[7] = -1e4  # the same shares, in numbers
     check_columns(x, w, far, target, lse, 1 / m, dx, dw)
+
+
+@pytest.mark.parametrize("m,n,k,dtype", [(100, 3000, 136, "f16"), (100, 3000, 136, "bf16"),
+                                         (1030, 8200, 2400, "bf16")])
+def test_scales_to_the_ends_of_binary32(m, n, k, dtype):
+    """A power of two in the loss is the same power in the gradients, bit for bit,
+    from the smallest factors to the largest; subnormal results are rounded once."""
+    x, w, b, target = ce.inputs(m, n, k, dtype, 0.2)
+    z, _ = ce.logits(x, w, b)
+    lse = torch.logsumexp(z, 1).float()
+    want = ce.run_grad(x, w, b, target, lse, scale=1 / 64)
+    assert all(torch.isfinite(v).all() and (v != 0).any() for v in want)
+
+    def same(got, e, which):
+        for i in which:
+            assert torch.equal(got[i], (want[i].double() * 2.0 ** e).to(want[i].dtype)), (e, i)
+
+    for e in (-140, -120, -110, -90, 100, 115, 123):
+        print(f"scale {m} {n} {k} {dtype} {e}", flush=True)
+        got = ce.run_grad(x, w, b, target, lse, scale=2.0 ** e / 64)
+        # binary16's range is its own, and subnormal bfloat16 is rounded from binary32's
+        same(got, e, (0, 1, 2) if dtype == "bf16" and e > -100 else (1, 2))
+    for p, q in ((100, -160), (-120, 140), (20, -80)):  # of the two factors
+        dloss = torch.full((m,), 2.0 ** p, device="cuda")
+        got = ce.run_grad(x, w, b, target, lse, dloss=dloss, scale=2.0 ** q / 64)
+        same(got, p + q, (1, 2))
