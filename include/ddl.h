@@ -657,7 +657,8 @@ int ddl_adamw_destroy(ddl_adamw handle);
  *   m = s (k / 127)^2 with k's sign, k = -127 .. 127
  *   v = s (k / 255)^4,               k = 0 .. 255
  * A step decodes them, moves them and the weights as ddl_adamw_step does (the
- * weights by the moments as they are before they are encoded again), and
+ * weights by the moments as they are before they are encoded again, with the
+ * hardware's root and reciprocal, so not to the same last bits), and
  * encodes: s is the largest magnitude of the block, rounded to binary32, and k
  * the code whose root is nearest to the value's; a v over 0 keeps k >= 1.
  * Codes and scales of 0 are the states before the first step.  A gradient that

@@ -29,6 +29,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <limits>
 #include <new>
 #include <type_traits>
 
@@ -66,7 +67,8 @@ struct Adam8Args {
     double b1, b2, c1, c2;  // c = 1 - b
     float step, root, eps;  // lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
     float keep;             // 1 - lr decay
-    int vec, subnormal;     // subnormal: eps does not cover roots of subnormal v
+    int vec;
+    int wide;               // the weights meet subnormal numbers (see ddl_adamw8_step)
 };
 
 // The largest of x over the wave in its lower half's lanes, and that of y in the
@@ -199,15 +201,16 @@ __device__ __forceinline__ void step_wave(const Adam8Args &a, const R &r, uint64
             const float mf = (float)x.m, vf = (float)x.v;
             top_m[b] = max(top_m[b], __builtin_bit_cast(uint32_t, mf) & 0x7fffffffu);
             top_v[b] = max(top_v[b], __builtin_bit_cast(uint32_t, vf));
-            // the hardware's root, 1 ulp off, takes subnormal numbers for 0
+            // The hardware's root and reciprocal are 1 ulp off (correctly rounded
+            // ones: 300M elements 960 us, so 890) and take subnormal numbers for 0.
             root[b][e] = __builtin_amdgcn_sqrtf(vf);
-            float d = root[b][e];
-            if (a.subnormal && vf < 0x1p-96f)
-                d = __builtin_amdgcn_sqrtf(vf * 0x1p64f) * 0x1p-32f;
-            // so is its reciprocal; a root of binary32 and eps are never subnormal
-            w[b][e] = __builtin_fmaf(-a.step,
-                                     mf * __builtin_amdgcn_rcpf(__builtin_fmaf(d, a.root, a.eps)),
-                                     a.keep * w[b][e]);
+            if (a.wide)
+                w[b][e] = a.keep * w[b][e] - a.step * (mf / (sqrtf(vf) * a.root + a.eps));
+            else
+                w[b][e] = __builtin_fmaf(
+                    -a.step,
+                    mf * __builtin_amdgcn_rcpf(__builtin_fmaf(root[b][e], a.root, a.eps)),
+                    a.keep * w[b][e]);
         }
         const uint64_t i = at + b * kBlock;
         store4<VEC>(a.w + i, lane, have[b], w[b]);
@@ -455,10 +458,12 @@ int ddl_adamw8_step(ddl_adamw8 h, const void *grad, int grad_dtype, signed char 
     a.c2 = 1 - beta2;
     a.step = (float)(lr / (1 - std::pow(beta1, (double)step)));
     a.root = (float)(1 / std::sqrt(1 - std::pow(beta2, (double)step)));
-    a.eps = (float)eps;
+    // an eps over 0 stays over 0: weights without a gradient so far do not move
+    a.eps = eps > 0 ? std::max((float)eps, std::numeric_limits<float>::denorm_min()) : 0.0f;
     a.keep = (float)(1 - lr * weight_decay);
-    // under it, roots of subnormal v are below a rounding of eps
-    a.subnormal = eps < 1e-11;
+    // roots of subnormal v, up to 2^-63, times a.root are more than a rounding of eps,
+    // or eps or its reciprocal is subnormal itself
+    a.wide = !(eps >= (double)a.root * 0x1p-63 * 0x1p24 && eps <= 0x1p125);
     uintptr_t all = (uintptr_t)grad | (uintptr_t)copy | (uintptr_t)m | (uintptr_t)v;
     for (int i = 0; i < r.count; ++i)
         all |= (uintptr_t)r.w[i];
