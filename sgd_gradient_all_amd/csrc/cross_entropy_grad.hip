@@ -660,7 +660,8 @@ bool widens(uint64_t m, uint64_t n, uint64_t k, uint32_t passes) {
 // Classes of a piece: as many as dz and a packed w have room for, whole tiles, but
 // all of them where they fit.
 size_t piece_columns(size_t m, size_t n, size_t k) {
-    const size_t most = packs(k) || widens(m, n, k, 2) ? std::max(m, k) : m;
+    const size_t rows = up64(m);  // of dz
+    const size_t most = packs(k) || widens(m, n, k, 2) ? std::max<size_t>(rows, k) : rows;
     const size_t fit = std::max<size_t>(kPieceElements / most / 256, 1) * 256;
     return std::min<size_t>(fit, up64(n));
 }

@@ -63,3 +63,11 @@ def test_narrow_tiles_are_among_them(launches):
             names = [x for x, _ in launches(1, m, n, k, ddl.DDL_BF16, out)]
             dz = [x for x in names if "dz_kernel" in x]
             assert [tile(x) for x in dz] == [(64, 32)]
+
+
+@pytest.mark.parametrize("m", [1, 3, 16, 63])
+@pytest.mark.parametrize("n,k", [(1 << 22, 64), ((1 << 21) + 300, 2056), (3000000, 1001)])
+def test_few_rows_need_no_more_room_than_64(m, n, k):
+    """dz is held for whole k tiles of 64 rows, and a piece's size goes by those."""
+    assert ddl.cross_entropy_workspace("grad", m, n, k) \
+        <= ddl.cross_entropy_workspace("grad", 64, n, k)
