@@ -6,6 +6,8 @@ import subprocess
 import pytest
 
 import sgd_gradient_all_amd as ddl
+import test_gpu_cross_entropy as gpu_tests
+import test_gpu_cross_entropy_edges as edge_tests
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -71,3 +73,27 @@ def test_few_rows_need_no_more_room_than_64(m, n, k):
     """dz is held for whole k tiles of 64 rows, and a piece's size goes by those."""
     assert ddl.cross_entropy_workspace("grad", m, n, k) \
         <= ddl.cross_entropy_workspace("grad", 64, n, k)
+
+
+def test_gpu_tests_take_every_tile_through_registers(launches):
+    """w off 16 bytes: its rows go through registers in the loss, in dz (held in
+    either type) and, unless w is converted, in dx."""
+    seen = set()
+    sizes = [(*s, 1) for s in gpu_tests.LARGE + gpu_tests.SIZES] + edge_tests.THROUGH_REGISTERS
+    for m, n, k, first in sizes:
+        for op, out in ((0, ddl.DDL_F32), (1, ddl.DDL_F32), (1, ddl.DDL_BF16)):
+            for name, _ in launches(op, m, n, k, ddl.DDL_BF16, out, 2 * first):
+                if "Core" not in name or "both_kernel" in name:
+                    continue
+                products = re.findall(r"Lb(\d)ELb(\d)EEE", name)
+                what = "loss" if "loss_kernel" in name else "dz" if "dz_kernel" in name else \
+                    "dx" if products[-1][0] == "1" else "dw"
+                staged = re.search(r"Lb\dELb\dELb(\d)E", name).group(1) == "1"
+                seen.add((what, tile(name), staged, "4Half" in name))
+    for side in ((256, 256), (128, 128), (64, 64), (64, 32)):
+        for held in (False, True):
+            assert ("dz", side, True, held) in seen, (side, held)
+        assert ("loss", side, True, False) in seen, side
+    for side in ((256, 256), (128, 128), (64, 64)):
+        assert ("dx", side, True, False) in seen, side
+    assert ("dx", (256, 256), False, False) in seen

@@ -160,3 +160,35 @@ def test_scales_to_the_ends_of_binary32(m, n, k, dtype):
         dloss = torch.full((m,), 2.0 ** p, device="cuda")
         got = ce.run_grad(x, w, b, target, lse, dloss=dloss, scale=2.0 ** q / 64)
         same(got, p + q, (1, 2))
+
+
+# (m, n, k, elements that w starts past a 16-byte boundary): with test_large's sizes, every
+# tile of bfloat16's products with rows of w through registers; which is which is
+# checked on the host
+THROUGH_REGISTERS = [(7621, 130, 552, 1), (990, 8469, 1496, 0), (151, 7761, 7456, 1),
+                     (1970, 605, 1024, 1), (800, 662, 2432, 1)]
+
+
+@pytest.mark.parametrize("m,n,k,first", THROUGH_REGISTERS)
+def test_rows_through_registers(m, n, k, first):
+    x, w, b, target = ce.inputs(m, n, k, "bf16", 0.1)
+    off = ce.strided(w, 0, first)
+    for out in (torch.bfloat16, torch.float32):
+        print(f"through registers {m} {n} {k} {first} {out}", flush=True)
+        loss, lse = ce.run_loss(x, off, b, target, 0.1)
+        ce.check_loss(x, w, b, target, 0.1, loss, lse)
+        dx, dw, db = ce.run_grad(x, off, b, target, lse, scale=1 / m, a=0.1, out=out)
+        ce.check_grad(x, w, b, target, lse, None, 1 / m, 0.1, dx, dw, db)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("m,n,k", [(1, 131072, 512), (2, 50001, 1000), (3, 40000, 1023)])
+def test_gradient_of_a_token_or_a_few(m, n, k, dtype):
+    """Large vocabularies: every class of every output."""
+    x, w, b, target = ce.inputs(m, n, k, dtype, 0.0)
+    loss, lse = ce.run_loss(x, w, b, target)
+    ce.check_loss(x, w, b, target, 0.0, loss, lse)
+    for out in (ce.T[dtype], torch.float32):
+        print(f"a few {m} {n} {k} {out}", flush=True)
+        dx, dw, db = ce.run_grad(x, w, b, target, lse, scale=1 / m, out=out)
+        ce.check_grad(x, w, b, target, lse, None, 1 / m, 0.0, dx, dw, db)
