@@ -411,25 +411,21 @@ __device__ __forceinline__ uint32_t target_of(const LossArgs &a, uint32_t m) {
     return t < 0 ? ~0u : (uint64_t)t >= a.n ? (uint32_t)kBadTarget : (uint32_t)t;
 }
 
-// Up to 64 rows: the weights are read once and bound the time, or the few steps of
-// each sum do.  A workgroup takes a run of groups of 16 columns; for each, its 8
-// waves take an eighth of k, straight into the matrix instruction's registers,
-// for R groups of 16 rows; then the lanes add the parts up, a row and column each,
-// and keep the rows' largest logit and sum as they go.
+// Up to 64 rows of few classes (by_groups): the few steps of each sum bound the time.
+// A workgroup takes 16 columns; its 8 waves take an eighth of k each, straight into the
+// matrix instruction's registers, for R groups of 16 rows; then the lanes add the parts
+// up, a row and column each, and join the rows' logits.
 constexpr int kFewWaves = 8;
 constexpr uint64_t kFewRows = 64;
 
 template <class T, int R>
-__global__ __launch_bounds__(kFewWaves * 64) void few_kernel(LossArgs a, uint32_t groups) {
+__global__ __launch_bounds__(kFewWaves * 64) void few_kernel(LossArgs a) {
     using E = typename T::E;
-    constexpr uint32_t TURNS = R < 4 ? 2 : 1;  // as many as 64 KB of LDS hold
-    __shared__ f32x4 parts[TURNS][kFewWaves][R * 16][5];  // [wave][m][n / 4], a chunk of padding
+    __shared__ f32x4 parts[kFewWaves][R * 16][5];  // [wave][m][n / 4], a chunk of padding
     const uint32_t count = rows_of(a);
     const uint32_t l = threadIdx.x & 63u, wave = threadIdx.x >> 6, r = l & 15u, g = l >> 4;
     if (!count)
         return;
-    const uint32_t g0 = (uint32_t)((uint64_t)groups * blockIdx.x / gridDim.x);
-    const uint32_t g1 = (uint32_t)((uint64_t)groups * (blockIdx.x + 1) / gridDim.x);
     const uint32_t steps = (uint32_t)((a.x.k + 31) / 32);
     const uint32_t s0 = steps * wave / kFewWaves, s1 = steps * (wave + 1) / kFewWaves;
     const uint16_t *px[R];
@@ -442,100 +438,82 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_kernel(LossArgs a, uint32_
     constexpr uint32_t EACH = R < 2 ? 1 : R / 2;  // rows, 32 apart
     const uint32_t m0 = threadIdx.x >> 4, c = threadIdx.x & 15u;
     uint32_t want[EACH];
-    float top[EACH], sum[EACH], all[EACH];
 #pragma unroll
     for (uint32_t i = 0; i < EACH; ++i) {
         const uint32_t m = m0 + i * 32;
         want[i] = m < count ? target_of(a, m) : ~0u;
-        top[i] = kNone;
-        sum[i] = all[i] = 0.0f;
     }
-    for (uint32_t q = g0; q < g1; ++q) {
-        const uint64_t n0 = (uint64_t)q * 16;
-        const uint64_t rw = n0 + r < a.n ? n0 + r : a.n - 1;
-        const uint16_t *pw = a.w.plane[0] + rw * a.w.ld + g * 8;
-        f32x4 acc[R] = {};
-        constexpr uint32_t U = 8;
-        uint32_t s = s0;
-        for (; s + U <= s1 && (uint64_t)(s + U) * 32 <= a.x.k; s += U) {
-            gemm::s16x8 w[U];
+    const uint64_t n0 = (uint64_t)blockIdx.x * 16;
+    const uint64_t rw = n0 + r < a.n ? n0 + r : a.n - 1;
+    const uint16_t *pw = a.w.plane[0] + rw * a.w.ld + g * 8;
+    f32x4 acc[R] = {};
+    constexpr uint32_t U = 8;
+    uint32_t s = s0;
+    for (; s + U <= s1 && (uint64_t)(s + U) * 32 <= a.x.k; s += U) {
+        gemm::s16x8 w[U];
+#pragma unroll
+        for (uint32_t i = 0; i < U; ++i)
+            w[i] = __builtin_nontemporal_load((const gemm::s16x8 *)(pw + (uint64_t)(s + i) * 32));
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            gemm::s16x8 x[U];
 #pragma unroll
             for (uint32_t i = 0; i < U; ++i)
-                w[i] = __builtin_nontemporal_load(
-                    (const gemm::s16x8 *)(pw + (uint64_t)(s + i) * 32));
+                x[i] = *(const gemm::s16x8 *)(px[j] + (uint64_t)(s + i) * 32);
 #pragma unroll
-            for (int j = 0; j < R; ++j) {
-                gemm::s16x8 x[U];
-#pragma unroll
-                for (uint32_t i = 0; i < U; ++i)
-                    x[i] = *(const gemm::s16x8 *)(px[j] + (uint64_t)(s + i) * 32);
-#pragma unroll
-                for (uint32_t i = 0; i < U; ++i)
-                    acc[j] = T::mfma(w[i], x[i], acc[j]);
-            }
-        }
-        for (; s < s1; ++s) {
-            const bool in = (uint64_t)s * 32 + g * 8 < a.x.k;  // k is a multiple of 8
-            gemm::s16x8 w = {};
-            if (in)
-                w = *(const gemm::s16x8 *)(pw + (uint64_t)s * 32);
-#pragma unroll
-            for (int j = 0; j < R; ++j) {
-                gemm::s16x8 x = {};
-                if (in)
-                    x = *(const gemm::s16x8 *)(px[j] + (uint64_t)s * 32);
-                acc[j] = T::mfma(w, x, acc[j]);
-            }
-        }
-        // a wave that is a group ahead does not overwrite what the last one's
-        // sums are read from
-        if (TURNS == 1)
-            __syncthreads();
-#pragma unroll
-        for (int j = 0; j < R; ++j)
-            parts[q % TURNS][wave][j * 16 + r][g] = acc[j];
-        __syncthreads();
-        float b = 0.0f;
-        if (a.bias && n0 + c < a.n)
-            b = (float)((const E *)a.bias)[n0 + c];
-#pragma unroll
-        for (uint32_t i = 0; i < EACH; ++i) {
-            const uint32_t m = m0 + i * 32;
-            if (m >= count || n0 + c >= a.n)
-                continue;
-            float v = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kFewWaves; ++w)
-                v += parts[q % TURNS][w][m][c / 4][c % 4];
-            v += b;
-            if (want[i] == (uint32_t)(n0 + c))
-                a.rows.at[m] = v;
-            all[i] += v;
-            // each lane its own columns; -inf and NaN as elsewhere
-            const float old = top[i];
-            top[i] = fmaxf(old, v);
-            sum[i] = sum[i] * part_of(old, top[i]) + part_of(v, top[i]);
+            for (uint32_t i = 0; i < U; ++i)
+                acc[j] = T::mfma(w[i], x[i], acc[j]);
         }
     }
+    for (; s < s1; ++s) {
+        const bool in = (uint64_t)s * 32 + g * 8 < a.x.k;  // k is a multiple of 8
+        gemm::s16x8 w = {};
+        if (in)
+            w = *(const gemm::s16x8 *)(pw + (uint64_t)s * 32);
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            gemm::s16x8 x = {};
+            if (in)
+                x = *(const gemm::s16x8 *)(px[j] + (uint64_t)s * 32);
+            acc[j] = T::mfma(w, x, acc[j]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+        parts[wave][j * 16 + r][g] = acc[j];
+    __syncthreads();
+    const bool in = n0 + c < a.n;
+    const float b = a.bias && in ? (float)((const E *)a.bias)[n0 + c] : 0.0f;
 #pragma unroll
     for (uint32_t i = 0; i < EACH; ++i) {
         const uint32_t m = m0 + i * 32;
-        const float own = top[i];
+        float z = kNone, all = 0.0f;
+        if (m < count && in) {
+            z = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kFewWaves; ++w)
+                z += parts[w][m][c / 4][c % 4];
+            z += b;
+            if (want[i] == (uint32_t)(n0 + c))
+                a.rows.at[m] = z;
+            all = z;
+        }
+        float top = z;  // a NaN is in the sum
 #pragma unroll
         for (int d = 1; d < 16; d *= 2)
-            top[i] = fmaxf(top[i], __shfl_xor(top[i], d));
-        sum[i] *= part_of(own, top[i]);
+            top = fmaxf(top, __shfl_xor(top, d));
+        float sum = part_of(z, top);
 #pragma unroll
         for (int d = 1; d < 16; d *= 2) {
-            sum[i] += __shfl_xor(sum[i], d);
-            all[i] += __shfl_xor(all[i], d);
+            sum += __shfl_xor(sum, d);
+            all += __shfl_xor(all, d);
         }
         if (c == 0 && m < count) {
             const uint64_t at = (uint64_t)blockIdx.x * a.m + m;
-            a.top[at] = top[i];
-            a.sum[at] = sum[i];
+            a.top[at] = top;
+            a.sum[at] = sum;
             if (a.all)
-                a.all[at] = all[i];
+                a.all[at] = all;
         }
     }
 }
@@ -543,8 +521,6 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_kernel(LossArgs a, uint32_
 // A decoded token or a few: no matrix instruction, whose operand takes 64 bytes of
 // a row at a time.  A wave reads four rows of w as they lie, 1 KB a time, against
 // x in LDS, adds its lanes' sums up and keeps the largest logit and sum of its rows.
-constexpr uint64_t kVectorBytes = 32768;  // of x
-
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
     for (int d = 1; d < 64; d *= 2)
@@ -728,10 +704,39 @@ __global__ __launch_bounds__(256) void join_kernel(LossArgs a, uint32_t parts, f
 // host
 // ---------------------------------------------------------------------------
 
-// Workgroups for few rows: as many as are there at the same time.
-constexpr uint32_t kFewGroups = 1024;
+// Workgroups by vectors, as many as are there at the same time.  In us, 512, 1024 and
+// 2048 of them: 1 x 131072 x 4096 166, 165, 173; 1 x 32000 x 4096 48, 46, 47;
+// 4 x 131072 x 4096 179, 191, 188.
+constexpr uint32_t kVectorGroups = 1024;
 
-bool few(uint64_t m) { return m <= kFewRows; }
+// vector_kernel: one row at any length that LDS holds; up to four where the sums over
+// a wave, one for each row and class, are few beside the products.  In us, by vectors,
+// by groups of 16 columns (few_kernel) and by tiles:
+//   1 x 131072 x 4096 165, 203, 181;  1 x 32000 x 1024 16, 20, 19;
+//   2 x 64000 x 4096 91, 112, 114;  2 x 16000 x 2048 19, 21, 24;
+//   2 x 64000 x 1024 40, 31, 30;  4 x 64000 x 256 47, 16, 16;
+//   4 x 64000 x 4096 103, 117, 114;  4 x 32000 x 4096 59, 62, 46;  4 x 4000 x 2048 14, 12, 20.
+// More than 32 KB of x, by vectors and by the better of the others:
+//   1 x 64000 x 24576 478, 549;  2 x 20000 x 12288 90, 113;  2 x 1000 x 12288 20, 22;
+//   4 x 20000 x 5120 60, 44;  4 x 4000 x 6144 21, 16.
+bool by_vectors(uint64_t m, uint64_t k) {
+    if (!k || m > 4 || (m > 1 && k < 2048))
+        return false;
+    return m <= 2 ? m * k * 2 <= 49152 : 4 * k * 2 <= 32768;
+}
+
+// few_kernel: a workgroup that takes a second group of 16 columns waits for its loads
+// again, which tiles copy ahead, and the more rows a group has the longer it holds up
+// the next.  In us, by groups and by tiles:
+//   64 x 4096 x 1024 13, 16;  64 x 5000 x 1024 18, 16;  64 x 4096 x 4096 29, 31;
+//   64 x 5000 x 4096 48, 31;  32 x 8192 x 1024 14, 16;  32 x 8192 x 4096 34, 32;
+//   32 x 12000 x 4096 47, 37;  16 x 12000 x 1024 14, 17;  16 x 12000 x 4096 34, 37;
+//   16 x 16384 x 4096 43, 37;  64 x 131072 x 4096 671, 195.
+bool by_groups(uint64_t m, uint64_t n) {
+    const uint64_t groups = (n + 15) / 16;
+    return m <= kFewRows && groups <= (m <= 16 ? 768u : m <= 32 ? 512u : 256u);
+}
+
 bool packs(uint64_t m, uint64_t k) { return k % 8 && m >= kPackLoss; }
 
 struct LossCut {
@@ -744,8 +749,8 @@ LossCut loss_cut(uint64_t m, uint64_t n, uint64_t k) {
     LossCut c;
     c.plan = plan_product(m, n, k, true);
     c.parts = (uint32_t)((n + kSideN[c.plan.tile] - 1) / kSideN[c.plan.tile]);
-    if (few(m))
-        c.parts = std::max(c.parts, kFewGroups);
+    if (m <= kFewRows)  // at most 768 by groups, and by vectors
+        c.parts = std::max(c.parts, kVectorGroups);
     // whole tiles
     c.piece = packs(m, k) ? std::min<size_t>(std::max<size_t>(kPieceElements / k / 256, 1) * 256,
                                              (n + 255) / 256 * 256)
@@ -810,8 +815,10 @@ int loss(const ddl_ce_args *c, void *ws, hipStream_t s) {
     r.lse_out = c->lse;
     // straight to LDS or registers where every row starts on 16 bytes
     const bool direct = c->k % 8 == 0 && aligned16(c->w, c->ldw, 2);
+    const bool vectors = direct && by_vectors(c->m, c->k);
+    const bool groups = direct && !vectors && by_groups(c->m, c->n);
     int rc = DDL_OK;
-    if (direct && few(c->m) && aligned16(c->x, c->ldx, 2)) {
+    if ((vectors || groups) && aligned16(c->x, c->ldx, 2)) {
         a.target = c->target;
         a.x = operand(c->x, c->ldx, c->m, c->k);
     } else {
@@ -829,20 +836,19 @@ int loss(const ddl_ce_args *c, void *ws, hipStream_t s) {
     const LossCut t = loss_cut(c->m, c->n, c->k);
     const uint32_t side = kSideN[t.plan.tile];
     uint32_t parts = (uint32_t)((c->n + side - 1) / side);
-    const size_t m = c->m <= 2 ? c->m : 4;
-    if (direct && c->m <= m && m * c->k * 2 <= kVectorBytes && c->k) {
-        parts = (uint32_t)std::min<size_t>(kFewGroups, (c->n + 15) / 16);
+    if (vectors) {
+        const size_t m = c->m <= 2 ? c->m : 4;
+        parts = (uint32_t)std::min<size_t>(kVectorGroups, (c->n + 15) / 16);
         rc = launch(m == 1   ? vector_kernel<T, 1>
                     : m == 2 ? vector_kernel<T, 2>
                              : vector_kernel<T, 4>,
                     dim3(parts), dim3(256), m * c->k * sizeof(uint16_t), s, a);
-    } else if (direct && few(c->m)) {
-        const uint32_t groups = (uint32_t)((c->n + 15) / 16);
-        parts = std::min(kFewGroups, groups);
+    } else if (groups) {
+        parts = (uint32_t)((c->n + 15) / 16);
         rc = launch(c->m <= 16   ? few_kernel<T, 1>
                     : c->m <= 32 ? few_kernel<T, 2>
                                  : few_kernel<T, 4>,
-                    dim3(parts), dim3(kFewWaves * 64), 0, s, a, groups);
+                    dim3(parts), dim3(kFewWaves * 64), 0, s, a);
     } else if (t.piece) {
         a.x.k = a.rows.ld;  // zeros past k on both sides
         for (size_t first = 0; first < c->n && !rc; first += t.piece) {

@@ -97,3 +97,34 @@ def test_gpu_tests_take_every_tile_through_registers(launches):
     for side in ((256, 256), (128, 128), (64, 64)):
         assert ("dx", side, True, False) in seen, side
     assert ("dx", (256, 256), False, False) in seen
+
+
+@pytest.mark.parametrize("m,n,k,kernel", [
+    (1, 131072, 4096, "vector_kernel"), (1, 64000, 256, "vector_kernel"),
+    (2, 64000, 2048, "vector_kernel"), (2, 64000, 1024, "loss_kernel"),
+    (4, 64000, 256, "loss_kernel"), (4, 5000, 256, "few_kernel"),
+    (1, 100, 24576, "vector_kernel"), (1, 100, 24584, "few_kernel"),
+    (5, 1000, 2048, "few_kernel"), (16, 12288, 64, "few_kernel"), (16, 12289, 64, "loss_kernel"),
+    (32, 8192, 64, "few_kernel"), (32, 8193, 64, "loss_kernel"), (64, 4096, 64, "few_kernel"),
+    (64, 4097, 64, "loss_kernel"), (64, 131072, 4096, "loss_kernel"), (65, 16, 64, "loss_kernel")])
+def test_kernels_for_few_rows(m, n, k, kernel, launches):
+    for dtype in (ddl.DDL_F16, ddl.DDL_BF16):
+        names = [x for x, _ in launches(0, m, n, k, dtype)]
+        assert [x for x in ("vector_kernel", "few_kernel", "loss_kernel")
+                if any(x in name and "pack" not in name for name in names)] == [kernel]
+
+
+@pytest.mark.parametrize("m", [1, 2, 3, 4, 5, 16, 17, 33, 64])
+def test_room_for_the_parts_of_few_rows(m, launches):
+    """A workgroup's part of each row, of every kernel that takes the call."""
+    for n, k in ((1, 8), (300, 4096), (4096, 64), (12288, 64), (131072, 256), (1 << 22, 64)):
+        room = ddl.cross_entropy_workspace("forward", m, n, k)
+        for woff in (0, 2):
+            for name, groups in launches(0, m, n, k, ddl.DDL_F16, ddl.DDL_F32, woff):
+                if "vector_kernel" in name or ("few_kernel" in name and "pack" not in name):
+                    parts = groups
+                elif "loss_kernel" in name:
+                    parts = -(-n // tile(name)[1])
+                else:
+                    continue
+                assert 3 * 4 * parts * m <= room

@@ -192,3 +192,17 @@ def test_gradient_of_a_token_or_a_few(m, n, k, dtype):
         print(f"a few {m} {n} {k} {out}", flush=True)
         dx, dw, db = ce.run_grad(x, w, b, target, lse, scale=1 / m, out=out)
         ce.check_grad(x, w, b, target, lse, None, 1 / m, 0.0, dx, dw, db)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("m,n,k", [
+    (1, 300, 24576), (2, 300, 12288), (1, 300, 24584), (2, 300, 12296), (4, 300, 4096),
+    (3, 300, 4104), (2, 700, 2040), (16, 12288, 72), (16, 12289, 72), (32, 8192, 40),
+    (32, 8193, 40), (64, 4096, 72), (64, 4097, 72), (17, 8192, 8), (33, 4096, 264)])
+def test_few_rows_on_both_sides_of_the_rules(m, n, k, dtype):
+    """By vectors, by groups of 16 columns and by tiles."""
+    for a, bias, ignored in ((0.0, True, 0.0), (0.2, False, 0.4)):
+        x, w, b, target = ce.inputs(m, n, k, dtype, ignored, bias)
+        target[0] = n - 1
+        print(f"both sides {m} {n} {k} {dtype} {a}", flush=True)
+        ce.check_loss(x, w, b, target, a, *ce.run_loss(x, w, b, target, a))
