@@ -441,7 +441,7 @@ class AdamW8(_Spans):
 
     def _states(self, m, v, m_scale, v_scale, device):
         for t, name, dtype in ((m, "m", "torch.int8"), (v, "v", "torch.uint8")):
-            if str(t.dtype) != dtype:
+            if t is not None and str(t.dtype) != dtype:
                 raise ValueError(f"{name} has type {t.dtype}: expected {dtype}")
         return (_flat(m, self.need, "m", None, device), _flat(v, self.need, "v", None, device),
                 _flat(m_scale, self.blocks, "m_scale", _F32, device),
