@@ -573,9 +573,9 @@ int ddl_linear_wgrad(const ddl_wgrad_args *args, void *workspace, size_t workspa
  * (where one is wanted, and the loss infinite, larger values of its w come out as about
  * that largest one).  lse has to be the loss's own.  db is summed before dz is rounded.
  *
- * ld*, alignment, overlaps, workspace (never 0 bytes), stream, capture and errors as
- * in the linear layer; m, n and k up to 2^22, n at least 1.  Results are the same from call to
- * call. */
+ * ld*, alignment, overlaps, workspace (0 bytes only without rows), stream, capture and
+ * errors as in the linear layer; m, n and k up to 2^22, n at least 1.  Results are the
+ * same from call to call. */
 enum { DDL_CE_FORWARD = 0, DDL_CE_GRAD = 1 };
 
 typedef struct {

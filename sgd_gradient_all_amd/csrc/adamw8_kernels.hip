@@ -15,12 +15,13 @@
 //
 // A code is the one whose root is nearest to the value's.  Which one that is is
 // decided in binary64, where the card is as fast as in binary32, with every term
-// rounded as the formula reads: the same step gives the same codes everywhere.  A v over 0 keeps at least k = 1: rounded to 0 it would leave eps
-// alone under an m that is not 0.
+// rounded as the formula reads: the same step gives the same codes everywhere.  A v
+// over 0 keeps at least k = 1: rounded to 0 it would leave eps alone under an m that
+// is not 0.
 //
 // Bound by memory: 16 bytes an element with binary16 gradients and copies, against
 // 28 with binary32 states.  300M elements with binary32 gradients and bfloat16
-// copies take 950 us (5.7 TB/s of 18 bytes), with binary32 states 1735 us.  A wave
+// copies take 895 us (6.0 TB/s of 18 bytes), with binary32 states 1735 us.  A wave
 // takes two blocks, so that one row of exchanges finds both largest values and
 // enough waves fit to hide memory (four blocks, a block's maxima one after the
 // other: 1530 us); elements that binary64 has to decide are done one at a time

@@ -20,9 +20,11 @@
 //  - with bfloat16 operands, where it is faster (widens), as binary16, against x
 //    and w as binary16 too: their 8 bits fit it exactly down to 2^-31 of a column's
 //    largest value, which a power of two takes to the top of its range, and smaller
-//    ones to 2^-39 of it.  One pass then holds dz to 11 bits, and binary32 dw takes two for
-//    22.  Finding the largest value and converting takes 3% of 8192 x 131072 x 4096:
-//    20.8 ms, 34.4 in two parts of bfloat16.
+//    ones to 2^-39 of it.  One pass then holds dz to 11 bits, and binary32 dw takes
+//    two for 22.  8192 x 131072 x 4096 takes 21.6 ms, in two parts of bfloat16 35.4.
+//    16-bit results so come out 0.5 to 1% further from the exact ones than binary32's
+//    rounded once (0.00167 of their norm for 0.00166), and one in 30 to 50 is the neighbour
+//    of that.
 // db is summed from dz before it is rounded.
 #include <hip/hip_runtime.h>
 #include <math.h>
@@ -648,11 +650,12 @@ bool packs(uint64_t k) { return k % 8; }
 // bfloat16 operands go as binary16 where the passes that it saves, two or, with dw
 // in binary32, one, cost more than two launches and the pass over w, 6 bytes of each
 // of its elements.  In us, in parts and so, dw in 16 bits:
-//   512 x 1000 x 2048 41, 44;  700 x 1000 x 2048 56, 54;  1024 x 1000 x 2048 65, 56;
-//   256 x 65536 x 4096 776, 1027;  512 x 65536 x 4096 1267, 1257;
+//   512 x 1000 x 2048 42, 44;  700 x 1000 x 2048 57, 53;  1024 x 1000 x 2048 65, 56;
+//   256 x 65536 x 4096 787, 967;  512 x 65536 x 4096 1280, 1214;
+//   64 x 131072 x 4096 1092, 1586;
 // and in binary32:
-//   1024 x 1000 x 1024 51, 51;  1024 x 1000 x 2048 75, 68;  4096 x 1000 x 300 81, 69;
-//   512 x 65536 x 4096 1460, 1577;  1024 x 32000 x 4096 1216, 1138.
+//   1024 x 1000 x 1024 52, 51;  1024 x 1000 x 2048 75, 67;  4096 x 1000 x 300 87, 74;
+//   512 x 65536 x 4096 1455, 1570;  1024 x 32000 x 4096 1268, 1185.
 bool widens(uint64_t m, uint64_t n, uint64_t k, uint32_t passes) {
     return m * passes >= 1024 && (double)m * (double)n * (double)k >= 1.2e9;
 }
@@ -771,7 +774,9 @@ int launch_grad(GradArgs &g, const Plan &c, uint64_t m, hipStream_t s) {
 }
 
 // dx by 64 x 64 tiles beside dw by 64 x 64 or 128 x 128, whole sums: the parts'
-// memory is one product's.
+// memory is one product's.  Whole gradients in us, together and one after the other:
+// 512 x 1000 x 2048 41, 56;  128 x 1000 x 2048 38, 45;  1024 x 1000 x 768 41, 59;
+// 64 x 8000 x 512 27, 34;  300 x 520 x 2056 33, 43.
 bool go_together(const Plan &x, const Plan &w) {
     return x.tile == 2 && w.tile >= 1 && w.splits == 1;
 }
@@ -990,10 +995,6 @@ int clear(const ddl_ce_grad_args *a, hipStream_t s) {
     if (a->db && !rc)
         rc = launch(clear_kernel<V>, dim3(1), dim3(256), 0, s, (V *)a->db, 1, n, n);
     return rc;
-}
-
-bool row_ok(const void *p, size_t ld, size_t cols, size_t rows) {
-    return !p || (ld <= kMaxExtent && (ld >= cols || rows <= 1));
 }
 
 }  // namespace

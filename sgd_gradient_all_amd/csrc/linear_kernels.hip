@@ -496,10 +496,6 @@ int product(const Operand &a, const Operand &b, const Epilogue &e, uint64_t k, v
                   g.partial, g.splits);
 }
 
-bool row_ok(const void *p, size_t ld, size_t cols, size_t rows) {
-    return !p || (ld <= kMaxExtent && (ld >= cols || rows <= 1));
-}
-
 int check_workspace(int op, size_t m, size_t n, size_t k, const void *ws, size_t bytes) {
     const size_t need = workspace_bytes(op, m, n, k);
     if (!need)

@@ -119,6 +119,11 @@ inline bool aligned16(const void *p, size_t ld, size_t esz) {
 // Even addresses: a 16-bit element does not straddle its own size.
 inline bool element_ok(const void *p, size_t esz) { return (uintptr_t)p % esz == 0; }
 
+// A matrix's distance from row to row.
+inline bool row_ok(const void *p, size_t ld, size_t cols, size_t rows) {
+    return !p || (ld <= kMaxExtent && (ld >= cols || rows <= 1));
+}
+
 inline Operand operand(const void *p, size_t ld, size_t rows, size_t k) {
     Operand o;
     o.plane[0] = o.plane[1] = (const uint16_t *)p;
