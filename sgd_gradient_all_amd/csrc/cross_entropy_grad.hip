@@ -674,7 +674,7 @@ struct Buffers {
     uint16_t *dz[2], *half[2];
     uint16_t *w;         // packed
     uint16_t *x16, *w16; // bfloat16 as binary16
-    uint32_t *tops[3];   // of x, and of the even and the odd pieces of w
+    uint32_t *tops;      // [3][ld]: of x, and of the even and the odd pieces of w
     float *sum;          // dx's over the pieces: [m][ld]
     float *db;
     float *partial;
@@ -706,11 +706,9 @@ Buffers carve_grad(Carve &c, size_t m, size_t n, size_t k) {
         plane = c.take<uint16_t>(always ? 0 : up64(m) * piece);
     b.x16 = c.take<uint16_t>(up64(m) * b.rows.ld);
     b.w16 = c.take<uint16_t>(wide ? up64(piece) * b.rows.ld : 0);
-    uint32_t *tops = c.take<uint32_t>(3 * b.rows.ld);
-    for (size_t i = 0; i < 3; ++i)
-        b.tops[i] = tops + i * b.rows.ld;
-    b.rows.clear = tops;
+    b.rows.clear = c.take<uint32_t>(3 * b.rows.ld);
     b.rows.clear_count = 3 * b.rows.ld;
+    b.tops = b.rows.clear;
     b.sum = c.take<float>(piece < n ? m * b.rows.ld : 0);
     b.db = c.take<float>((m + 63) / 64 * piece);
     b.partial = c.take<float>(partial_floats(m, n, k, piece));
@@ -850,12 +848,13 @@ int gradient(const ddl_ce_grad_args *c, void *ws, hipStream_t s) {
             ++count;
         };
         const size_t odd = first / piece % 2;
+        uint32_t *now = b.tops + (1 + odd) * ld16, *next = b.tops + (2 - odd) * ld16;
         if ((wide || twice) && c->dw && k && first == 0)
-            widen(b.rows.x, ld16, m, b.rows.head, nullptr, b.tops[0], nullptr, b.x16);
+            widen(b.rows.x, ld16, m, b.rows.head, nullptr, b.tops, nullptr, b.x16);
         if (wide && c->dx && k)
             widen(w, ldw, have, nullptr,
                   l.bias && l.smoothing == 0.0 ? (const uint16_t *)l.bias + first : nullptr,
-                  b.tops[1 + odd], b.tops[2 - odd], b.w16);
+                  now, next, b.w16);
         if (count && !rc) {
             const dim3 groups(std::max(v.of[0].seek, v.of[1].seek), (uint32_t)((k + kTopColumns - 1) / kTopColumns), count);
             rc = launch(largest_kernel, groups, dim3(256), 0, s, v);
@@ -910,7 +909,7 @@ int gradient(const ddl_ce_grad_args *c, void *ws, hipStream_t s) {
             // a packed w's columns past k are zeros
             x.b = operand(w, ldw, pack ? ldw : k, have);
             if (wide) {  // so are its rows past the piece, and dz's columns
-                x.tops = b.tops[1 + odd];
+                x.tops = now;
                 x.a.k = up64(have);
                 x.b = operand(b.w16, ld16, ld16, up64(have));
             }
@@ -931,7 +930,7 @@ int gradient(const ddl_ce_grad_args *c, void *ws, hipStream_t s) {
             g.db = db;
             g.a = operand(twice ? b.half[0] : b.dz[0], d.ld, d.ld, 0);
             g.a.plane[1] = twice ? b.half[1] : b.dz[1];
-            g.tops = wide || twice ? b.tops[0] : nullptr;
+            g.tops = wide || twice ? b.tops : nullptr;
             g.b = operand(wide || twice ? b.x16 : b.rows.x, ld16, ld16, 0);
             g.partial = b.partial;
             g.part_ld = b.rows.ld;
