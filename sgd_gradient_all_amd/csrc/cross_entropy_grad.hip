@@ -856,7 +856,8 @@ int gradient(const ddl_ce_grad_args *c, void *ws, hipStream_t s) {
                   l.bias && l.smoothing == 0.0 ? (const uint16_t *)l.bias + first : nullptr,
                   now, next, b.w16);
         if (count && !rc) {
-            const dim3 groups(std::max(v.of[0].seek, v.of[1].seek), (uint32_t)((k + kTopColumns - 1) / kTopColumns), count);
+            const dim3 groups(std::max(v.of[0].seek, v.of[1].seek),
+                              (uint32_t)((k + kTopColumns - 1) / kTopColumns), count);
             rc = launch(largest_kernel, groups, dim3(256), 0, s, v);
             rc = rc ? rc
                     : launch(convert_kernel, dim3(v.of[0].groups + v.of[1].groups), dim3(256), 0, s,
